@@ -87,6 +87,7 @@ extern "C" {
 #define MM3IDX_DEV_SEQ_TOO_SHORT 4  /* seq_lens[i] < query_len              */
 #define MM3IDX_DEV_TIMEOUT       8  /* an on-chip pipeline wait gave up; outputs of that launch are invalid */
 #define MM3IDX_DEV_BAD_ROWS     16  /* ragged calls: cu_seqlens_q does not run from 0 to total_q without decreasing */
+#define MM3IDX_DEV_BAD_TOKEN    32  /* mm3idx_verify_drafts: a drafted token outside [0, vocab) (rejected) */
 
 #define MM3IDX_MAX_TOPK            32  /* largest topk served                  */
 #define MM3IDX_MAX_DECODE_ROWS     32  /* heads * query_len limit of the fused decode kernel */
@@ -382,6 +383,210 @@ int mm3idx_forward_workspace_bytes(int32_t heads, int32_t num_decodes, int32_t d
                                    int32_t num_prefills, int32_t prefill_max_query_len,
                                    int32_t max_seq_len, int32_t topk, int32_t nvfp4,
                                    size_t *bytes);
+
+/* ------------------------------------------------------------------------
+ * The operators that use the selection in one decode step: attention over
+ * the paged key-value cache, eviction of blocks from it by the attention
+ * weight they took, and verification of drafted tokens.  The pages stop at
+ * the page table of the selected blocks; these three are this library's own.
+ * ------------------------------------------------------------------------ */
+
+/* element types */
+#define MM3IDX_TYPE_BF16  0
+#define MM3IDX_TYPE_FP16  1
+#define MM3IDX_TYPE_FP32  2   /* probabilities only */
+#define MM3IDX_TYPE_E4M3  3   /* keys and values only */
+
+#define MM3IDX_ERR_ATTENTION_SHAPE  (-13) /* heads, head_dim, page size or element types not served */
+#define MM3IDX_ERR_ATTENTION_LAYOUT (-14) /* q, k, v, out, lse or weights misaligned, or their strides too small */
+#define MM3IDX_ERR_BUDGET           (-15) /* budget < init + local, local < 1, init < 0 or a decay outside [0, 1] */
+#define MM3IDX_ERR_VOCAB            (-16) /* vocab < 1, draft count outside 0..MM3IDX_MAX_DRAFTS or overlapping rows */
+
+#define MM3IDX_MAX_DRAFTS 31           /* most drafted tokens a request has     */
+#define MM3IDX_MAX_WEIGHT_ENTRIES 1024 /* query_len * topk limit of mm3idx_weights_t */
+
+/* One attention problem.  Host struct; the pointers in it are device
+ * pointers.  Strides count elements. */
+typedef struct mm3idx_attention {
+    const void    *q;              /* [num_reqs * query_len, q_heads, head_dim], d stride 1, 16-byte aligned */
+    int64_t        q_token_stride; /* multiples of 8                                        */
+    int64_t        q_head_stride;
+    int32_t        q_heads;        /* a multiple of kv_heads                                */
+    int32_t        kv_heads;       /* query head h reads key-value head h / (q_heads / kv_heads) */
+    int32_t        head_dim;       /* 64 or 128                                             */
+    int32_t        q_type;         /* MM3IDX_TYPE_BF16 or _FP16; out has the same type      */
+    int32_t        kv_type;        /* q_type, or MM3IDX_TYPE_E4M3                           */
+    const void    *k_cache;        /* [num_pages, page_size, kv_heads, head_dim], d stride 1, 16-byte aligned;
+                                      page, token and head strides positive multiples of 16 bytes, in any order */
+    int64_t        k_page_stride, k_token_stride, k_head_stride;
+    const void    *v_cache;        /* as k_cache                                            */
+    int64_t        v_page_stride, v_token_stride, v_head_stride;
+    float          k_scale;        /* multiplies every key element (finite, > 0)            */
+    float          v_scale;        /* multiplies every value element (finite)               */
+    int32_t        num_pages;      /* pages that both caches have, >= 1                     */
+    int32_t        page_size;      /* tokens a page: 16, 32, 64 or 128                      */
+    const int32_t *page_table;     /* int32 [num_reqs, table_stride]; token t of request i is in page
+                                      page_table[i, t / page_size]                          */
+    int64_t        table_stride;   /* >= table_width                                        */
+    int32_t        table_width;    /* readable columns, >= cdiv(max_seq_len, page_size)     */
+    const int32_t *seq_lens;       /* int32 [num_reqs]; 0: an empty slot of the batch       */
+    int32_t        num_reqs;       /* >= 0                                                  */
+    int32_t        query_len;      /* query tokens a request, >= 1                          */
+    int32_t        max_seq_len;    /* bound on seq_lens fixed across graph replays          */
+    float          sm_scale;       /* finite, > 0                                           */
+    void          *out;            /* [num_reqs * query_len, q_heads, head_dim] of q_type, d stride 1, 16-byte aligned */
+    int64_t        out_token_stride, out_head_stride; /* multiples of 8 that do not overlap */
+    float         *lse;            /* fp32 [num_reqs * query_len, q_heads], or NULL         */
+    int64_t        lse_token_stride; /* >= q_heads                                          */
+    float         *block_weights;  /* fp32 [num_reqs * query_len, cdiv(max_seq_len, 128)], or NULL */
+    int64_t        block_weights_stride; /* >= cdiv(max_seq_len, 128)                       */
+} mm3idx_attention_t;
+
+/*
+ * mm3idx_paged_attention -- attention of a few new tokens a request over its
+ * paged keys and values.  Query j of request i sits at position
+ * pos = seq_lens[i] - query_len + j, as in the scoring calls, and sees tokens
+ * 0..pos:
+ *     s[t]   = sm_scale * k_scale * sum_d q[d] * k[t, d]
+ *     p[t]   = exp(s[t] - lse),  lse = log sum over the visible t of exp(s[t])
+ *     out[d] = v_scale * sum over the visible t of p[t] * v[t, d]
+ *     block_weights[row, b] = sum over the query heads and the visible tokens
+ *                             t in [128 b, 128 b + 128) of p[t]
+ * Masked tokens do not count whatever their keys and values hold, NaN and
+ * infinity among it.  A row that sees nothing (an empty slot, pos < 0, pages
+ * outside the cache) gets zeros and lse = -inf, as does one whose scores are
+ * all -inf.  block_weights is written for all cdiv(max_seq_len, 128) columns,
+ * 0 past the row's last block.
+ *
+ * Attention over selected blocks is the same call on the page table of
+ * mm3idx_decode_sparse_table: page_table = sparse_block_table_out, seq_lens =
+ * sparse_context_lens_out, query_len = 1, num_reqs = its rows, max_seq_len =
+ * 128 * topk, page_size = 128 / pages_per_block; with block_page_stride 2P the
+ * values start P pages behind the keys in the same pool.  block_weights[row,
+ * k] then belongs to the row's k-th id.
+ *
+ * workspace: >= mm3idx_attention_workspace_bytes(...) bytes, 256-byte
+ * aligned, zero-filled before its first use and kept by the caller for the
+ * next call, under the rules of mm3idx_decode.  One workspace serves every
+ * batch that its bounds cover.  Device status: MM3IDX_DEV_BAD_PAGE,
+ * _SEQ_TOO_LONG, _SEQ_TOO_SHORT (0 < seq_len < query_len), _TIMEOUT.
+ */
+int mm3idx_paged_attention(const mm3idx_attention_t *a, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * mm3idx_attention_workspace_bytes -- workspace of mm3idx_paged_attention: a
+ * ticket per (request, kv head), the partial results of those that are split
+ * across CTAs, and with block_weights != 0 one fp32 per (row, query head,
+ * block).  Reads the current device's SM count; no allocation.
+ */
+int mm3idx_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                     int32_t num_reqs, int32_t query_len, int32_t max_seq_len,
+                                     int32_t block_weights, size_t *bytes);
+
+/* The weight that the blocks of every request have taken so far, and one
+ * step's share.  Host struct of device pointers; strides count elements. */
+typedef struct mm3idx_weights {
+    float         *acc;            /* fp32 [num_reqs, acc_stride]                           */
+    int64_t        acc_stride;     /* >= cdiv(max_seq_len, 128)                             */
+    const float   *block_weights;  /* fp32 [num_reqs * query_len, weights_stride], or NULL: nothing is added */
+    int64_t        weights_stride; /* >= cdiv(max_seq_len, 128), with ids >= topk           */
+    const int32_t *ids;            /* NULL: column b of block_weights is block b; else int32
+                                      [num_reqs * query_len, ids_stride]: column k is block ids[row, k], -1: none */
+    int64_t        ids_stride;     /* >= topk                                               */
+    int32_t        topk;           /* columns of ids; query_len * topk <= MM3IDX_MAX_WEIGHT_ENTRIES */
+    const int32_t *seq_lens;       /* int32 [num_reqs]                                      */
+    int32_t        num_reqs;
+    int32_t        query_len;      /* rows of block_weights a request                       */
+    int32_t        max_seq_len;
+    double         decay;          /* 0..1                                                  */
+} mm3idx_weights_t;
+
+/*
+ * mm3idx_accumulate_weights -- acc[i, b] = decay * acc[i, b] + the sum of
+ * request i's weights of block b, in place, for its blocks
+ * b < cdiv(seq_lens[i], 128); the other columns are left as they are.  Summed in 64 bits and rounded
+ * once, so the result does not depend on an order; an id given twice counts
+ * twice, one outside the request's blocks is ignored.
+ */
+int mm3idx_accumulate_weights(const mm3idx_weights_t *w, void *stream);
+
+/* One table that eviction compacts: a column per 128-token block. */
+typedef struct mm3idx_evict_table {
+    const int32_t *in;             /* int32 [num_reqs, in_stride]; NULL: no such table      */
+    int64_t        in_stride;      /* >= cdiv(max_seq_len, 128)                             */
+    int32_t       *out;            /* int32 [num_reqs, out_stride]; may be `in` itself with its stride */
+    int64_t        out_stride;     /* >= budget                                             */
+    int32_t       *freed;          /* int32 [num_reqs, freed_stride], or NULL               */
+    int64_t        freed_stride;   /* >= max(1, cdiv(max_seq_len, 128) - budget)            */
+} mm3idx_evict_table_t;
+
+typedef struct mm3idx_eviction {
+    int32_t        budget;         /* most blocks a request keeps                           */
+    int32_t        init_blocks;    /* first blocks always kept, >= 0                        */
+    int32_t        local_blocks;   /* last blocks always kept, >= 1; init + local <= budget */
+    mm3idx_evict_table_t tables[2];/* e.g. the index-K cache's table and the attention's    */
+    int32_t       *ids;            /* int32 [num_reqs, ids_stride], or NULL: the kept blocks' ids */
+    int64_t        ids_stride;     /* >= budget                                             */
+    float         *acc_out;        /* fp32 [num_reqs, acc_out_stride]; may be w->acc itself */
+    int64_t        acc_out_stride; /* >= cdiv(max_seq_len, 128)                             */
+    int32_t       *seq_lens_out;   /* int32 [num_reqs]; may be w->seq_lens itself           */
+} mm3idx_eviction_t;
+
+/*
+ * mm3idx_evict_blocks -- the sum of mm3idx_accumulate_weights (w->acc itself
+ * is only read), then eviction by it: of a request's n = cdiv(seq_len, 128) blocks the
+ * first init_blocks, the last local_blocks and the heaviest of the others by
+ * (acc desc, id asc; NaN counts as heaviest) stay until `budget` are kept; all
+ * of them when n <= budget.  The kept blocks keep their order and become blocks
+ * 0..kept-1:
+ *   ids     the kept blocks' former ids, ascending, -1 up to budget;
+ *   out     their table entries, -1 up to budget (columns from budget on are
+ *           left as they are);
+ *   freed   the entries of the evicted blocks in id order, -1 up to
+ *           max(1, cdiv(max_seq_len, 128) - budget);
+ *   acc_out their weights, 0 up to cdiv(max_seq_len, 128);
+ *   seq_lens_out  seq_len - 128 * evicted (an evicted block is always full).
+ * Outputs must not overlap inputs in another way than the ones
+ * named.  Lengths are clamped to 0..max_seq_len (MM3IDX_DEV_SEQ_TOO_LONG).
+ */
+int mm3idx_evict_blocks(const mm3idx_weights_t *w, const mm3idx_eviction_t *e, void *stream);
+
+/* Drafted tokens of a batch.  Host struct of device pointers; strides count
+ * elements; the vocabulary has stride 1. */
+typedef struct mm3idx_drafts {
+    const void    *target;         /* [num_reqs, drafts + 1, vocab] probabilities of the target */
+    int64_t        target_req_stride, target_row_stride;
+    const void    *draft;          /* [num_reqs, drafts, vocab] the drafter's; NULL: each drafted token had probability 1 */
+    int64_t        draft_req_stride, draft_row_stride;
+    int32_t        type;           /* MM3IDX_TYPE_FP32, _BF16 or _FP16                      */
+    const int32_t *tokens;         /* int32 [num_reqs, tokens_stride]                       */
+    int64_t        tokens_stride;  /* >= drafts                                             */
+    const int32_t *draft_lens;     /* int32 [num_reqs], or NULL: `drafts` each (clamped to 0..drafts) */
+    const float   *uniforms;       /* fp32 [num_reqs, uniforms_stride] in [0, 1): column j decides draft j,
+                                      column `drafts` draws the last token                  */
+    int64_t        uniforms_stride;/* >= drafts + 1                                         */
+    int32_t        num_reqs;
+    int32_t        drafts;         /* 0..MM3IDX_MAX_DRAFTS                                  */
+    int32_t        vocab;          /* >= 1                                                  */
+    int32_t       *out;            /* int32 [num_reqs, out_stride]: the accepted drafts, the drawn token, -1 */
+    int64_t        out_stride;     /* >= drafts + 1                                         */
+    int32_t       *accepted;       /* int32 [num_reqs]                                      */
+} mm3idx_drafts_t;
+
+/*
+ * mm3idx_verify_drafts -- speculative sampling.  With p_j = target[i, j] and
+ * q_j = draft[i, j], draft j of request i (token d) is accepted while
+ * u_j * q_j(d) < p_j(d) (exact products).  At the first one that is not, the
+ * token is drawn from max(p_j - q_j, 0), or from p_j where that is zero
+ * throughout; when all draft_lens[i] are accepted, from p at that row.  The
+ * draw is the smallest token whose cumulative weight exceeds u * total.
+ * Weights are summed as 64-bit integers in units of 2^-52 (probabilities are
+ * clamped to 0..1 and NaN counts as 0, so every fp32 value from 2^-29 on is
+ * exact), which makes the token independent of the order of the sum.  A row
+ * without any weight gives token vocab - 1.  A row must sum to less than 2048.
+ */
+int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
 
 /*
  * mm3idx_get_device_error -- synchronises `stream`, then reads and clears the

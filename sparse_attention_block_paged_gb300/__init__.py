@@ -17,12 +17,22 @@ Entry points (names after the vLLM MiniMax-M3 ``index_topk`` page):
 * :func:`decode_nvfp4` -- the same over NVFP4 index-K pages
 * :func:`prefill`      -- tensor-core scores + selector for long query runs
 * :func:`forward`      -- a batch of decode requests followed by prefill requests
+
+and the operators that use the selection in a decode step:
+
+* :func:`paged_attention`    -- new tokens over a paged key-value cache, all of it
+  or the selected blocks
+* :func:`accumulate_weights` -- the attention weight that the blocks have taken
+* :func:`evict_blocks`       -- the lightest blocks out of the cache
+* :func:`verify_drafts`      -- drafted tokens against the target's probabilities
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -38,6 +48,10 @@ MAX_TOPK = 32
 MAX_DECODE_ROWS = 32
 STATIC_SCRATCH_BYTES = 8 << 20
 DEV_BAD_PAGE, DEV_SEQ_TOO_LONG, DEV_SEQ_TOO_SHORT, DEV_TIMEOUT, DEV_BAD_ROWS = 1, 2, 4, 8, 16
+DEV_BAD_TOKEN = 32
+MAX_DRAFTS = 31
+MAX_WEIGHT_ENTRIES = 1024
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 
 
 class Mm3idxError(RuntimeError):
@@ -78,6 +92,116 @@ class SparseTable(ctypes.Structure):
         ("sparse_block_table_out", ctypes.c_void_p),
         ("sparse_table_stride", ctypes.c_int64),
         ("sparse_context_lens_out", ctypes.c_void_p),
+    ]
+
+
+class Attention(ctypes.Structure):
+    """mm3idx_attention_t."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("q_type", ctypes.c_int32),
+        ("kv_type", ctypes.c_int32),
+        ("k_cache", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_cache", ctypes.c_void_p),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("num_reqs", ctypes.c_int32),
+        ("query_len", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+        ("lse_token_stride", ctypes.c_int64),
+        ("block_weights", ctypes.c_void_p),
+        ("block_weights_stride", ctypes.c_int64),
+    ]
+
+
+class Weights(ctypes.Structure):
+    """mm3idx_weights_t."""
+    _fields_ = [
+        ("acc", ctypes.c_void_p),
+        ("acc_stride", ctypes.c_int64),
+        ("block_weights", ctypes.c_void_p),
+        ("weights_stride", ctypes.c_int64),
+        ("ids", ctypes.c_void_p),
+        ("ids_stride", ctypes.c_int64),
+        ("topk", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("num_reqs", ctypes.c_int32),
+        ("query_len", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("decay", ctypes.c_double),
+    ]
+
+
+class EvictTable(ctypes.Structure):
+    """mm3idx_evict_table_t."""
+    _fields_ = [
+        ("in_", ctypes.c_void_p),
+        ("in_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("freed", ctypes.c_void_p),
+        ("freed_stride", ctypes.c_int64),
+    ]
+
+
+class EvictionArgs(ctypes.Structure):
+    """mm3idx_eviction_t."""
+    _fields_ = [
+        ("budget", ctypes.c_int32),
+        ("init_blocks", ctypes.c_int32),
+        ("local_blocks", ctypes.c_int32),
+        ("tables", EvictTable * 2),
+        ("ids", ctypes.c_void_p),
+        ("ids_stride", ctypes.c_int64),
+        ("acc_out", ctypes.c_void_p),
+        ("acc_out_stride", ctypes.c_int64),
+        ("seq_lens_out", ctypes.c_void_p),
+    ]
+
+
+class Drafts(ctypes.Structure):
+    """mm3idx_drafts_t."""
+    _fields_ = [
+        ("target", ctypes.c_void_p),
+        ("target_req_stride", ctypes.c_int64),
+        ("target_row_stride", ctypes.c_int64),
+        ("draft", ctypes.c_void_p),
+        ("draft_req_stride", ctypes.c_int64),
+        ("draft_row_stride", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+        ("tokens", ctypes.c_void_p),
+        ("tokens_stride", ctypes.c_int64),
+        ("draft_lens", ctypes.c_void_p),
+        ("uniforms", ctypes.c_void_p),
+        ("uniforms_stride", ctypes.c_int64),
+        ("num_reqs", ctypes.c_int32),
+        ("drafts", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("accepted", ctypes.c_void_p),
     ]
 
 
@@ -139,6 +263,14 @@ SYMBOLS = {
     "mm3idx_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
+    "mm3idx_paged_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.c_void_p,
+                                              ctypes.c_size_t, ctypes.c_void_p]),
+    "mm3idx_attention_workspace_bytes": (ctypes.c_int, [ctypes.c_int32] * 7 +
+                                         [ctypes.POINTER(ctypes.c_size_t)]),
+    "mm3idx_accumulate_weights": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.c_void_p]),
+    "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.POINTER(EvictionArgs),
+                                           ctypes.c_void_p]),
+    "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Drafts), ctypes.c_void_p]),
 }
 
 
@@ -178,9 +310,14 @@ def _stream(device, stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """Make the inputs' GPU current for a library call: the library takes the
     SM count, its status word and its static scratch from the current device."""
+    if torch.device(device).index == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(device)
 
 
@@ -586,6 +723,325 @@ def decode_static(idx_q, index_cache, block_table, seq_lens, *, query_len, max_s
                                         out.data_ptr(), out.stride(0), out.stride(1),
                                         _stream(idx_q.device, stream)), "mm3idx_decode_static")
     return out[:, :rows, :]
+
+
+# ------------------------------------------------ using the selection
+
+def _allocating_on(stream):
+    """Tensors that a call makes belong to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-D tensor (free when it has one row)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, num_reqs: int,
+                              query_len: int, max_seq_len: int,
+                              block_weights: bool = False) -> int:
+    size, n = lib.mm3idx_attention_workspace_bytes, ctypes.c_size_t(0)
+    _check(size(q_heads, kv_heads, head_dim, num_reqs, query_len, max_seq_len,
+                1 if block_weights else 0, ctypes.byref(n)), "mm3idx_attention_workspace_bytes")
+    return n.value
+
+
+def new_attention_workspace(q_heads, kv_heads, head_dim, num_reqs, query_len, max_seq_len,
+                            block_weights=False, device=None):
+    """A zero-filled workspace for :func:`paged_attention`, reusable across
+    calls of one stream whose batches stay within these bounds."""
+    device = torch.device(device or "cuda")
+    with _on(device):
+        n = attention_workspace_bytes(q_heads, kv_heads, head_dim, num_reqs, query_len,
+                                      max_seq_len, block_weights)
+        return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max_seq_len,
+                    sm_scale, k_scale=1.0, v_scale=1.0, out=None, lse=None, block_weights=None,
+                    workspace=None, stream=None):
+    """Attention of ``query_len`` new tokens a request over its paged keys and
+    values, causal: q [num_reqs * query_len, q_heads, head_dim] bf16 or fp16,
+    caches [pages, page_size, kv_heads, head_dim] of the same type or
+    float8_e4m3fn (times ``k_scale`` / ``v_scale``) with any 16-byte strides,
+    int32 page table [num_reqs, >= cdiv(max_seq_len, page_size)] and lengths
+    (0: an empty slot, its rows become 0).  Returns ``out``, like q.
+
+    ``lse`` fp32 [rows, q_heads] and ``block_weights`` fp32 [rows,
+    cdiv(max_seq_len, 128)] are written when given: the log-sum-exp of each
+    row's scores, and the softmax weight that each 128-token block took,
+    summed over the heads.
+
+    Over selected blocks: ``page_table``, ``seq_lens`` = the sparse table and
+    context lengths of :func:`decode_sparse_table`, ``query_len=1`` and
+    ``max_seq_len = 128 * topk``."""
+    _need(q.ndim == 3 and q.dtype in (torch.bfloat16, torch.float16) and q.stride(2) == 1,
+          "queries must be bf16 or fp16 [tokens, heads, head_dim] with contiguous head_dim")
+    _need(k_cache.ndim == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
+          and k_cache.stride(3) == 1 and v_cache.stride(3) == 1
+          and k_cache.shape[3] == q.shape[2]
+          and k_cache.dtype in (q.dtype, torch.float8_e4m3fn),
+          "caches must be [pages, page_size, kv_heads, head_dim] with contiguous head_dim, "
+          "of the queries' type or float8_e4m3fn")
+    _need(page_table.ndim == 2 and page_table.dtype == torch.int32
+          and (page_table.stride(1) == 1 or page_table.shape[1] <= 1)
+          and seq_lens.ndim == 1 and seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(),
+          "page table and lengths must be int32 with unit stride")
+    dev = q.device
+    _on_gpu(q, k_cache, v_cache, page_table, seq_lens)
+    rows, heads, dim = q.shape
+    pages, size, kv_heads, _ = k_cache.shape
+    reqs = seq_lens.shape[0]
+    _need(rows == reqs * query_len and page_table.shape[0] == reqs,
+          "queries must have batch * query_len rows and the page table one row per request")
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+    _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev
+          and out.stride(2) == 1, "out must be like the queries")
+    a = Attention()
+    a.q, a.out = q.data_ptr(), out.data_ptr()
+    a.q_token_stride = q.stride(0) if rows > 1 else heads * dim
+    a.q_head_stride = q.stride(1) if heads > 1 else dim
+    a.out_token_stride = out.stride(0) if rows > 1 else heads * dim
+    a.out_head_stride = out.stride(1) if heads > 1 else dim
+    a.q_heads, a.kv_heads, a.head_dim = heads, kv_heads, dim
+    a.q_type, a.kv_type = TYPES[q.dtype], TYPES[k_cache.dtype]
+    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    sp, st, sh, _ = k_cache.stride()
+    a.k_page_stride = sp if pages > 1 else size * kv_heads * dim
+    a.k_token_stride, a.k_head_stride = st, sh if kv_heads > 1 else dim
+    sp, st, sh, _ = v_cache.stride()
+    a.v_page_stride = sp if pages > 1 else size * kv_heads * dim
+    a.v_token_stride, a.v_head_stride = st, sh if kv_heads > 1 else dim
+    a.k_scale, a.v_scale, a.sm_scale = k_scale, v_scale, sm_scale
+    a.num_pages, a.page_size = pages, size
+    a.page_table, a.table_stride = page_table.data_ptr(), _row_stride(page_table)
+    a.table_width = page_table.shape[1]
+    a.seq_lens, a.num_reqs = seq_lens.data_ptr(), reqs
+    a.query_len, a.max_seq_len = query_len, max_seq_len
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.ndim == 2 and lse.shape[0] >= rows
+              and lse.shape[1] == heads and (lse.stride(1) == 1 or heads == 1)
+              and lse.device == dev,
+              "lse must be fp32 [>= rows, heads] with unit inner stride")
+        a.lse, a.lse_token_stride = lse.data_ptr(), _row_stride(lse)
+    if block_weights is not None:
+        width = _cdiv(max_seq_len, 128)
+        _need(block_weights.dtype == torch.float32 and block_weights.ndim == 2
+              and block_weights.shape[0] >= rows and block_weights.shape[1] >= width
+              and (block_weights.stride(1) == 1 or block_weights.shape[1] == 1)
+              and block_weights.device == dev,
+              "block_weights must be fp32 [>= rows, >= cdiv(max_seq_len, 128)] with unit inner "
+              "stride")
+        a.block_weights, a.block_weights_stride = (block_weights.data_ptr(),
+                                                   _row_stride(block_weights))
+    if workspace is None:
+        with _allocating_on(stream):
+            workspace = new_attention_workspace(heads, kv_heads, dim, reqs, query_len, max_seq_len,
+                                                block_weights is not None, dev)
+    wp, wn = _ws(workspace, dev)
+    with _on(dev):
+        _check(lib.mm3idx_paged_attention(ctypes.byref(a), wp, wn, _stream(dev, stream)),
+               "mm3idx_paged_attention")
+    return out
+
+
+def _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay):
+    width = _cdiv(max_seq_len, 128)
+    reqs = seq_lens.shape[0]
+    _need(seq_lens.ndim == 1 and seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(),
+          "lengths must be contiguous int32")
+    _need(acc.dtype == torch.float32 and acc.ndim == 2 and acc.shape[0] == reqs
+          and acc.shape[1] >= width and (acc.stride(1) == 1 or acc.shape[1] == 1),
+          "weights must be fp32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit inner stride")
+    _on_gpu(acc, seq_lens)
+    w = Weights()
+    w.acc, w.acc_stride = acc.data_ptr(), _row_stride(acc)
+    w.seq_lens, w.num_reqs = seq_lens.data_ptr(), reqs
+    w.query_len, w.max_seq_len, w.decay = query_len, max_seq_len, decay
+    if block_weights is not None:
+        _need(block_weights.dtype == torch.float32 and block_weights.ndim == 2
+              and block_weights.shape[0] >= reqs * query_len
+              and (block_weights.stride(1) == 1 or block_weights.shape[1] == 1)
+              and block_weights.device == acc.device,
+              "block_weights must be fp32 [>= num_reqs * query_len, columns] with unit inner "
+              "stride")
+        w.block_weights, w.weights_stride = block_weights.data_ptr(), _row_stride(block_weights)
+        _need(block_weights.shape[1] >= (width if ids is None else ids.shape[-1]),
+              "block_weights must have a column per block, or per id")
+    _need(ids is None or block_weights is not None, "ids need block_weights")
+    if ids is not None:
+        if ids.ndim == 3:                       # the ids of one index head, as decode returns them
+            _need(ids.shape[0] == 1, "ids must be those of one index head")
+            ids = ids[0]
+        _need(ids.dtype == torch.int32 and ids.ndim == 2 and ids.shape[0] >= reqs * query_len
+              and (ids.stride(1) == 1 or ids.shape[1] == 1) and ids.device == acc.device,
+              "ids must be int32 [>= num_reqs * query_len, topk] with unit inner stride")
+        w.ids, w.ids_stride, w.topk = ids.data_ptr(), _row_stride(ids), ids.shape[1]
+    return w
+
+
+def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, ids=None,
+                       decay=1.0, stream=None):
+    """``acc`` [num_reqs, >= cdiv(max_seq_len, 128)] = decay * acc + this step's
+    ``block_weights`` (of :func:`paged_attention`) summed over the request's
+    ``query_len`` rows, in place: column b is block b, or with ``ids`` (int32
+    [rows, topk] or [1, rows, topk], -1: none) column k is block ids[row, k]."""
+    w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
+    with _on(acc.device):
+        _check(lib.mm3idx_accumulate_weights(ctypes.byref(w), _stream(acc.device, stream)),
+               "mm3idx_accumulate_weights")
+    return acc
+
+
+class Eviction(NamedTuple):
+    """What :func:`evict_blocks` leaves: the kept blocks' former ids
+    [num_reqs, budget] (-1 behind them), the shortened lengths, the kept
+    blocks' weights (0 behind them), each table compacted and the entries of
+    the evicted blocks (-1 behind them)."""
+    ids: torch.Tensor
+    seq_lens: torch.Tensor
+    weights: torch.Tensor
+    block_table: torch.Tensor
+    freed: torch.Tensor
+    attention_block_table: Optional[torch.Tensor] = None
+    attention_freed: Optional[torch.Tensor] = None
+
+
+def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_blocks, max_seq_len,
+                 block_weights=None, ids=None, query_len=1, decay=1.0,
+                 attention_block_table=None, in_place=False, out=None, stream=None):
+    """Brings the accumulated weights up to date as :func:`accumulate_weights`
+    does, then keeps at most ``budget`` 128-token blocks of each request: the
+    first ``init_blocks``, the last ``local_blocks`` (at least 1) and the
+    heaviest others (equal weights: the lower id).  Returns an
+    :class:`Eviction` of the compacted tables, weights and lengths; the
+    inputs are left as they are, or with ``in_place`` overwritten by them
+    (their columns from ``budget`` on stay as they were).  ``out``: an
+    Eviction of the same shapes to write into."""
+    w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
+    dev, reqs, width = acc.device, seq_lens.shape[0], _cdiv(max_seq_len, 128)
+    given = (block_table, attention_block_table)
+    for t in given:
+        _need(t is None or (t.dtype == torch.int32 and t.ndim == 2 and t.shape[0] == reqs
+                            and t.shape[1] >= width and (t.stride(1) == 1 or t.shape[1] == 1)
+                            and t.device == dev),
+              "block tables must be int32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit inner "
+              "stride, on the weights' GPU")
+    _need(block_table is not None, "a block table is needed")
+    _need(budget >= 1, "budget must be at least 1")
+    gone = max(1, width - budget)
+    if out is None:
+        with _allocating_on(stream):
+            def ints(columns):
+                return torch.empty((reqs, columns), dtype=torch.int32, device=dev)
+
+            _need(not in_place or all(t is None or t.shape[1] >= budget for t in given),
+                  "in-place tables must have at least budget columns")
+            second = attention_block_table is not None
+            out = Eviction(
+                ints(budget), seq_lens if in_place else torch.empty_like(seq_lens),
+                acc if in_place else torch.empty((reqs, width), dtype=torch.float32, device=dev),
+                block_table if in_place else ints(budget), ints(gone),
+                (attention_block_table if in_place else ints(budget)) if second else None,
+                ints(gone) if second else None)
+    else:
+        _need(not in_place, "out and in_place exclude each other")
+        _need((out.attention_block_table is None) == (attention_block_table is None)
+              and out.weights.dtype == torch.float32 and out.weights.shape[1] >= width
+              and out.seq_lens.dtype == torch.int32 and out.seq_lens.shape == seq_lens.shape
+              and out.seq_lens.is_contiguous()
+              and all(t is None or (t.device == dev and t.shape[0] == reqs and
+                                    (t.ndim == 1 or t.stride(1) == 1 or t.shape[1] == 1))
+                      for t in out)
+              and all(t is None or (t.dtype == torch.int32 and t.shape[1] >= n) for t, n in (
+                  (out.ids, budget), (out.block_table, budget), (out.freed, gone),
+                  (out.attention_block_table, budget), (out.attention_freed, gone))),
+              "out must be an Eviction of these shapes")
+    e = EvictionArgs()
+    e.budget, e.init_blocks, e.local_blocks = budget, init_blocks, local_blocks
+    e.ids, e.ids_stride = out.ids.data_ptr(), _row_stride(out.ids)
+    e.acc_out, e.acc_out_stride = out.weights.data_ptr(), _row_stride(out.weights)
+    e.seq_lens_out = out.seq_lens.data_ptr()
+    tables = ((block_table, out.block_table, out.freed),
+              (attention_block_table, out.attention_block_table, out.attention_freed))
+    for k, (old, new, freed) in enumerate(tables):
+        if old is None:
+            continue
+        t = e.tables[k]
+        t.in_, t.in_stride = old.data_ptr(), _row_stride(old)
+        t.out, t.out_stride = new.data_ptr(), _row_stride(new)
+        t.freed, t.freed_stride = freed.data_ptr(), _row_stride(freed)
+    with _on(dev):
+        _check(lib.mm3idx_evict_blocks(ctypes.byref(w), ctypes.byref(e), _stream(dev, stream)),
+               "mm3idx_evict_blocks")
+    return out
+
+
+def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, draft_lens=None,
+                  out=None, accepted=None, stream=None):
+    """Speculative sampling: draft j of a request (token d) is accepted while
+    ``uniforms[:, j] * draft_probs[:, j, d] < target_probs[:, j, d]``; at the
+    first that is not, a token is drawn by ``uniforms[:, drafts]`` from
+    max(target - draft, 0), and from the target's next row when all are.
+
+    target_probs [num_reqs, drafts + 1, vocab] and draft_probs [num_reqs,
+    drafts, vocab] (None: the drafter was certain) of one type, fp32, bf16 or
+    fp16; draft_tokens int32 [num_reqs, drafts]; uniforms fp32 in [0, 1)
+    [num_reqs, drafts + 1]; draft_lens int32 [num_reqs] when requests have
+    fewer.  Returns (tokens int32 [num_reqs, drafts + 1]: the accepted drafts,
+    the drawn token, then -1; the number accepted, int32 [num_reqs])."""
+    _need(target_probs.ndim == 3 and (target_probs.stride(2) == 1 or target_probs.shape[2] == 1)
+          and target_probs.dtype in (torch.float32, torch.bfloat16, torch.float16),
+          "target_probs must be fp32, bf16 or fp16 [num_reqs, drafts + 1, vocab] with contiguous "
+          "vocab")
+    reqs, rows, vocab = target_probs.shape
+    k = rows - 1
+    _need(k >= 0, "target_probs must have drafts + 1 rows")
+    dev = target_probs.device
+    _need(draft_tokens.dtype == torch.int32 and tuple(draft_tokens.shape) == (reqs, k)
+          and (k <= 1 or draft_tokens.stride(1) == 1),
+          "draft_tokens must be int32 [num_reqs, drafts] with unit inner stride")
+    _need(uniforms.dtype == torch.float32 and tuple(uniforms.shape) == (reqs, rows)
+          and (k == 0 or uniforms.stride(1) == 1),
+          "uniforms must be fp32 [num_reqs, drafts + 1] with unit inner stride")
+    _need(draft_probs is None or (draft_probs.dtype == target_probs.dtype
+                                  and tuple(draft_probs.shape) == (reqs, k, vocab)
+                                  and (draft_probs.stride(2) == 1 or vocab == 1)),
+          "draft_probs must be [num_reqs, drafts, vocab] of target_probs' type")
+    _need(draft_lens is None or (draft_lens.dtype == torch.int32 and draft_lens.is_contiguous()
+                                 and tuple(draft_lens.shape) == (reqs,)),
+          "draft_lens must be contiguous int32 [num_reqs]")
+    _on_gpu(target_probs, draft_tokens, uniforms,
+            *(t for t in (draft_probs, draft_lens, out, accepted) if t is not None))
+    if out is None or accepted is None:
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty((reqs, rows), dtype=torch.int32, device=dev)
+            if accepted is None:
+                accepted = torch.empty((reqs,), dtype=torch.int32, device=dev)
+    _need(out.dtype == torch.int32 and tuple(out.shape) == (reqs, rows)
+          and (k == 0 or out.stride(1) == 1) and accepted.dtype == torch.int32
+          and tuple(accepted.shape) == (reqs,) and accepted.is_contiguous(),
+          "out must be int32 [num_reqs, drafts + 1] with unit inner stride, accepted int32 "
+          "[num_reqs]")
+    d = Drafts()
+    d.target, d.type = target_probs.data_ptr(), TYPES[target_probs.dtype]
+    d.target_req_stride, d.target_row_stride = target_probs.stride(0), target_probs.stride(1)
+    if draft_probs is not None:
+        d.draft = draft_probs.data_ptr()
+        d.draft_req_stride, d.draft_row_stride = draft_probs.stride(0), draft_probs.stride(1)
+    d.tokens, d.tokens_stride = draft_tokens.data_ptr(), _row_stride(draft_tokens)
+    if draft_lens is not None:
+        d.draft_lens = draft_lens.data_ptr()
+    d.uniforms, d.uniforms_stride = uniforms.data_ptr(), _row_stride(uniforms)
+    d.num_reqs, d.drafts, d.vocab = reqs, k, vocab
+    d.out, d.out_stride, d.accepted = out.data_ptr(), _row_stride(out), accepted.data_ptr()
+    with _on(dev):
+        _check(lib.mm3idx_verify_drafts(ctypes.byref(d), _stream(dev, stream)),
+               "mm3idx_verify_drafts")
+    return out, accepted
 
 
 def _stream_device(stream):

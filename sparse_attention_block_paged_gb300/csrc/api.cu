@@ -14,6 +14,7 @@
 #include "../../include/mm3idx.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "serving.h"
 
 using namespace mm3idx;
 
@@ -639,6 +640,21 @@ __global__ void wait_timeout_check_kernel(int32_t* status) {
 
 }  // namespace
 
+namespace mm3idx {
+
+int library_device(int* sms, int32_t** status) {
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc) return rc;
+  *sms = dev->sms;
+  *status = dev->status;
+  return MM3IDX_OK;
+}
+
+TensorMapEncode tensor_map_encoder() { return encode_fn(); }
+
+}  // namespace mm3idx
+
 extern "C" {
 
 int mm3idx_check_wait_timeout(int32_t warps, void* stream) {
@@ -668,6 +684,15 @@ const char* mm3idx_status_string(int status) {
     case MM3IDX_ERR_CUDA: return "CUDA runtime or driver call failed";
     case MM3IDX_ERR_STATIC_SCRATCH:
       return "problem needs more decode scratch than the library's static array (MM3IDX_STATIC_SCRATCH_BYTES)";
+    case MM3IDX_ERR_ATTENTION_SHAPE:
+      return "attention serves q_heads a multiple of kv_heads, head_dim 64 or 128, pages of 16, 32, 64 or 128 tokens, "
+             "bf16 or fp16 queries over keys and values of the same type or e4m3";
+    case MM3IDX_ERR_ATTENTION_LAYOUT:
+      return "attention tensors must be 16-byte aligned with strides that are multiples of 16 bytes, and outputs must not overlap";
+    case MM3IDX_ERR_BUDGET:
+      return "eviction needs init >= 0, local >= 1, init + local <= budget and a decay in 0..1";
+    case MM3IDX_ERR_VOCAB:
+      return "verification needs vocab >= 1, 0..31 drafts and rows that do not overlap";
     default: return "unknown status";
   }
 }

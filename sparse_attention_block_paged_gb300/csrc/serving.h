@@ -1,0 +1,111 @@
+// serving.h -- argument blocks and launcher declarations of the operators
+// that use the selection (paged attention, block eviction, draft
+// verification), shared by their C ABI (api_serving.cu) and kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace mm3idx {
+
+// Defined in api.cu: the current device's SM count and status word, and the
+// driver's tensor-map encoder (nullptr when the driver has none).
+int library_device(int* sms, int32_t** status);
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncode tensor_map_encoder();
+
+struct AttentionArgs {
+  const void* q;
+  int64_t q_tok, q_head;      // element strides
+  int32_t kv_heads;
+  int32_t group;              // query heads per kv head
+  int32_t head_dim;
+  int32_t q_type, kv_type;    // MM3IDX_TYPE_*
+  const void* k;
+  const void* v;
+  int64_t k_page, k_tok, k_head;
+  int64_t v_page, v_tok, v_head;
+  int32_t num_pages;
+  int32_t page_shift;         // log2 of the page's tokens
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  int32_t num_reqs, query_len, max_seq_len;
+  float scale;                // sm_scale * k_scale
+  float v_scale;
+  void* out;
+  int64_t o_tok, o_head;
+  float* lse;                 // may be null
+  int64_t lse_tok;
+  float* weights;             // [rows, w_stride] fp32, may be null
+  int64_t w_stride;
+  int32_t w_width;            // cdiv(max_seq_len, 128)
+  float* lse_ws;              // [rows, q heads] log-sum-exp, for the weights
+  int32_t* status;
+};
+
+struct WeightArgs {
+  float* acc;
+  int64_t acc_stride;
+  const float* w;             // null: nothing to add
+  int64_t w_stride;
+  const int32_t* ids;         // null: dense
+  int64_t ids_stride;
+  int32_t topk;
+  const int32_t* seq_lens;
+  int32_t num_reqs, query_len, max_seq_len;
+  double decay;
+  int32_t* status;
+};
+
+struct EvictTable {
+  const int32_t* in;
+  int64_t in_stride;
+  int32_t* out;
+  int64_t out_stride;
+  int32_t* freed;
+  int64_t freed_stride;
+};
+
+struct EvictArgs {
+  WeightArgs w;
+  int32_t budget, init_blocks, local_blocks;
+  int32_t width;              // cdiv(max_seq_len, 128)
+  EvictTable t[2];
+  int32_t* ids;
+  int64_t ids_stride;
+  float* acc_out;
+  int64_t acc_out_stride;
+  int32_t* seq_out;
+};
+
+struct DraftArgs {
+  const void* target;
+  int64_t t_req, t_row;
+  const void* draft;          // null: drafted tokens had probability 1
+  int64_t d_req, d_row;
+  int32_t type;
+  const int32_t* tokens;
+  int64_t tok_stride;
+  const int32_t* lens;        // null: drafts each
+  const float* u;
+  int64_t u_stride;
+  int32_t num_reqs, drafts, vocab;
+  int32_t* out;
+  int64_t out_stride;
+  int32_t* accepted;
+  int32_t* status;
+};
+
+cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_accumulate(const WeightArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_verify(const DraftArgs& a, int sms, cudaStream_t s);
+
+}  // namespace mm3idx

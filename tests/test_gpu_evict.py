@@ -1,0 +1,159 @@
+"""mm3idx_accumulate_weights and mm3idx_evict_blocks against a plain form:
+the sums rounded once, the kept ids, tables, freed entries and lengths exact."""
+
+import math
+
+import pytest
+import torch
+
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mm(cuda_device):
+    import sparse_attention_block_paged_gb300 as m
+    m.get_device_error()
+    return m
+
+
+def inputs(lens, *, ql, topk, seed, ties=False, max_seq_len=None):
+    g = torch.Generator().manual_seed(seed)
+    most = max_seq_len or max(max(lens), 1)
+    width, reqs = R.cdiv(most, 128), len(lens)
+
+    def mass(*shape):
+        x = torch.exp(2 * torch.randn(*shape, generator=g))
+        return torch.round(x).clamp(max=4) if ties else x
+
+    acc = mass(reqs, width + 3)
+    if topk:
+        ids = torch.full((reqs * ql, topk), -1, dtype=torch.int32)
+        for r in range(reqs * ql):
+            n = R.cdiv(max(0, lens[r // ql]), 128)
+            m = min(n, topk)
+            if m:
+                ids[r, :m] = torch.randperm(n, generator=g)[:m].sort().values.to(torch.int32)
+        w = mass(reqs * ql, topk)
+    else:
+        ids, w = None, mass(reqs * ql, width + 1)
+    tables = [torch.randint(0, 10 ** 6, (reqs, width + k), generator=g, dtype=torch.int32)
+              for k in (0, 5)]
+    return acc, ids, w, tables, width, most
+
+
+CASES = [
+    # lens, query_len, topk, budget, init, local, decay, ties
+    ([1, 128, 129, 0, 5000, 4096], 1, 0, 8, 1, 2, 1.0, False),
+    ([1, 128, 129, 0, 5000, 4096], 2, 4, 8, 1, 2, 0.9, False),
+    ([4000, 300, 4000], 4, 16, 3, 1, 2, 1.0, False),            # only the forced blocks stay
+    ([4000, 300, 4000], 1, 32, 100, 1, 2, 0.5, False),          # everything stays
+    ([20000, 19999, 100, 12345], 3, 16, 40, 0, 1, 1.0, True),   # many equal weights
+    ([20000, 19999, 100, 12345], 1, 0, 41, 3, 5, 0.0, True),
+    ([128 * 5000, 128 * 1025 - 1, 128 * 1024], 1, 0, 1024, 4, 8, 0.99, False),
+    ([128 * 9000 + 1, 77], 8, 32, 2050, 1, 2, 0.99, False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"max{max(c[0])}q{c[1]}k{c[2]}b{c[3]}")
+def test_evict_matches_plain_form(mm, case):
+    lens, ql, topk, budget, init, local, decay, ties = case
+    acc, ids, w, tables, width, most = inputs(lens, ql=ql, topk=topk, seed=sum(lens) + topk,
+                                              ties=ties)
+    new, kept, out_lens = R.evict_ref(acc, lens, tables, budget=budget, init=init, local=local,
+                                      max_seq_len=most, weights=w, ids=ids, ql=ql, decay=decay)
+    d = dict(acc=acc.cuda(), ids=None if ids is None else ids.cuda(), w=w.cuda(),
+             lens=torch.tensor(lens, dtype=torch.int32).cuda(), t=[t.cuda() for t in tables])
+    kw = dict(budget=budget, init_blocks=init, local_blocks=local, max_seq_len=most,
+              block_weights=d["w"], ids=d["ids"], query_len=ql, decay=decay)
+
+    # the sum alone, in place
+    summed = mm.accumulate_weights(d["acc"].clone(), d["w"], d["lens"], query_len=ql,
+                                   max_seq_len=most, ids=d["ids"], decay=decay).cpu()
+    for i, n in enumerate(lens):
+        n = R.cdiv(n, 128)
+        assert torch.equal(summed[i, :n], new[i][:n].float())
+        assert torch.equal(summed[i, n:], acc[i, n:])
+
+    def expect(r, padded_to):
+        for i, stay in enumerate(kept):
+            n = R.cdiv(lens[i], 128)
+            gone = [b for b in range(n) if b not in set(stay)]
+            m = len(stay)
+            assert r.ids[i].tolist() == stay + [-1] * (budget - m)
+            assert int(r.seq_lens[i]) == out_lens[i]
+            assert torch.equal(r.weights[i, :m].cpu(), new[i][stay].float())
+            assert (r.weights[i, m:width] == 0).all()
+            for table, got, freed in ((tables[0], r.block_table, r.freed),
+                                      (tables[1], r.attention_block_table, r.attention_freed)):
+                row = table[i].tolist()
+                assert got[i, :budget].tolist() == [row[b] for b in stay] + [-1] * (budget - m)
+                if padded_to:
+                    assert got[i, budget:].tolist() == row[budget:]
+                f = freed[i].tolist()
+                assert f == [row[b] for b in gone] + [-1] * (len(f) - len(gone))
+
+    r = mm.evict_blocks(d["acc"], d["lens"], d["t"][0], attention_block_table=d["t"][1], **kw)
+    expect(r, False)
+    assert torch.equal(d["acc"].cpu(), acc) and torch.equal(d["t"][0].cpu(), tables[0])
+    assert d["lens"].tolist() == lens
+    # into the same buffers, captured and replayed
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            mm.evict_blocks(d["acc"], d["lens"], d["t"][0], attention_block_table=d["t"][1],
+                            out=r, **kw)
+        for t in r:
+            t.fill_(9)
+        graph.replay()
+        graph.replay()
+    side.synchronize()
+    expect(r, False)
+    # in place (where the tables have the columns)
+    if budget <= width:
+        r = mm.evict_blocks(d["acc"], d["lens"], d["t"][0], attention_block_table=d["t"][1],
+                            in_place=True, **kw)
+        assert r.block_table is d["t"][0] and r.weights is d["acc"] and r.seq_lens is d["lens"]
+        expect(r, True)
+        assert torch.equal(d["acc"][:, width:].cpu(), acc[:, width:])
+    assert mm.get_device_error() == 0
+
+
+def test_without_new_weights_and_with_nan(mm):
+    acc = torch.tensor([[5.0, 1.0, float("nan"), 3.0, -0.0, 0.0, float("inf"), 2.0]])
+    lens = torch.tensor([8 * 128 - 3], dtype=torch.int32).cuda()
+    table = torch.arange(10, 18, dtype=torch.int32)[None].cuda()
+    r = mm.evict_blocks(acc.cuda(), lens, table, budget=5, init_blocks=0, local_blocks=1,
+                        max_seq_len=1024)
+    assert r.ids.tolist() == [[0, 2, 3, 6, 7]]
+    assert r.freed.tolist() == [[11, 14, 15]]
+    assert r.block_table.tolist() == [[10, 12, 13, 16, 17]]
+    assert r.seq_lens.tolist() == [8 * 128 - 3 - 3 * 128]
+    r = mm.evict_blocks(acc.cuda(), lens, table, budget=7, init_blocks=0, local_blocks=1,
+                        max_seq_len=1024)
+    assert r.ids.tolist() == [[0, 1, 2, 3, 4, 6, 7]]      # -0 and 0 are equal: the lower id stays
+    assert r.attention_block_table is None
+
+
+def test_ids_given_twice_and_outside(mm):
+    acc = torch.ones((1, 4)).cuda()
+    lens = torch.tensor([400], dtype=torch.int32).cuda()
+    ids = torch.tensor([[2, 2, -1, 4, 3], [0, 2, 70000, -5, 1]], dtype=torch.int32).cuda()
+    w = torch.arange(1.0, 11.0).view(2, 5).cuda()
+    mm.accumulate_weights(acc, w, lens, query_len=2, max_seq_len=512, ids=ids, decay=0.5)
+    assert acc.tolist() == [[6.5, 10.5, 10.5, 5.5]]
+    assert mm.get_device_error() == 0
+
+
+def test_lengths_out_of_bounds_are_clamped(mm):
+    acc = torch.arange(8.0).view(2, 4).cuda()
+    lens = torch.tensor([900, -2], dtype=torch.int32).cuda()
+    table = torch.arange(8, dtype=torch.int32).view(2, 4).cuda()
+    r = mm.evict_blocks(acc, lens, table, budget=2, init_blocks=0, local_blocks=1,
+                        max_seq_len=512)
+    assert mm.get_device_error() == mm.DEV_SEQ_TOO_LONG | mm.DEV_SEQ_TOO_SHORT
+    assert r.ids.tolist() == [[2, 3], [-1, -1]] and r.seq_lens.tolist() == [256, 0]
+    assert r.freed.tolist() == [[0, 1], [-1, -1]]
