@@ -20,9 +20,10 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmm3idx.so")
 SOURCES = ["api.cu", "decode.cu", "decode_fp4.cu", "prefill.cu", "select.cu", "dequant.cu",
-           "sparse_table.cu", "api_serving.cu", "attention.cu", "evict.cu", "verify.cu"]
+           "sparse_table.cu", "api_serving.cu", "attention.cu", "attention_bf16.cu",
+           "attention_fp16.cu", "attention_e4m3.cu", "evict.cu", "verify.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "warp_select.cuh", "decode_common.cuh", "nvfp4.cuh",
-           "serving.h"]
+           "serving.h", "attention.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -68,14 +68,55 @@ int check_attention(const mm3idx_attention_t* a) {
   return MM3IDX_OK;
 }
 
-size_t attention_ws_bytes(int sms, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                          int32_t num_reqs, int32_t query_len, int32_t max_seq_len, bool weights) {
-  (void)sms;
-  (void)kv_heads;
-  (void)head_dim;
-  (void)max_seq_len;
-  (void)weights;
-  return align256(static_cast<size_t>(num_reqs) * query_len * q_heads * 4);
+// Workspace: [tickets][partial references and sums][partial outputs], and for
+// block weights [rows' log-sum-exps][tiles' log-sum-exps], each 256-aligned.
+struct AttentionWs {
+  size_t tickets, ml, o, row, tile, total;
+};
+
+AttentionWs attention_ws(int sms, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                         int32_t num_reqs, int32_t query_len, int32_t max_seq_len, bool weights) {
+  const int64_t rows = static_cast<int64_t>(q_heads / kv_heads) * query_len;  // of a kv head
+  const size_t tasks = static_cast<size_t>(num_reqs) * kv_heads * cdiv(rows, 64);
+  const int r = static_cast<int>(rows < 64 ? rows : 64);
+  AttentionWs w{};
+  w.tickets = 0;
+  w.ml = w.tickets + align256(tasks * 4);
+  w.o = w.ml + static_cast<size_t>(2 * sms) * 64 * 8;
+  w.row = w.o + static_cast<size_t>(2 * sms) * 64 * head_dim * 4;
+  w.tile = w.row + (weights ? align256(static_cast<size_t>(num_reqs) * query_len * q_heads * 4) : 0);
+  w.total = w.tile + (weights ? align256(tasks * cdiv(max_seq_len, kBlock) * 16 *
+                                         attention_row_tiles16(r) * 4)
+                              : 0);
+  return w;
+}
+
+// [pages, heads, tokens, d] of one cache: boxes of one page and kv head, at
+// most 128 bytes of d.
+int make_cache_map(const mm3idx_attention_t* p, bool values, CUtensorMap* m) {
+  TensorMapEncode enc = tensor_map_encoder();
+  if (!enc) return MM3IDX_ERR_CUDA;
+  const cuuint64_t size = p->kv_type == MM3IDX_TYPE_E4M3 ? 1 : 2;
+  const CUtensorMapDataType type = p->kv_type == MM3IDX_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : p->kv_type == MM3IDX_TYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint32_t row = static_cast<cuuint32_t>(p->head_dim * size > 128 ? 128 : p->head_dim * size);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->head_dim),
+                              static_cast<cuuint64_t>(p->page_size),
+                              static_cast<cuuint64_t>(p->kv_heads),
+                              static_cast<cuuint64_t>(p->num_pages)};
+  const cuuint64_t strides[3] = {
+      static_cast<cuuint64_t>(values ? p->v_token_stride : p->k_token_stride) * size,
+      static_cast<cuuint64_t>(values ? p->v_head_stride : p->k_head_stride) * size,
+      static_cast<cuuint64_t>(values ? p->v_page_stride : p->k_page_stride) * size};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row / size),
+                             static_cast<cuuint32_t>(p->page_size), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, type, 4, const_cast<void*>(values ? p->v_cache : p->k_cache), dims,
+                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MM3IDX_OK : MM3IDX_ERR_ATTENTION_LAYOUT;
 }
 
 int check_weights(const mm3idx_weights_t* w) {
@@ -128,8 +169,9 @@ int mm3idx_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t 
   int32_t* status = nullptr;
   const int rc = library_device(&sms, &status);
   if (rc) return rc;
-  *bytes = attention_ws_bytes(sms, q_heads, kv_heads, head_dim, num_reqs, query_len, max_seq_len,
-                              block_weights != 0);
+  *bytes = attention_ws(sms, q_heads, kv_heads, head_dim, num_reqs, query_len, max_seq_len,
+                        block_weights != 0)
+               .total;
   return MM3IDX_OK;
 }
 
@@ -141,9 +183,9 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   int sms = 0;
   int32_t* status = nullptr;
   if ((rc = library_device(&sms, &status))) return rc;
-  const size_t need = attention_ws_bytes(sms, p->q_heads, p->kv_heads, p->head_dim, p->num_reqs,
-                                         p->query_len, p->max_seq_len, p->block_weights != nullptr);
-  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const AttentionWs w = attention_ws(sms, p->q_heads, p->kv_heads, p->head_dim, p->num_reqs,
+                                     p->query_len, p->max_seq_len, p->block_weights != nullptr);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return MM3IDX_ERR_WORKSPACE;
   AttentionArgs a{};
   a.q = p->q;
@@ -154,14 +196,6 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   a.head_dim = p->head_dim;
   a.q_type = p->q_type;
   a.kv_type = p->kv_type;
-  a.k = p->k_cache;
-  a.v = p->v_cache;
-  a.k_page = p->k_page_stride;
-  a.k_tok = p->k_token_stride;
-  a.k_head = p->k_head_stride;
-  a.v_page = p->v_page_stride;
-  a.v_tok = p->v_token_stride;
-  a.v_head = p->v_head_stride;
   a.num_pages = p->num_pages;
   a.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
   a.table = p->page_table;
@@ -181,8 +215,23 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   a.w_stride = p->block_weights_stride;
   a.w_width = static_cast<int32_t>(cdiv(p->max_seq_len, kBlock));
   a.status = status;
-  a.lse_ws = static_cast<float*>(workspace);
-  return cuda_status(launch_attention(a, sms, static_cast<cudaStream_t>(stream)));
+  const int rows = a.group * a.query_len;
+  a.row_tiles = static_cast<int32_t>(cdiv(rows, 64));
+  a.tasks = a.kv_heads * a.row_tiles;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.tickets = reinterpret_cast<unsigned int*>(ws + w.tickets);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  if (p->block_weights) {
+    a.row_lse = reinterpret_cast<float*>(ws + w.row);
+    a.tile_lse = reinterpret_cast<float*>(ws + w.tile);
+  }
+  CUtensorMap kmap, vmap;
+  if ((rc = make_cache_map(p, false, &kmap)) || (rc = make_cache_map(p, true, &vmap))) return rc;
+  // One CTA an SM; no more than there can be tiles.
+  const int64_t most = static_cast<int64_t>(p->num_reqs) * a.tasks * (cdiv(p->max_seq_len, kBlock) + 2);
+  const int grid = static_cast<int>(most < sms ? most : sms);
+  return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
 }
 
 int mm3idx_accumulate_weights(const mm3idx_weights_t* w, void* stream) {

@@ -1,0 +1,1027 @@
+// attention.cuh -- attention of a few new tokens a request over the paged
+// key-value cache (include/mm3idx.h, mm3idx_paged_attention), one kernel per
+// element type, head size and row count; the type's instances are compiled in
+// attention_<type>.cu.
+//
+// Mathematics.  For a query row and the tokens it sees, taken in any order and
+// any grouping, three numbers are enough: the reference m, the sum
+// l = sum 2^(x_t - m) and the vector o = sum 2^(x_t - m) v_t, with
+// x_t = scale log2(e) q.k_t.  Two such triples join to m = max(m1, m2),
+// l = l1 2^(m1-m) + l2 2^(m2-m), o alike; the result is o / l, and
+// m + log2 l is the (base 2) log-sum-exp.  Every warp keeps a triple of its
+// own over its part of the tokens, CTAs join their warps' through shared
+// memory, and a (request, kv head) that several CTAs share is joined by the
+// last of them to finish, in a fixed order, so a result never depends on timing.
+//
+// What bounds it.  K and V of the visible tokens are read once: 4 D bytes a
+// token in 16 bits against 4 D flops a query head, 2 to 16 flops a byte for
+// the group sizes in use, far below what the tensor cores need: the kernel is
+// a stream of pages from HBM.  So:
+//
+//   * Work partition.  The list of all (request, kv head, 128-token tile) is
+//     cut into equal shares on the device, one a CTA, one CTA an SM; lengths
+//     need no host round trip and cost no imbalance.
+//   * Pages go through a ring of slots in shared memory (192 KB for 16-bit
+//     D = 128: six slots of 128 tokens, keys and values in turn), filled by
+//     one producer warp with 4-D tiled TMA copies, so strides and page sizes
+//     cost nothing and about three tiles are in flight.
+//   * Eight warps consume it.  The query rows of one kv head (group x
+//     query_len) are rows of 16-row matrix products (mma.sync m16n8k16: with
+//     this few rows the kernel needs a tenth of even that rate, and a warp
+//     that owns its scores needs no exchange with others inside the loop).
+//     Warp w owns 16-row tile w % RT and token group w / RT of each tile.
+//   * The reference m moves only when a score passes it by 8 (a factor of 256
+//     in the weights, which fp32 sums and 16-bit weights hold without loss),
+//     so the accumulators are rarely rescaled.
+//   * Weights for the second product are held as the sum of two 16-bit numbers
+//     (one would cost an error as large as the output's own rounding; the
+//     second product's extra MMAs hide behind the copies).  Over e4m3 values
+//     one fp16 number is enough: its step is 1/8 of the output's in bf16.
+//   * e4m3 pages are widened to fp16 (exact) in registers.  The query is then
+//     fp16 as well, scaled by a power of two so that its largest element is
+//     in [1, 2): what this loses is below 2^-25 of that element.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/mm3idx.h"
+#include "ptx.cuh"
+#include "serving.h"
+
+namespace mm3idx {
+namespace attn {
+
+constexpr int kConsumers = 8;                    // warps
+constexpr int kProducer = kConsumers;            // warp index
+constexpr int kWeigher = kConsumers + 1;         // warp that writes the tiles' weights
+constexpr int kThreads = (kConsumers + 2) * 32;
+constexpr int kTile = kBlock;                    // tokens of a tile
+constexpr int kRedStride = 40;                   // floats of a 32-column row in the join buffer
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.0f;
+
+// Positions that a (request, kv head) takes in the list beyond its tiles (its
+// start and its join cost time, too), and the fewest positions worth a CTA.
+constexpr int kSegCost = 2;
+constexpr int kMinShare = 4;
+
+template <int KV, int D>
+struct Cfg {
+  static constexpr bool kByte = KV == MM3IDX_TYPE_E4M3;
+  static constexpr int kElem = kByte ? 1 : 2;
+  static constexpr int kRow = D * kElem > 128 ? 128 : D * kElem;  // bytes of a row in a copy
+  static constexpr int kHalves = D * kElem / kRow;                // copies of a page
+  static constexpr int kHalf = kTile * kRow;
+  static constexpr int kSlot = kHalves * kHalf;
+  static constexpr int kSlots = kSlot == 32768 ? 6 : kSlot == 16384 ? 12 : 16;  // even: keys, values
+  static constexpr uint32_t kSwizzle = kRow == 128 ? 0x70 : 0x30;
+  static constexpr int oRed = kSlots * kSlot;
+  static constexpr int oMl = oRed + kConsumers * 16 * kRedStride * 4;
+  static constexpr int oFin = oMl + kConsumers * 16 * 8;
+  static constexpr int oSlice = oFin + 64 * 8;
+  static constexpr int oBar = oSlice + kSlots / 2 * kConsumers * 16 * 4;
+  static constexpr int oMask = oBar + 3 * kSlots * 8;
+  static constexpr int oMisc = oMask + kSlots * 4;
+  static constexpr int kSmem = oMisc + 128 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+struct Misc {
+  long long lo, hi, total, p0, pl;
+  int t0, tl, grid;
+  int abort, last;
+  long long scan[kConsumers];
+};
+
+__device__ __forceinline__ int request_len(const AttentionArgs& a, int i) {
+  return min(max(__ldg(a.seq_lens + i), 0), a.max_seq_len);
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Positions of one task (request, kv head, 64-row tile) in the list.
+__device__ __forceinline__ long long task_slots(int len) {
+  return len > 0 ? tiles_of(len) + kSegCost : 0;
+}
+
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+// The consumer threads: this CTA's share of the list and the tasks at its ends.
+__device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.num_reqs + kConsumers * 32 - 1) / (kConsumers * 32);
+  const int first = min(tid * per, a.num_reqs), end = min(first + per, a.num_reqs);
+  long long mine = 0;
+  int bits = 0;
+  for (int i = first; i < end; ++i) {
+    const int raw = __ldg(a.seq_lens + i);
+    if (raw > a.max_seq_len) bits |= MM3IDX_DEV_SEQ_TOO_LONG;
+    if (raw != 0 && raw < a.query_len) bits |= MM3IDX_DEV_SEQ_TOO_SHORT;
+    mine += task_slots(min(max(raw, 0), a.max_seq_len));
+  }
+  if (bits && blockIdx.x == 0) atomicOr(a.status, bits);
+  mine *= a.tasks;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) m->scan[warp] = incl;
+  consumer_sync();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kConsumers; ++w) {
+    const long long s = m->scan[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  // No share is empty: at most one CTA per kMinShare positions takes part.
+  const long long most = total / kMinShare;
+  const int G = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+  const long long c = blockIdx.x;
+  const long long lo = c < G ? total * c / G : 0, hi = c < G ? total * (c + 1) / G : 0;
+  if (tid == 0) {
+    m->lo = lo;
+    m->hi = hi;
+    m->total = total;
+    m->grid = G;
+  }
+  if (hi <= lo || mine == 0) return;
+  const bool has_lo = before <= lo && lo < before + mine;
+  const bool has_hi = before <= hi - 1 && hi - 1 < before + mine;
+  if (!has_lo && !has_hi) return;
+  long long P = before;
+  for (int i = first; i < end; ++i) {
+    const long long one = task_slots(request_len(a, i));
+    const long long all = one * a.tasks;
+    if (has_lo && P <= lo && lo < P + all) {
+      const int h = static_cast<int>((lo - P) / one);
+      m->t0 = i * a.tasks + h;
+      m->p0 = P + h * one;
+    }
+    if (has_hi && P <= hi - 1 && hi - 1 < P + all) {
+      const int h = static_cast<int>((hi - 1 - P) / one);
+      m->tl = i * a.tasks + h;
+      m->pl = P + h * one;
+    }
+    P += all;
+  }
+}
+
+// One stretch of a CTA's share: tiles [b0, b1) of a task.
+struct Segment {
+  int task, req, len;
+  int b0, b1, nb;
+  long long pos;       // the task's first position in the list
+};
+
+// The stretches of the share, the two that other CTAs may share first.
+struct Walker {
+  long long lo, hi, p0, pl, P;
+  int t0, tl, t, stage;
+  __device__ explicit Walker(const Misc* m)
+      : lo(m->lo), hi(m->hi), p0(m->p0), pl(m->pl), P(0), t0(m->t0), tl(m->tl), t(0), stage(0) {}
+  __device__ __forceinline__ bool emit(const AttentionArgs& a, int task, long long pos,
+                                       Segment& s) const {
+    s.task = task;
+    s.req = task / a.tasks;
+    s.len = request_len(a, s.req);
+    s.nb = tiles_of(s.len);
+    s.pos = pos;
+    const long long pb = pos + kSegCost;
+    const long long from = pb > lo ? pb : lo, to = pb + s.nb < hi ? pb + s.nb : hi;
+    if (s.nb == 0 || to <= from) return false;
+    s.b0 = static_cast<int>(from - pb);
+    s.b1 = static_cast<int>(to - pb);
+    return true;
+  }
+  __device__ bool next(const AttentionArgs& a, Segment& s) {
+    if (lo >= hi) return false;
+    if (stage == 0) {
+      stage = 1;
+      if (emit(a, t0, p0, s)) return true;
+    }
+    if (stage == 1) {
+      stage = 2;
+      t = t0 + 1;
+      P = p0 + task_slots(request_len(a, t0 / a.tasks));
+      if (tl != t0 && emit(a, tl, pl, s)) return true;
+    }
+    while (t < tl) {
+      const int task = t++;
+      const long long pos = P;
+      P += task_slots(request_len(a, task / a.tasks));
+      if (emit(a, task, pos, s)) return true;
+    }
+    return false;
+  }
+};
+
+// The CTA whose share holds position x.
+__device__ __forceinline__ int cta_of(long long x, long long total, int grid) {
+  return static_cast<int>(((x + 1) * grid - 1) / total);
+}
+
+// ------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// D += A B: A 16x16 (row), B 16x8 (col), D 16x8 fp32.
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats as a pair of 16-bit numbers (lo in the low half), and what the
+// rounding left as a second pair.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t packed) {
+  float a, b;
+  if constexpr (BF16) {
+    a = __uint_as_float(packed << 16);
+    b = __uint_as_float(packed & 0xffff0000u);
+  } else {
+    const __half2 h = *reinterpret_cast<const __half2*>(&packed);
+    a = __low2float(h);
+    b = __high2float(h);
+  }
+  return pack2<BF16>(lo - a, hi - b);
+}
+
+// Two e4m3 numbers (the low 16 bits, or the high ones) as two fp16.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+// The halves of a pair (tokens t and t + 1) that lie below `end`.
+__device__ __forceinline__ uint32_t below(int t, int end) {
+  return (t < end ? 0x0000ffffu : 0u) | (t + 1 < end ? 0xffff0000u : 0u);
+}
+
+// ------------------------------------------------------------------- kernel
+//
+// Fragments (thread t of a warp, c = t & 3, g = t >> 2).  Scores of 16 tokens:
+// s[0], s[1] row g, tokens 2c, 2c+1; s[2], s[3] row g+8; s[4..7] the same for
+// tokens 8+2c, 9+2c.  As the A operand of the second product they are, packed,
+// in place.  16-bit caches: d runs in order; e4m3: the thread's 2 D/16 k-steps
+// walk the D/4 bytes from c D/4 of a token's key (queries alike), and column n
+// of output tile 4 t + i is d = 32 t + 4 n + i, so that a thread loads four
+// neighbouring bytes of a value row.
+
+template <int KV, int D>
+struct State {
+  float o[D / 8][4];
+  float m0, m1, l0, l1;
+};
+
+template <int KV, int D, int RT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const AttentionArgs a) {
+  using C = Cfg<KV, D>;
+  constexpr int S = C::kSlots;
+  constexpr bool kByte = C::kByte;
+  constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
+  constexpr int TG = kConsumers / RT;               // token groups of a tile
+  constexpr int NS = RT;                            // 16-token slices of a warp
+  constexpr int NT = D / 8;                         // output tiles of 8 columns
+  constexpr int KS = D / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  float* red = reinterpret_cast<float*>(sm + C::oRed);
+  float2* ml = reinterpret_cast<float2*>(sm + C::oMl);     // [warp][16]
+  float2* fin = reinterpret_cast<float2*>(sm + C::oFin);   // [row of the task]
+  float* slice = reinterpret_cast<float*>(sm + C::oSlice); // [slot / 2][warp][16]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::oBar);
+  uint64_t* empty = full + S;
+  uint64_t* done = empty + S;                              // value slots: the tile's weights are there
+  uint32_t* mask = reinterpret_cast<uint32_t*>(sm + C::oMask);
+  Misc* misc = reinterpret_cast<Misc*>(sm + C::oMisc);
+  volatile int* abort_flag = &misc->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool weigh = a.tile_lse != nullptr;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kConsumers + ((s & 1) && weigh ? 1 : 0));
+      mbar_init(&done[s], kConsumers);
+    }
+    misc->abort = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x == kProducer * 32) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  // A programmatic dependent launch: what the kernel before it wrote is read
+  // (and the workspace it used is written) only after this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp < kConsumers) partition(a, misc);
+  __syncthreads();
+  Walker walk(misc);
+  Segment sg;
+
+  if (warp == kProducer) {
+    // ---------------------------------------------------------- producer
+    const int per = kTile >> a.page_shift;       // pages of a tile
+    const int batch = 32 / per;                  // tiles whose page ids one register holds
+    const int box = C::kRow << a.page_shift;
+    uint32_t slot = 0, round = 0, items = 0;
+    bool ok = true;
+    while (ok && walk.next(a, sg)) {
+      const int head = (sg.task % a.tasks) / a.row_tiles;
+      const int32_t* table = a.table + static_cast<int64_t>(sg.req) * a.table_stride;
+      const int pages = (sg.len + (1 << a.page_shift) - 1) >> a.page_shift;
+      auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
+      int cur = ids_from(sg.b0 * per), nxt = ids_from(sg.b0 * per + 32), k = 0;
+      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++k) {
+        if (k == batch) {
+          k = 0;
+          cur = nxt;
+          nxt = ids_from(b * per + 32);
+        }
+        const int id = __shfl_sync(0xffffffffu, cur, (k * per + lane) & 31);
+        const bool need = lane < per && b * per + lane < pages;
+        const uint32_t good = __ballot_sync(0xffffffffu, need && id >= 0 && id < a.num_pages);
+        if (__ballot_sync(0xffffffffu, need) != good && lane == 0)
+          atomicOr(a.status, MM3IDX_DEV_BAD_PAGE);
+        const int p = lane / C::kHalves, half = lane % C::kHalves;
+        const int page = __shfl_sync(0xffffffffu, id, p);
+        const bool issue = lane < per * C::kHalves && ((good >> p) & 1u);
+        const uint32_t bytes = __popc(good) * C::kHalves * box;
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          if (round > 0) ok = warp_wait(&empty[slot], (round - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            mask[slot] = good;
+            if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
+            else mbar_arrive(&full[slot]);
+          }
+          __syncwarp();
+          if (issue)
+            tma_load_4d(smem_u32(sm) + slot * C::kSlot + half * C::kHalf + p * box,
+                        kv ? &vmap : &kmap, &full[slot], half * (C::kRow / C::kElem), 0, head,
+                        page);
+          ++items;
+          if (++slot == S) {
+            slot = 0;
+            ++round;
+          }
+        }
+      }
+    }
+    // Every copy that was started lands before the CTA can exit.
+    if (lane == 0) {
+      const uint32_t pending = items < S ? items : S;
+      for (uint32_t k = 0; k < pending; ++k) {
+        const uint32_t idx = items - 1 - k;
+        int dummy = 0;
+        mbar_wait(&full[idx % S], (idx / S) & 1, &dummy);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWeigher) {
+    // ------------------------------------- log-sum-exp of each tile's rows
+    if (weigh) {
+      uint32_t slot = 1, round = 0;
+      bool ok = true;
+      while (ok && walk.next(a, sg)) {
+        for (int b = sg.b0; b < sg.b1 && ok; ++b) {
+          ok = warp_wait(&done[slot], round & 1, abort_flag);
+          if (!ok) break;
+          const float* from = slice + (slot >> 1) * kConsumers * 16;
+          float* to = a.tile_lse + (static_cast<int64_t>(sg.task) * a.w_width + b) * (RT * 16);
+          for (int r = lane; r < RT * 16; r += 32) {
+            float x[TG], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+              x[t] = from[(t * RT + (r >> 4)) * 16 + (r & 15)];
+              top = fmaxf(top, x[t]);
+            }
+            const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int t = 0; t < TG; ++t) sum += ex2(x[t] - ref);
+            to[r] = ref + lg2(sum);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          slot += 2;
+          if (slot > S) {
+            slot = 1;
+            ++round;
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- consumers
+    const int c = lane & 3, g = lane >> 2;
+    const int rt = warp % RT, tg = warp / RT;
+    const uint32_t ring = smem_u32(sm);
+    State<KV, D> st;
+    uint32_t slot = 0, phase = 0;
+    bool dead = false;       // a wait gave up: go through the motions to the end
+
+    // Rows of empty requests.
+    {
+      const int heads = a.kv_heads * a.group;
+      for (int i = blockIdx.x * kConsumers + warp; i < a.num_reqs; i += gridDim.x * kConsumers) {
+        if (request_len(a, i) > 0) continue;
+        const int per_row = heads * (D / 8);
+        for (int e = lane; e < a.query_len * per_row; e += 32) {
+          const int64_t row = static_cast<int64_t>(i) * a.query_len + e / per_row;
+          const int h = e % per_row / (D / 8), d = e % (D / 8) * 8;
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head + d;
+          *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+          if (d == 0) {
+            if (a.lse) a.lse[row * a.lse_tok + h] = -INFINITY;
+            if (weigh) a.row_lse[row * heads + h] = -INFINITY;
+          }
+        }
+      }
+    }
+
+    while (walk.next(a, sg)) {
+      const int sub = sg.task % a.tasks;                   // kv head and 64-row tile
+      const int head = sub / a.row_tiles, row0 = (sub % a.row_tiles) * 64;
+      const int R = a.group * a.query_len;
+      const int rows = min(64, R - row0);                  // of this task
+      const int64_t tok0 = static_cast<int64_t>(sg.req) * a.query_len;
+      // Row r of the kv head is query token r / group, query head r % group.
+      const int ra = row0 + rt * 16 + g, rb = ra + 8;
+      const bool va = ra < R, vb = rb < R;
+      const int ja = min(ra, R - 1) / a.group, jb = min(rb, R - 1) / a.group;
+      const int shift = sg.len - a.query_len + 1;          // query token j sees [0, shift + j)
+      const int j_lo = min(row0 + rt * 16, R - 1) / a.group;
+      const int j_hi = min(row0 + rt * 16 + 15, R - 1) / a.group;
+      const int lim_a = shift + ja, lim_b = shift + jb;
+      const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
+      const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
+
+      // Queries.
+      uint32_t q[KS][4];
+      float sc_a = a.scale * kLog2e, sc_b = sc_a;
+      {
+        const uint16_t* qa = static_cast<const uint16_t*>(a.q) + (tok0 + ja) * a.q_tok +
+                             static_cast<int64_t>(head * a.group + min(ra, R - 1) % a.group) * a.q_head;
+        const uint16_t* qb = static_cast<const uint16_t*>(a.q) + (tok0 + jb) * a.q_tok +
+                             static_cast<int64_t>(head * a.group + min(rb, R - 1) % a.group) * a.q_head;
+        if constexpr (!kByte) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const int d = ks * 16 + 2 * c;
+            q[ks][0] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d)) : 0u;
+            q[ks][1] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d)) : 0u;
+            q[ks][2] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d + 8)) : 0u;
+            q[ks][3] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d + 8)) : 0u;
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint16_t* src = (x ? qb : qa) + c * (D / 4);
+            const bool valid = x ? vb : va;
+            float f[D / 4];
+            float top = 0.0f;
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (valid) w = __ldg(reinterpret_cast<const uint4*>(src) + u);
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                if (a.q_type == MM3IDX_TYPE_BF16) {
+                  lo = __uint_as_float(ww[e] << 16);
+                  hi = __uint_as_float(ww[e] & 0xffff0000u);
+                } else {
+                  const __half2 h = *reinterpret_cast<const __half2*>(&ww[e]);
+                  lo = __low2float(h);
+                  hi = __high2float(h);
+                }
+                f[u * 8 + 2 * e] = lo;
+                f[u * 8 + 2 * e + 1] = hi;
+                top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+              }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^e of the row's largest element (1 where that is 0)
+            const int e = min(static_cast<int>(__float_as_uint(top) >> 23), 253);
+            const float down = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+            const float up = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+            if (x) sc_b *= up;
+            else sc_a *= up;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              q[ks][x] = pack2<false>(f[4 * ks] * down, f[4 * ks + 1] * down);
+              q[ks][2 + x] = pack2<false>(f[4 * ks + 2] * down, f[4 * ks + 3] * down);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.0f;
+      st.m0 = st.m1 = -INFINITY;
+      st.l0 = st.l1 = 0.0f;
+
+      for (int b = sg.b0; b < sg.b1; ++b) {
+        // ------------------------------------------------------- scores
+        if (!dead) dead = !warp_wait(&full[slot], phase, abort_flag);
+        const uint32_t pages = mask[slot];
+        const uint32_t kbase = ring + slot * C::kSlot;
+        const int t0 = b * kTile;
+        float s[NS][8];
+        bool act[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const int ts = (tg * NS + n) * 16;
+          act[n] = !idle && !dead && t0 + ts < lim_hi && ((pages >> (ts >> a.page_shift)) & 1u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[n][e] = 0.0f;
+          if (act[n]) {
+            float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&s[n][0]);
+            float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&s[n][4]);
+            if constexpr (!kByte) {
+              const int tok = ts + ((lane >> 4) << 3) + (lane & 7);
+              const uint32_t row = kbase + tok * C::kRow;
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks) {
+                const int ch = ks * 2 + ((lane >> 3) & 1);
+                uint32_t r[4];
+                ldmatrix4(row + (ch >> 3) * C::kHalf + (((ch & 7) ^ (tok & 7)) << 4), r);
+                mma<kBf>(lo, q[ks], r[0], r[1]);
+                mma<kBf>(hi, q[ks], r[2], r[3]);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t off = (ts + 8 * x + g) * C::kRow + c * (D / 4);
+                const uint32_t twist = (off >> 3) & C::kSwizzle;
+#pragma unroll
+                for (int u = 0; u < D / 64; ++u) {
+                  const uint4 w = lds128(kbase + ((off + 16 * u) ^ twist));
+                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    mma<false>(x ? hi : lo, q[u * 4 + e], widen_lo(ww[e]), widen_hi(ww[e]));
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        ++slot;      // the values' slot (kSlots is even)
+
+        // ------------------------------------------------------ softmax
+        float top_a = -INFINITY, top_b = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const int t = t0 + (tg * NS + n) * 16 + 2 * c;
+          const bool whole = act[n] && t0 + (tg * NS + n) * 16 + 16 <= lim_lo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool first = (e & 2) == 0;
+            const int tok = t + (e & 1) + ((e & 4) ? 8 : 0);
+            float x = s[n][e] * (first ? sc_a : sc_b);
+            if (!whole && (!act[n] || tok >= (first ? lim_a : lim_b))) x = -INFINITY;
+            s[n][e] = x;
+            if (first) top_a = fmaxf(top_a, x);
+            else top_b = fmaxf(top_b, x);
+          }
+        }
+        if (__any_sync(0xffffffffu, top_a > st.m0 + kRaise || top_b > st.m1 + kRaise)) {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, o));
+            top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, o));
+          }
+          const float na = fmaxf(st.m0, top_a), nb = fmaxf(st.m1, top_b);
+          const float fa = na == -INFINITY ? 0.0f : ex2(st.m0 - na);
+          const float fb = nb == -INFINITY ? 0.0f : ex2(st.m1 - nb);
+          st.m0 = na;
+          st.m1 = nb;
+          st.l0 *= fa;
+          st.l1 *= fb;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            st.o[n][0] *= fa;
+            st.o[n][1] *= fa;
+            st.o[n][2] *= fb;
+            st.o[n][3] *= fb;
+          }
+        }
+        const float ref_a = st.m0 == -INFINITY ? 0.0f : st.m0;
+        const float ref_b = st.m1 == -INFINITY ? 0.0f : st.m1;
+        uint32_t p[NS][4], pr[NS][4];
+        float sum_a = 0.0f, sum_b = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = ex2(s[n][e] - ((e & 2) ? ref_b : ref_a));
+          sum_a += (w[0] + w[1]) + (w[4] + w[5]);
+          sum_b += (w[2] + w[3]) + (w[6] + w[7]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            p[n][k] = pack2<kBf>(w[2 * k], w[2 * k + 1]);
+            if constexpr (!kByte) pr[n][k] = pack2_rest<kBf>(w[2 * k], w[2 * k + 1], p[n][k]);
+          }
+        }
+        st.l0 += sum_a;
+        st.l1 += sum_b;
+        // ------------------------------------------------------- values
+        if (!dead) dead = !warp_wait(&full[slot], phase, abort_flag);
+        const uint32_t vbase = ring + slot * C::kSlot;
+        // (the values' arrival says that the slot's last weights were read)
+        if (weigh) {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            sum_a += __shfl_xor_sync(0xffffffffu, sum_a, o);
+            sum_b += __shfl_xor_sync(0xffffffffu, sum_b, o);
+          }
+          if (c == 0) {
+            float* to = slice + ((slot >> 1) * kConsumers + warp) * 16;
+            to[g] = ref_a + lg2(sum_a);
+            to[g + 8] = ref_b + lg2(sum_b);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&done[slot]);
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          if (!act[n] || dead) continue;
+          const int ts = (tg * NS + n) * 16, t = t0 + ts + 2 * c;
+          const bool edge = t0 + ts + 16 > lim_lo;
+          // B operands of output tiles 2u, 2u+1 (16-bit) or 4u .. 4u+3 (e4m3)
+          auto load_v = [&](int u, uint32_t* r) {
+            if constexpr (!kByte) {
+              const int tok = ts + (lane & 15);
+              const int ch = u * 2 + (lane >> 4);
+              uint32_t x[4];
+              ldmatrix4_trans(vbase + tok * C::kRow + (ch >> 3) * C::kHalf +
+                                  (((ch & 7) ^ (tok & 7)) << 4), x);
+              r[0] = x[0]; r[1] = x[1]; r[2] = x[2]; r[3] = x[3];
+            } else {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t off = (ts + 2 * c + (k & 1) + (k >> 1) * 8) * C::kRow + u * 32 + g * 4;
+                w[k] = lds32(vbase + (off ^ ((off >> 3) & C::kSwizzle)));
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t x = __byte_perm(w[2 * k], w[2 * k + 1], 0x5140);
+                const uint32_t y = __byte_perm(w[2 * k], w[2 * k + 1], 0x7362);
+                r[0 + k] = widen_lo(x);
+                r[2 + k] = widen_hi(x);
+                r[4 + k] = widen_lo(y);
+                r[6 + k] = widen_hi(y);
+              }
+            }
+          };
+          constexpr int TU = kByte ? 4 : 2;       // output tiles of one load
+          if (!edge) {
+#pragma unroll
+            for (int u = 0; u < NT / TU; ++u) {
+              uint32_t r[2 * TU];
+              load_v(u, r);
+#pragma unroll
+              for (int k = 0; k < TU; ++k) {
+                mma<kBf>(st.o[u * TU + k], p[n], r[2 * k], r[2 * k + 1]);
+                if constexpr (!kByte) mma<kBf>(st.o[u * TU + k], pr[n], r[2 * k], r[2 * k + 1]);
+              }
+            }
+          } else {
+            // The last tokens: values that a row does not see do not meet its
+            // weights (0 times NaN), so the rows of each query token take
+            // their product with the values behind its limit zeroed.
+            for (int j = j_lo; j <= j_hi; ++j) {
+              const int end = shift + j;
+              const uint32_t k0 = below(t, end), k1 = below(t + 8, end);
+#pragma unroll
+              for (int u = 0; u < NT / TU; ++u) {
+                uint32_t r[2 * TU];
+                load_v(u, r);
+#pragma unroll
+                for (int k = 0; k < TU; ++k) {
+                  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma<kBf>(x, p[n], r[2 * k] & k0, r[2 * k + 1] & k1);
+                  if constexpr (!kByte) mma<kBf>(x, pr[n], r[2 * k] & k0, r[2 * k + 1] & k1);
+                  if (ja == j) {
+                    st.o[u * TU + k][0] += x[0];
+                    st.o[u * TU + k][1] += x[1];
+                  }
+                  if (jb == j) {
+                    st.o[u * TU + k][2] += x[2];
+                    st.o[u * TU + k][3] += x[3];
+                  }
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (++slot == S) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+
+      // ------------------------------------------------ join of the warps
+      // Quad sums of l, then the warps' triples through shared memory.  A
+      // first pass writes the result, or this CTA's partial one; the last CTA
+      // of a shared task then joins the partial ones in a second pass.
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
+        st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
+      }
+      const bool whole = sg.b0 == 0 && sg.b1 == sg.nb;
+      const long long pb = sg.pos + kSegCost;
+      const int first_cta = cta_of(pb, misc->total, misc->grid);
+      const int last_cta = cta_of(pb + sg.nb - 1, misc->total, misc->grid);
+      bool final = whole;
+      for (int pass = 0; pass < 2; ++pass) {
+        if (c == 0) {
+          ml[warp * 16 + g] = make_float2(st.m0, st.l0);
+          ml[warp * 16 + g + 8] = make_float2(st.m1, st.l1);
+        }
+        consumer_sync();
+        float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+          ma = fmaxf(ma, ml[(t * RT + rt) * 16 + g].x);
+          mb = fmaxf(mb, ml[(t * RT + rt) * 16 + g + 8].x);
+        }
+        const float fa = ma == -INFINITY ? 0.0f : ex2(st.m0 - ma);
+        const float fb = mb == -INFINITY ? 0.0f : ex2(st.m1 - mb);
+        const int slot_id = 2 * blockIdx.x + (sg.pos > walk.lo ? 1 : 0);
+        if (threadIdx.x < RT * 16) {
+          const int r = threadIdx.x;
+          float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+          for (int t = 0; t < TG; ++t) top = fmaxf(top, ml[(t * RT + (r >> 4)) * 16 + (r & 15)].x);
+#pragma unroll
+          for (int t = 0; t < TG; ++t) {
+            const float2 x = ml[(t * RT + (r >> 4)) * 16 + (r & 15)];
+            if (top != -INFINITY) sum += x.y * ex2(x.x - top);
+          }
+          if (final) {
+            if (r < rows) {
+              const int64_t row = tok0 + (row0 + r) / a.group;
+              const int h = head * a.group + (row0 + r) % a.group;
+              const float lse2 = sum == 0.0f ? -INFINITY : top + lg2(sum);
+              if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
+              if (weigh) a.row_lse[row * a.kv_heads * a.group + h] = lse2;
+            }
+            fin[r].x = sum == 0.0f ? 0.0f : a.v_scale / sum;
+          } else if (r < rows) {
+            __stcg(a.part_ml + static_cast<int64_t>(slot_id) * 64 + r, make_float2(top, sum));
+          }
+        }
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float* mine = red + warp * 16 * kRedStride;
+#pragma unroll
+          for (int u = 0; u < D / 32; ++u) {
+            if (u != ch) continue;             // static register indices
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float(&o)[4] = st.o[u * 4 + k];
+              if constexpr (!kByte) {
+                *reinterpret_cast<float2*>(mine + g * kRedStride + 8 * k + 2 * c) =
+                    make_float2(o[0] * fa, o[1] * fa);
+                *reinterpret_cast<float2*>(mine + (g + 8) * kRedStride + 8 * k + 2 * c) =
+                    make_float2(o[2] * fb, o[3] * fb);
+              } else {
+                mine[g * kRedStride + 8 * c + k] = o[0] * fa;
+                mine[g * kRedStride + 8 * c + 4 + k] = o[1] * fa;
+                mine[(g + 8) * kRedStride + 8 * c + k] = o[2] * fb;
+                mine[(g + 8) * kRedStride + 8 * c + 4 + k] = o[3] * fb;
+              }
+            }
+          }
+          consumer_sync();
+#pragma unroll
+          for (int q2 = 0; q2 < RT; ++q2) {
+            const int r = q2 * 16 + (threadIdx.x >> 4), col = (threadIdx.x & 15) * 2;
+            if (r >= rows) continue;
+            float x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+              const float2 v = *reinterpret_cast<const float2*>(
+                  red + ((t * RT + q2) * 16 + (threadIdx.x >> 4)) * kRedStride + col);
+              x += v.x;
+              y += v.y;
+            }
+            if (final) {
+              const float f = fin[r].x;
+              const int64_t row = tok0 + (row0 + r) / a.group;
+              const int h = head * a.group + (row0 + r) % a.group;
+              uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
+                              ch * 32 + col;
+              *reinterpret_cast<uint32_t*>(out) = a.q_type == MM3IDX_TYPE_BF16
+                                                      ? pack2<true>(x * f, y * f)
+                                                      : pack2<false>(x * f, y * f);
+            } else {
+              __stcg(reinterpret_cast<float2*>(
+                         a.part_o + (static_cast<int64_t>(slot_id) * 64 + r) * D + ch * 32 + col),
+                     make_float2(x, y));
+            }
+          }
+          consumer_sync();
+        }
+        if (final) break;
+        // Publish; the last CTA of the task goes on with the partial results.
+        __threadfence();
+        consumer_sync();
+        if (threadIdx.x == 0) {
+          int last = 0;
+          if (!dead) {
+            const unsigned wrap = last_cta - first_cta;
+            last = atomicInc(a.tickets + sg.task, wrap) == wrap;
+            __threadfence();
+          }
+          misc->last = last;
+        }
+        consumer_sync();
+        if (!misc->last) break;
+        final = true;
+        st.m0 = st.m1 = -INFINITY;
+        st.l0 = st.l1 = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.o[n][e] = 0.0f;
+        const int rla = rt * 16 + g, rlb = rla + 8;
+        for (int t = first_cta + tg; t <= last_cta; t += TG) {
+          const long long share_lo = misc->total * t / misc->grid;
+          const int64_t from = 2 * t + (sg.pos > share_lo ? 1 : 0);
+          const float2 none = make_float2(-INFINITY, 0.0f);
+          const float2 xa = rla < rows ? __ldcg(a.part_ml + from * 64 + rla) : none;
+          const float2 xb = rlb < rows ? __ldcg(a.part_ml + from * 64 + rlb) : none;
+          const float na = fmaxf(st.m0, xa.x), nb = fmaxf(st.m1, xb.x);
+          const float ga = na == -INFINITY ? 0.0f : ex2(st.m0 - na);
+          const float gb = nb == -INFINITY ? 0.0f : ex2(st.m1 - nb);
+          const float ha = na == -INFINITY ? 0.0f : ex2(xa.x - na);
+          const float hb = nb == -INFINITY ? 0.0f : ex2(xb.x - nb);
+          st.m0 = na;
+          st.m1 = nb;
+          // one thread of a quad carries l: the quad sum is already done
+          st.l0 = st.l0 * ga + xa.y * ha;
+          st.l1 = st.l1 * gb + xb.y * hb;
+          const float* pa = a.part_o + (from * 64 + rla) * D;
+          const float* pb2 = a.part_o + (from * 64 + rlb) * D;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float2 va2 = make_float2(0.0f, 0.0f), vb2 = va2;
+            if constexpr (!kByte) {
+              if (rla < rows) va2 = __ldcg(reinterpret_cast<const float2*>(pa + n * 8 + 2 * c));
+              if (rlb < rows) vb2 = __ldcg(reinterpret_cast<const float2*>(pb2 + n * 8 + 2 * c));
+            } else {
+              const int d = (n >> 2) * 32 + 8 * c + (n & 3);
+              if (rla < rows) va2 = make_float2(__ldcg(pa + d), __ldcg(pa + d + 4));
+              if (rlb < rows) vb2 = make_float2(__ldcg(pb2 + d), __ldcg(pb2 + d + 4));
+            }
+            st.o[n][0] = st.o[n][0] * ga + va2.x * ha;
+            st.o[n][1] = st.o[n][1] * ga + va2.y * ha;
+            st.o[n][2] = st.o[n][2] * gb + vb2.x * hb;
+            st.o[n][3] = st.o[n][3] * gb + vb2.y * hb;
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && misc->abort) atomicOr(a.status, MM3IDX_DEV_TIMEOUT);
+}
+
+template <int KV, int D, int RT>
+cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
+                      int grid, cudaStream_t s) {
+  using C = Cfg<KV, D>;
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<KV, D, RT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_kernel<KV, D, RT>, kmap, vmap, a);
+}
+
+template <int KV, int D>
+cudaError_t launch_d(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
+                     int grid, cudaStream_t s) {
+  const int tiles = attention_row_tiles16(a.group * a.query_len);
+  if (tiles == 1) return launch_rt<KV, D, 1>(kmap, vmap, a, grid, s);
+  if (tiles == 2) return launch_rt<KV, D, 2>(kmap, vmap, a, grid, s);
+  return launch_rt<KV, D, 4>(kmap, vmap, a, grid, s);
+}
+
+template <int KV>
+cudaError_t launch_kv(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
+                      int grid, cudaStream_t s) {
+  return a.head_dim == 128 ? launch_d<KV, 128>(kmap, vmap, a, grid, s)
+                           : launch_d<KV, 64>(kmap, vmap, a, grid, s);
+}
+
+}  // namespace attn
+}  // namespace mm3idx

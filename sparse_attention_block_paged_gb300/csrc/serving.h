@@ -27,10 +27,8 @@ struct AttentionArgs {
   int32_t group;              // query heads per kv head
   int32_t head_dim;
   int32_t q_type, kv_type;    // MM3IDX_TYPE_*
-  const void* k;
-  const void* v;
-  int64_t k_page, k_tok, k_head;
-  int64_t v_page, v_tok, v_head;
+  int32_t row_tiles;          // 64-row tiles of a kv head's group * query_len rows
+  int32_t tasks;              // kv_heads * row_tiles, of a request
   int32_t num_pages;
   int32_t page_shift;         // log2 of the page's tokens
   const int32_t* table;
@@ -46,9 +44,17 @@ struct AttentionArgs {
   float* weights;             // [rows, w_stride] fp32, may be null
   int64_t w_stride;
   int32_t w_width;            // cdiv(max_seq_len, 128)
-  float* lse_ws;              // [rows, q heads] log-sum-exp, for the weights
+  // workspace
+  unsigned int* tickets;      // [num_reqs * tasks], 0 between calls
+  float2* part_ml;            // [2 * grid][64]: reference and sum of a CTA's share of a task
+  float* part_o;              // [2 * grid][64][head_dim]
+  float* row_lse;             // with weights: [rows, q heads], base 2
+  float* tile_lse;            // with weights: [num_reqs * tasks][w_width][rows of the kernel], base 2
   int32_t* status;
 };
+
+// 16-row tiles that the kernel works on at a time: 1, 2 or 4.
+inline int attention_row_tiles16(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 struct WeightArgs {
   float* acc;
@@ -103,7 +109,14 @@ struct DraftArgs {
   int32_t* status;
 };
 
-cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_attention(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_fp16(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_e4m3(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const AttentionArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_accumulate(const WeightArgs& a, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const DraftArgs& a, int sms, cudaStream_t s);
