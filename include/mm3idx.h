@@ -400,7 +400,7 @@ int mm3idx_forward_workspace_bytes(int32_t heads, int32_t num_decodes, int32_t d
 #define MM3IDX_ERR_ATTENTION_SHAPE  (-13) /* heads, head_dim, page size or element types not served */
 #define MM3IDX_ERR_ATTENTION_LAYOUT (-14) /* q, k, v, out, lse or weights misaligned, or their strides too small */
 #define MM3IDX_ERR_BUDGET           (-15) /* budget < init + local, local < 1, init < 0 or a decay outside [0, 1] */
-#define MM3IDX_ERR_VOCAB            (-16) /* vocab < 1, draft count outside 0..MM3IDX_MAX_DRAFTS or overlapping rows */
+#define MM3IDX_ERR_VOCAB            (-16) /* vocab outside 1..2^30, draft count outside 0..MM3IDX_MAX_DRAFTS or overlapping rows */
 
 #define MM3IDX_MAX_DRAFTS 31           /* most drafted tokens a request has     */
 #define MM3IDX_MAX_WEIGHT_ENTRIES 1024 /* query_len * topk limit of mm3idx_weights_t */
@@ -568,7 +568,7 @@ typedef struct mm3idx_drafts {
     int64_t        uniforms_stride;/* >= drafts + 1                                         */
     int32_t        num_reqs;
     int32_t        drafts;         /* 0..MM3IDX_MAX_DRAFTS                                  */
-    int32_t        vocab;          /* >= 1                                                  */
+    int32_t        vocab;          /* 1..2^30                                               */
     int32_t       *out;            /* int32 [num_reqs, out_stride]: the accepted drafts, the drawn token, -1 */
     int64_t        out_stride;     /* >= drafts + 1                                         */
     int32_t       *accepted;       /* int32 [num_reqs]                                      */
@@ -581,10 +581,10 @@ typedef struct mm3idx_drafts {
  * token is drawn from max(p_j - q_j, 0), or from p_j where that is zero
  * throughout; when all draft_lens[i] are accepted, from p at that row.  The
  * draw is the smallest token whose cumulative weight exceeds u * total.
- * Weights are summed as 64-bit integers in units of 2^-52 (probabilities are
- * clamped to 0..1 and NaN counts as 0, so every fp32 value from 2^-29 on is
+ * Weights are summed as 64-bit integers in units of 2^-46 (probabilities are
+ * clamped to 0..1, NaN counts as 0, and every fp32 value from 2^-23 on is
  * exact), which makes the token independent of the order of the sum.  A row
- * without any weight gives token vocab - 1.  A row must sum to less than 2048.
+ * without any weight gives token vocab - 1.  A row must sum to less than 2^17.
  */
 int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
 

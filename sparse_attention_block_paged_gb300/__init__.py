@@ -32,6 +32,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -205,6 +206,26 @@ class Drafts(ctypes.Structure):
     ]
 
 
+def _image(cls):
+    """The packer of a structure's image from its fields' values in order (a
+    call that fills a ctypes structure field by field takes several times as
+    long).  0 stands for a null pointer."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i",
+             ctypes.c_float: "f", ctypes.c_double: "d"}
+    form = "@"
+    for _, kind in cls._fields_:
+        if kind in codes:
+            form += codes[kind]
+        else:                                   # an array of structures of 8-byte fields
+            form += "".join(codes[k] for _, k in kind._type_._fields_) * kind._length_
+    packer = struct.Struct(form + "0q")
+    assert packer.size == ctypes.sizeof(cls), cls.__name__
+    return packer.pack
+
+
+_attention_image, _weights_image = _image(Attention), _image(Weights)
+_eviction_image, _drafts_image = _image(EvictionArgs), _image(Drafts)
+
 SYMBOLS = {
     "mm3idx_version": (ctypes.c_int32, []),
     "mm3idx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -263,14 +284,14 @@ SYMBOLS = {
     "mm3idx_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
-    "mm3idx_paged_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.c_void_p,
-                                              ctypes.c_size_t, ctypes.c_void_p]),
+    # the structures of these go as images (bytes) or by reference
+    "mm3idx_paged_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
     "mm3idx_attention_workspace_bytes": (ctypes.c_int, [ctypes.c_int32] * 7 +
                                          [ctypes.POINTER(ctypes.c_size_t)]),
-    "mm3idx_accumulate_weights": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.c_void_p]),
-    "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.POINTER(EvictionArgs),
-                                           ctypes.c_void_p]),
-    "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Drafts), ctypes.c_void_p]),
+    "mm3idx_accumulate_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
 }
 
 
@@ -304,29 +325,32 @@ def _stream(device, stream=None):
     """The stream a call launches on: `stream`, which must belong to the
     inputs' GPU, else that GPU's current stream."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(device.index)
     _need(torch.device(stream.device) == torch.device(device),
           "stream must belong to the inputs' GPU")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
+# the handle of a GPU's current stream (an object of torch.cuda.Stream made
+# for it costs 2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _HERE = contextlib.nullcontext()
 
 
 def _on(device):
     """Make the inputs' GPU current for a library call: the library takes the
     SM count, its status word and its static scratch from the current device."""
-    if torch.device(device).index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         return _HERE
     return torch.cuda.device(device)
 
 
 def _ws(workspace, device):
     """(pointer, bytes) of a caller-provided workspace on the inputs' GPU."""
-    _need(isinstance(workspace, torch.Tensor) and workspace.device == torch.device(device)
+    _need(isinstance(workspace, torch.Tensor) and workspace.device == device
           and workspace.is_contiguous(),
           "workspace must be a contiguous tensor on the inputs' GPU")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _cdiv(a, b):
@@ -775,111 +799,123 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max
     Over selected blocks: ``page_table``, ``seq_lens`` = the sparse table and
     context lengths of :func:`decode_sparse_table`, ``query_len=1`` and
     ``max_seq_len = 128 * topk``."""
-    _need(q.ndim == 3 and q.dtype in (torch.bfloat16, torch.float16) and q.stride(2) == 1,
-          "queries must be bf16 or fp16 [tokens, heads, head_dim] with contiguous head_dim")
-    _need(k_cache.ndim == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
-          and k_cache.stride(3) == 1 and v_cache.stride(3) == 1
-          and k_cache.shape[3] == q.shape[2]
-          and k_cache.dtype in (q.dtype, torch.float8_e4m3fn),
-          "caches must be [pages, page_size, kv_heads, head_dim] with contiguous head_dim, "
-          "of the queries' type or float8_e4m3fn")
-    _need(page_table.ndim == 2 and page_table.dtype == torch.int32
-          and (page_table.stride(1) == 1 or page_table.shape[1] <= 1)
-          and seq_lens.ndim == 1 and seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(),
-          "page table and lengths must be int32 with unit stride")
-    dev = q.device
-    _on_gpu(q, k_cache, v_cache, page_table, seq_lens)
+    # Each property is read once and the structure packed in one go: the call
+    # itself takes as long as a small batch's kernel.
+    dtype, dev = q.dtype, q.device
+    if not (q.ndim == 3 and (dtype is torch.bfloat16 or dtype is torch.float16)
+            and q.stride(2) == 1):
+        raise ValueError("queries must be bf16 or fp16 [tokens, heads, head_dim] with contiguous "
+                         "head_dim")
     rows, heads, dim = q.shape
+    kv = k_cache.dtype
+    if not (k_cache.ndim == 4 and k_cache.shape == v_cache.shape and kv is v_cache.dtype
+            and (kv is dtype or kv is torch.float8_e4m3fn) and k_cache.shape[3] == dim):
+        raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] with contiguous "
+                         "head_dim, of the queries' type or float8_e4m3fn")
     pages, size, kv_heads, _ = k_cache.shape
+    kp, kt, kh, kd = k_cache.stride()
+    vp, vt, vh, vd = v_cache.stride()
+    if kd != 1 or vd != 1:
+        raise ValueError("caches must have contiguous head_dim")
+    if not (page_table.ndim == 2 and page_table.dtype is torch.int32 and seq_lens.ndim == 1
+            and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()):
+        raise ValueError("page table and lengths must be int32 with unit stride")
+    table_rows, width = page_table.shape
+    table_stride, one = page_table.stride()
+    if one != 1 and width > 1:
+        raise ValueError("page table and lengths must be int32 with unit stride")
+    if not (q.is_cuda and k_cache.device == dev and v_cache.device == dev
+            and page_table.device == dev and seq_lens.device == dev):
+        raise ValueError("all inputs must be on the same GPU")
     reqs = seq_lens.shape[0]
-    _need(rows == reqs * query_len and page_table.shape[0] == reqs,
-          "queries must have batch * query_len rows and the page table one row per request")
+    if rows != reqs * query_len or table_rows != reqs:
+        raise ValueError("queries must have batch * query_len rows and the page table one row per "
+                         "request")
     if out is None:
         with _allocating_on(stream):
-            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev
-          and out.stride(2) == 1, "out must be like the queries")
-    a = Attention()
-    a.q, a.out = q.data_ptr(), out.data_ptr()
-    a.q_token_stride = q.stride(0) if rows > 1 else heads * dim
-    a.q_head_stride = q.stride(1) if heads > 1 else dim
-    a.out_token_stride = out.stride(0) if rows > 1 else heads * dim
-    a.out_head_stride = out.stride(1) if heads > 1 else dim
-    a.q_heads, a.kv_heads, a.head_dim = heads, kv_heads, dim
-    a.q_type, a.kv_type = TYPES[q.dtype], TYPES[k_cache.dtype]
-    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    sp, st, sh, _ = k_cache.stride()
-    a.k_page_stride = sp if pages > 1 else size * kv_heads * dim
-    a.k_token_stride, a.k_head_stride = st, sh if kv_heads > 1 else dim
-    sp, st, sh, _ = v_cache.stride()
-    a.v_page_stride = sp if pages > 1 else size * kv_heads * dim
-    a.v_token_stride, a.v_head_stride = st, sh if kv_heads > 1 else dim
-    a.k_scale, a.v_scale, a.sm_scale = k_scale, v_scale, sm_scale
-    a.num_pages, a.page_size = pages, size
-    a.page_table, a.table_stride = page_table.data_ptr(), _row_stride(page_table)
-    a.table_width = page_table.shape[1]
-    a.seq_lens, a.num_reqs = seq_lens.data_ptr(), reqs
-    a.query_len, a.max_seq_len = query_len, max_seq_len
+            out = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
+    elif not (out.shape == q.shape and out.dtype is dtype and out.device == dev):
+        raise ValueError("out must be like the queries")
+    qt, qh, _ = q.stride()
+    ot, oh, od = out.stride()
+    if od != 1:
+        raise ValueError("out must be like the queries")
+    if rows <= 1:                               # strides of dimensions of one are free
+        qt = ot = heads * dim
+    if heads <= 1:
+        qh = oh = dim
+    if pages <= 1:
+        kp = vp = size * kv_heads * dim
+    if kv_heads <= 1:
+        kh = vh = dim
+    lse_at = lse_stride = weights_at = weights_stride = 0
     if lse is not None:
         _need(lse.dtype == torch.float32 and lse.ndim == 2 and lse.shape[0] >= rows
               and lse.shape[1] == heads and (lse.stride(1) == 1 or heads == 1)
               and lse.device == dev,
               "lse must be fp32 [>= rows, heads] with unit inner stride")
-        a.lse, a.lse_token_stride = lse.data_ptr(), _row_stride(lse)
+        lse_at, lse_stride = lse.data_ptr(), _row_stride(lse)
     if block_weights is not None:
-        width = _cdiv(max_seq_len, 128)
         _need(block_weights.dtype == torch.float32 and block_weights.ndim == 2
-              and block_weights.shape[0] >= rows and block_weights.shape[1] >= width
+              and block_weights.shape[0] >= rows
+              and block_weights.shape[1] >= _cdiv(max_seq_len, 128)
               and (block_weights.stride(1) == 1 or block_weights.shape[1] == 1)
               and block_weights.device == dev,
               "block_weights must be fp32 [>= rows, >= cdiv(max_seq_len, 128)] with unit inner "
               "stride")
-        a.block_weights, a.block_weights_stride = (block_weights.data_ptr(),
-                                                   _row_stride(block_weights))
+        weights_at, weights_stride = block_weights.data_ptr(), _row_stride(block_weights)
+    image = _attention_image(
+        q.data_ptr(), qt, qh, heads, kv_heads, dim, TYPES[dtype], TYPES[kv],
+        k_cache.data_ptr(), kp, kt, kh, v_cache.data_ptr(), vp, vt, vh, k_scale, v_scale,
+        pages, size, page_table.data_ptr(), table_stride if reqs > 1 else max(width, 1), width,
+        seq_lens.data_ptr(), reqs, query_len, max_seq_len, sm_scale, out.data_ptr(), ot, oh,
+        lse_at, lse_stride, weights_at, weights_stride)
     if workspace is None:
         with _allocating_on(stream):
             workspace = new_attention_workspace(heads, kv_heads, dim, reqs, query_len, max_seq_len,
                                                 block_weights is not None, dev)
     wp, wn = _ws(workspace, dev)
     with _on(dev):
-        _check(lib.mm3idx_paged_attention(ctypes.byref(a), wp, wn, _stream(dev, stream)),
+        _check(lib.mm3idx_paged_attention(image, wp, wn, _stream(dev, stream)),
                "mm3idx_paged_attention")
     return out
 
 
 def _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay):
-    width = _cdiv(max_seq_len, 128)
+    """The checks and the image of mm3idx_weights_t."""
+    width, dev = _cdiv(max_seq_len, 128), acc.device
+    if not (seq_lens.ndim == 1 and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()):
+        raise ValueError("lengths must be contiguous int32")
     reqs = seq_lens.shape[0]
-    _need(seq_lens.ndim == 1 and seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(),
-          "lengths must be contiguous int32")
-    _need(acc.dtype == torch.float32 and acc.ndim == 2 and acc.shape[0] == reqs
-          and acc.shape[1] >= width and (acc.stride(1) == 1 or acc.shape[1] == 1),
-          "weights must be fp32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit inner stride")
-    _on_gpu(acc, seq_lens)
-    w = Weights()
-    w.acc, w.acc_stride = acc.data_ptr(), _row_stride(acc)
-    w.seq_lens, w.num_reqs = seq_lens.data_ptr(), reqs
-    w.query_len, w.max_seq_len, w.decay = query_len, max_seq_len, decay
+    if not (acc.dtype is torch.float32 and acc.ndim == 2 and acc.shape[0] == reqs
+            and acc.shape[1] >= width and (acc.stride(1) == 1 or acc.shape[1] == 1)):
+        raise ValueError("weights must be fp32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit "
+                         "inner stride")
+    if not (acc.is_cuda and seq_lens.device == dev):
+        raise ValueError("all inputs must be on the same GPU")
+    w_at = w_stride = ids_at = ids_stride = topk = 0
     if block_weights is not None:
-        _need(block_weights.dtype == torch.float32 and block_weights.ndim == 2
-              and block_weights.shape[0] >= reqs * query_len
-              and (block_weights.stride(1) == 1 or block_weights.shape[1] == 1)
-              and block_weights.device == acc.device,
-              "block_weights must be fp32 [>= num_reqs * query_len, columns] with unit inner "
-              "stride")
-        w.block_weights, w.weights_stride = block_weights.data_ptr(), _row_stride(block_weights)
-        _need(block_weights.shape[1] >= (width if ids is None else ids.shape[-1]),
-              "block_weights must have a column per block, or per id")
-    _need(ids is None or block_weights is not None, "ids need block_weights")
+        rows, columns = block_weights.shape
+        if not (block_weights.dtype is torch.float32 and rows >= reqs * query_len
+                and (columns == 1 or block_weights.stride(1) == 1)
+                and block_weights.device == dev
+                and columns >= (width if ids is None else ids.shape[-1])):
+            raise ValueError("block_weights must be fp32 [>= num_reqs * query_len, a column per "
+                             "block or id] with unit inner stride")
+        w_at, w_stride = block_weights.data_ptr(), _row_stride(block_weights)
     if ids is not None:
         if ids.ndim == 3:                       # the ids of one index head, as decode returns them
             _need(ids.shape[0] == 1, "ids must be those of one index head")
             ids = ids[0]
-        _need(ids.dtype == torch.int32 and ids.ndim == 2 and ids.shape[0] >= reqs * query_len
-              and (ids.stride(1) == 1 or ids.shape[1] == 1) and ids.device == acc.device,
-              "ids must be int32 [>= num_reqs * query_len, topk] with unit inner stride")
-        w.ids, w.ids_stride, w.topk = ids.data_ptr(), _row_stride(ids), ids.shape[1]
-    return w
+        rows, topk = ids.shape
+        if not (block_weights is not None and ids.dtype is torch.int32
+                and rows >= reqs * query_len and (topk == 1 or ids.stride(1) == 1)
+                and ids.device == dev):
+            raise ValueError("ids must be int32 [>= num_reqs * query_len, topk] with unit inner "
+                             "stride, with their block_weights")
+        ids_at, ids_stride = ids.data_ptr(), _row_stride(ids)
+    return _weights_image(acc.data_ptr(), _row_stride(acc), w_at, w_stride, ids_at, ids_stride,
+                          topk, seq_lens.data_ptr(), reqs, query_len, max_seq_len, decay)
 
 
 def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, ids=None,
@@ -890,7 +926,7 @@ def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, 
     [rows, topk] or [1, rows, topk], -1: none) column k is block ids[row, k]."""
     w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
     with _on(acc.device):
-        _check(lib.mm3idx_accumulate_weights(ctypes.byref(w), _stream(acc.device, stream)),
+        _check(lib.mm3idx_accumulate_weights(w, _stream(acc.device, stream)),
                "mm3idx_accumulate_weights")
     return acc
 
@@ -922,33 +958,37 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
     Eviction of the same shapes to write into."""
     w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
     dev, reqs, width = acc.device, seq_lens.shape[0], _cdiv(max_seq_len, 128)
-    given = (block_table, attention_block_table)
-    for t in given:
-        _need(t is None or (t.dtype == torch.int32 and t.ndim == 2 and t.shape[0] == reqs
-                            and t.shape[1] >= width and (t.stride(1) == 1 or t.shape[1] == 1)
-                            and t.device == dev),
-              "block tables must be int32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit inner "
-              "stride, on the weights' GPU")
-    _need(block_table is not None, "a block table is needed")
-    _need(budget >= 1, "budget must be at least 1")
+    second = attention_block_table
+    for t in (block_table,) if second is None else (block_table, second):
+        if not (t.dtype is torch.int32 and t.ndim == 2 and t.shape[0] == reqs
+                and t.shape[1] >= width and (t.shape[1] == 1 or t.stride(1) == 1)
+                and t.device == dev):
+            raise ValueError("block tables must be int32 [num_reqs, >= cdiv(max_seq_len, 128)] "
+                             "with unit inner stride, on the weights' GPU")
+        if in_place and t.shape[1] < budget:
+            raise ValueError("in-place tables must have at least budget columns")
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
     gone = max(1, width - budget)
     if out is None:
         with _allocating_on(stream):
-            def ints(columns):
-                return torch.empty((reqs, columns), dtype=torch.int32, device=dev)
-
-            _need(not in_place or all(t is None or t.shape[1] >= budget for t in given),
-                  "in-place tables must have at least budget columns")
-            second = attention_block_table is not None
-            out = Eviction(
-                ints(budget), seq_lens if in_place else torch.empty_like(seq_lens),
-                acc if in_place else torch.empty((reqs, width), dtype=torch.float32, device=dev),
-                block_table if in_place else ints(budget), ints(gone),
-                (attention_block_table if in_place else ints(budget)) if second else None,
-                ints(gone) if second else None)
+            # one buffer, a range of columns each
+            sizes = [budget, gone] if in_place else [budget, gone, budget]
+            if second is not None:
+                sizes += [gone] if in_place else [gone, budget]
+            parts = torch.empty((reqs, sum(sizes)), dtype=torch.int32, device=dev).split(sizes, 1)
+            if in_place:
+                out = Eviction(parts[0], seq_lens, acc, block_table, parts[1], second,
+                               None if second is None else parts[2])
+            else:
+                out = Eviction(parts[0], torch.empty_like(seq_lens),
+                               torch.empty((reqs, width), dtype=torch.float32, device=dev),
+                               parts[2], parts[1],
+                               *(() if second is None else (parts[4], parts[3])))
     else:
         _need(not in_place, "out and in_place exclude each other")
-        _need((out.attention_block_table is None) == (attention_block_table is None)
+        _need((out.attention_block_table is None) == (out.attention_freed is None)
+              == (second is None)
               and out.weights.dtype == torch.float32 and out.weights.shape[1] >= width
               and out.seq_lens.dtype == torch.int32 and out.seq_lens.shape == seq_lens.shape
               and out.seq_lens.is_contiguous()
@@ -959,23 +999,19 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
                   (out.ids, budget), (out.block_table, budget), (out.freed, gone),
                   (out.attention_block_table, budget), (out.attention_freed, gone))),
               "out must be an Eviction of these shapes")
-    e = EvictionArgs()
-    e.budget, e.init_blocks, e.local_blocks = budget, init_blocks, local_blocks
-    e.ids, e.ids_stride = out.ids.data_ptr(), _row_stride(out.ids)
-    e.acc_out, e.acc_out_stride = out.weights.data_ptr(), _row_stride(out.weights)
-    e.seq_lens_out = out.seq_lens.data_ptr()
-    tables = ((block_table, out.block_table, out.freed),
-              (attention_block_table, out.attention_block_table, out.attention_freed))
-    for k, (old, new, freed) in enumerate(tables):
-        if old is None:
-            continue
-        t = e.tables[k]
-        t.in_, t.in_stride = old.data_ptr(), _row_stride(old)
-        t.out, t.out_stride = new.data_ptr(), _row_stride(new)
-        t.freed, t.freed_stride = freed.data_ptr(), _row_stride(freed)
+
+    def table(old, new, freed):
+        return (old.data_ptr(), _row_stride(old), new.data_ptr(), _row_stride(new),
+                freed.data_ptr(), _row_stride(freed))
+
+    e = _eviction_image(
+        budget, init_blocks, local_blocks, *table(block_table, out.block_table, out.freed),
+        *((0,) * 6 if second is None else
+          table(second, out.attention_block_table, out.attention_freed)),
+        out.ids.data_ptr(), _row_stride(out.ids), out.weights.data_ptr(),
+        _row_stride(out.weights), out.seq_lens.data_ptr())
     with _on(dev):
-        _check(lib.mm3idx_evict_blocks(ctypes.byref(w), ctypes.byref(e), _stream(dev, stream)),
-               "mm3idx_evict_blocks")
+        _check(lib.mm3idx_evict_blocks(w, e, _stream(dev, stream)), "mm3idx_evict_blocks")
     return out
 
 
@@ -992,55 +1028,57 @@ def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, dra
     [num_reqs, drafts + 1]; draft_lens int32 [num_reqs] when requests have
     fewer.  Returns (tokens int32 [num_reqs, drafts + 1]: the accepted drafts,
     the drawn token, then -1; the number accepted, int32 [num_reqs])."""
-    _need(target_probs.ndim == 3 and (target_probs.stride(2) == 1 or target_probs.shape[2] == 1)
-          and target_probs.dtype in (torch.float32, torch.bfloat16, torch.float16),
-          "target_probs must be fp32, bf16 or fp16 [num_reqs, drafts + 1, vocab] with contiguous "
-          "vocab")
+    dtype, dev = target_probs.dtype, target_probs.device
+    if not (target_probs.ndim == 3 and (dtype is torch.float32 or dtype is torch.bfloat16
+                                        or dtype is torch.float16)):
+        raise ValueError("target_probs must be fp32, bf16 or fp16 [num_reqs, drafts + 1, vocab]")
     reqs, rows, vocab = target_probs.shape
+    tr, tt, one = target_probs.stride()
+    if (one != 1 and vocab != 1) or rows < 1:
+        raise ValueError("target_probs must have drafts + 1 rows of contiguous vocab")
     k = rows - 1
-    _need(k >= 0, "target_probs must have drafts + 1 rows")
-    dev = target_probs.device
-    _need(draft_tokens.dtype == torch.int32 and tuple(draft_tokens.shape) == (reqs, k)
-          and (k <= 1 or draft_tokens.stride(1) == 1),
-          "draft_tokens must be int32 [num_reqs, drafts] with unit inner stride")
-    _need(uniforms.dtype == torch.float32 and tuple(uniforms.shape) == (reqs, rows)
-          and (k == 0 or uniforms.stride(1) == 1),
-          "uniforms must be fp32 [num_reqs, drafts + 1] with unit inner stride")
-    _need(draft_probs is None or (draft_probs.dtype == target_probs.dtype
-                                  and tuple(draft_probs.shape) == (reqs, k, vocab)
-                                  and (draft_probs.stride(2) == 1 or vocab == 1)),
-          "draft_probs must be [num_reqs, drafts, vocab] of target_probs' type")
-    _need(draft_lens is None or (draft_lens.dtype == torch.int32 and draft_lens.is_contiguous()
-                                 and tuple(draft_lens.shape) == (reqs,)),
-          "draft_lens must be contiguous int32 [num_reqs]")
-    _on_gpu(target_probs, draft_tokens, uniforms,
-            *(t for t in (draft_probs, draft_lens, out, accepted) if t is not None))
+    if not (draft_tokens.dtype is torch.int32 and draft_tokens.shape == (reqs, k)
+            and (k <= 1 or draft_tokens.stride(1) == 1)):
+        raise ValueError("draft_tokens must be int32 [num_reqs, drafts] with unit inner stride")
+    if not (uniforms.dtype is torch.float32 and uniforms.shape == (reqs, rows)
+            and (k == 0 or uniforms.stride(1) == 1)):
+        raise ValueError("uniforms must be fp32 [num_reqs, drafts + 1] with unit inner stride")
+    draft_at = dr = dt = 0
+    if draft_probs is not None:
+        if not (draft_probs.dtype is dtype and draft_probs.shape == (reqs, k, vocab)):
+            raise ValueError("draft_probs must be [num_reqs, drafts, vocab] of target_probs' type")
+        dr, dt, one = draft_probs.stride()
+        if one != 1 and vocab != 1:
+            raise ValueError("draft_probs must have contiguous vocab")
+        draft_at = draft_probs.data_ptr()
+    lens_at = 0
+    if draft_lens is not None:
+        if not (draft_lens.dtype is torch.int32 and draft_lens.is_contiguous()
+                and draft_lens.shape == (reqs,)):
+            raise ValueError("draft_lens must be contiguous int32 [num_reqs]")
+        lens_at = draft_lens.data_ptr()
+    if not (target_probs.is_cuda and draft_tokens.device == dev and uniforms.device == dev
+            and (draft_probs is None or draft_probs.device == dev)
+            and (draft_lens is None or draft_lens.device == dev)):
+        raise ValueError("all inputs must be on the same GPU")
     if out is None or accepted is None:
         with _allocating_on(stream):
             if out is None:
                 out = torch.empty((reqs, rows), dtype=torch.int32, device=dev)
             if accepted is None:
                 accepted = torch.empty((reqs,), dtype=torch.int32, device=dev)
-    _need(out.dtype == torch.int32 and tuple(out.shape) == (reqs, rows)
-          and (k == 0 or out.stride(1) == 1) and accepted.dtype == torch.int32
-          and tuple(accepted.shape) == (reqs,) and accepted.is_contiguous(),
-          "out must be int32 [num_reqs, drafts + 1] with unit inner stride, accepted int32 "
-          "[num_reqs]")
-    d = Drafts()
-    d.target, d.type = target_probs.data_ptr(), TYPES[target_probs.dtype]
-    d.target_req_stride, d.target_row_stride = target_probs.stride(0), target_probs.stride(1)
-    if draft_probs is not None:
-        d.draft = draft_probs.data_ptr()
-        d.draft_req_stride, d.draft_row_stride = draft_probs.stride(0), draft_probs.stride(1)
-    d.tokens, d.tokens_stride = draft_tokens.data_ptr(), _row_stride(draft_tokens)
-    if draft_lens is not None:
-        d.draft_lens = draft_lens.data_ptr()
-    d.uniforms, d.uniforms_stride = uniforms.data_ptr(), _row_stride(uniforms)
-    d.num_reqs, d.drafts, d.vocab = reqs, k, vocab
-    d.out, d.out_stride, d.accepted = out.data_ptr(), _row_stride(out), accepted.data_ptr()
+    if not (out.dtype is torch.int32 and out.shape == (reqs, rows) and out.device == dev
+            and (k == 0 or out.stride(1) == 1) and accepted.dtype is torch.int32
+            and accepted.shape == (reqs,) and accepted.is_contiguous()
+            and accepted.device == dev):
+        raise ValueError("out must be int32 [num_reqs, drafts + 1] with unit inner stride, "
+                         "accepted int32 [num_reqs]")
+    image = _drafts_image(
+        target_probs.data_ptr(), tr, tt, draft_at, dr, dt, TYPES[dtype], draft_tokens.data_ptr(),
+        _row_stride(draft_tokens), lens_at, uniforms.data_ptr(), _row_stride(uniforms), reqs, k,
+        vocab, out.data_ptr(), _row_stride(out), accepted.data_ptr())
     with _on(dev):
-        _check(lib.mm3idx_verify_drafts(ctypes.byref(d), _stream(dev, stream)),
-               "mm3idx_verify_drafts")
+        _check(lib.mm3idx_verify_drafts(image, _stream(dev, stream)), "mm3idx_verify_drafts")
     return out, accepted
 
 

@@ -292,7 +292,7 @@ int mm3idx_evict_blocks(const mm3idx_weights_t* w, const mm3idx_eviction_t* e, v
 
 int mm3idx_verify_drafts(const mm3idx_drafts_t* d, void* stream) {
   if (!d || d->num_reqs < 0) return MM3IDX_ERR_INVALID_ARGUMENT;
-  if (d->vocab < 1 || d->drafts < 0 || d->drafts > MM3IDX_MAX_DRAFTS) return MM3IDX_ERR_VOCAB;
+  if (d->vocab < 1 || d->vocab > (1 << 30) || d->drafts < 0 || d->drafts > MM3IDX_MAX_DRAFTS) return MM3IDX_ERR_VOCAB;
   if (d->type != MM3IDX_TYPE_FP32 && d->type != MM3IDX_TYPE_BF16 && d->type != MM3IDX_TYPE_FP16)
     return MM3IDX_ERR_INVALID_ARGUMENT;
   if (d->num_reqs == 0) return MM3IDX_OK;

@@ -1,11 +1,22 @@
 // verify.cu -- verification of drafted tokens against the target's
 // probabilities (include/mm3idx.h, mm3idx_verify_drafts).
 //
-// One CTA per request.  The accepted drafts need one probability of each row;
-// only the row of the first rejected draft (or the last row) is read whole,
-// twice: once for its total weight, once for the token whose cumulative
-// weight passes u * total.  Weights are 64-bit integers in units of 2^-52, so
-// sums are exact whatever their order.
+// Mathematics.  Draft j (token d) is accepted while u_j q_j(d) < p_j(d), both
+// products exact in fp64.  That needs one number of each row; only one row a
+// request is read whole: with w(v) = p(v), or max(p(v) - q(v), 0) at the first
+// rejected draft, the drawn token is the smallest v with
+// w(0) + .. + w(v) > floor(u W), W the row's total.  Weights are 64-bit integers
+// in units of 2^-46, so the sums are exact in any order and the token depends
+// on neither the split nor the card (fp32 sums of 10^5 terms would move it in
+// about 2 of 100 draws, and fp64 adds run at a fiftieth of the integer rate).
+//
+// What bounds it.  One pass over a row of p and one of q from HBM; for a few
+// requests the chain of dependent loads (lengths, tokens, probabilities, row,
+// token).  A cluster of CTAs takes a request, each a contiguous part of the
+// row, its warps chunks of it whose sums stay in shared memory; the CTAs
+// exchange their totals through distributed shared memory, and the one whose
+// part holds the point reads the one chunk again that holds it.  One launch, no
+// workspace, nothing read twice but that chunk.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -15,40 +26,129 @@
 namespace mm3idx {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 4;          // 16-byte loads of a lane and row in flight
+constexpr int kMaxChunks = 512;     // of a CTA's part
+constexpr int kMaxCluster = 16;
 
 template <int TYPE>
-__device__ __forceinline__ float prob_at(const void* p, int64_t i) {
-  if (TYPE == MM3IDX_TYPE_FP32) return __ldg(static_cast<const float*>(p) + i);
-  if (TYPE == MM3IDX_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+struct Elem {
+  static constexpr int kSize = TYPE == MM3IDX_TYPE_FP32 ? 4 : 2;
+  static constexpr int kPer = 16 / kSize;          // elements of a 16-byte load
+  static constexpr int kStep = 32 * kPer * kGroups;  // elements of a warp step
+};
+
+template <int TYPE>
+__device__ __forceinline__ float prob_at(const char* p, int64_t i) {
+  if constexpr (TYPE == MM3IDX_TYPE_FP32) return __ldg(reinterpret_cast<const float*>(p) + i);
+  const uint16_t x = __ldg(reinterpret_cast<const uint16_t*>(p) + i);
+  if constexpr (TYPE == MM3IDX_TYPE_BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
+  return __half2float(__ushort_as_half(x));
 }
 
-// A probability in units of 2^-52: clamped to 0..1, NaN as 0.
-__device__ __forceinline__ int64_t fixed(float p) {
-  p = fminf(fmaxf(p, 0.0f), 1.0f);   // fmaxf(NaN, 0) is 0
-  return __float2ll_rn(p * 4503599627370496.0f);
+// Element e of a 16-byte load.
+template <int TYPE>
+__device__ __forceinline__ float elem_of(const uint4& v, int e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (TYPE == MM3IDX_TYPE_FP32) return __uint_as_float(w[e]);
+  const uint32_t x = w[e >> 1];
+  if constexpr (TYPE == MM3IDX_TYPE_BF16) return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? x >> 16 : x & 0xffffu)));
 }
+
+// A probability (clamped to 0..1, NaN as 0) in units of 2^-46, as two whole
+// numbers: high 2^23 + low.  Adding 2^23 leaves a whole number in a float's
+// mantissa, so both are differences of float images; fp32 instructions run at
+// 128 a clock and SM where a conversion to 64 bits takes the slow pipe
+// (256 requests x 131072: 131 us with it).
+struct Limbs {
+  uint32_t high, low;
+};
+__device__ __forceinline__ Limbs limbs(float p) {
+  constexpr float kBase = 8388608.0f;                      // 2^23
+  p = __saturatef(p);
+  const float h = __fmaf_rz(p, kBase, kBase);
+  const float rest = __fmaf_rn(kBase - h, 1.0f / kBase, p);  // exact: p's bits below 2^-23
+  const float l = __fmaf_rn(rest, kBase * kBase, kBase);
+  return Limbs{__float_as_uint(h), __float_as_uint(l)};
+}
+constexpr uint32_t kZero = 0x4B000000u;                    // the image of 2^23
 
 // floor(u * total) for u in [0, 1) (clamped, NaN as 0).
-__device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
+__device__ __forceinline__ uint64_t point_of(float u, uint64_t total) {
   u = fminf(fmaxf(u, 0.0f), 0.99999994f);
   return __umul64hi(__float2ull_rz(u * 18446744073709551616.0f), total);
 }
 
-// What is left of the row at token v: p, or max(p - q, 0).
+// The weights of a row.  Elements are addressed by x = token + skew, so that
+// x a multiple of kPer is a 16-byte boundary of p, whatever the row's address.
 template <int TYPE>
 struct Row {
-  const void* p;
-  const void* q;     // null: nothing is taken off
+  using E = Elem<TYPE>;
+  const char* p;     // token 0
+  const char* q;     // null: nothing is taken off
   int without;       // a token whose weight is dropped, -1: none
-  __device__ __forceinline__ uint64_t weight(int v) const {
-    int64_t w = fixed(prob_at<TYPE>(p, v));
-    if (q) w = max(w - fixed(prob_at<TYPE>(q, v)), static_cast<int64_t>(0));
-    return v == without ? 0 : static_cast<uint64_t>(w);
+  int skew, end;     // tokens are x in [skew, end)
+  bool q_wide;       // q has its 16-byte boundaries where p has
+
+  __device__ __forceinline__ Row(const char* p_, const char* q_, int without_, int vocab)
+      : p(p_), q(q_), without(without_) {
+    skew = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / E::kSize;
+    end = skew + vocab;
+    q_wide = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+  }
+  // kPer elements from x (a multiple of kPer), 0 outside the row.
+  __device__ __forceinline__ uint4 load(const char* row, bool wide, int x) const {
+    const char* at = row + static_cast<int64_t>(x - skew) * E::kSize;
+    if (wide && x >= skew && x + E::kPer <= end) {
+      uint4 v;
+      asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+      return v;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < E::kPer; ++e) {
+      if (x + e < skew || x + e >= end) continue;
+      if constexpr (E::kSize == 4) w[e] = __ldg(reinterpret_cast<const uint32_t*>(at) + e);
+      else w[e >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(at) + e)) << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The weight of element e of the loads at x, added to two running sums (of
+  // no more than 2^8 elements: each limb is below 2^24).
+  __device__ __forceinline__ void add(const uint4& vp, const uint4& vq, int x, int e, int32_t& high,
+                                      int32_t& low) const {
+    const float fp = elem_of<TYPE>(vp, e);
+    const Limbs lp = limbs(fp);
+    Limbs lq{kZero, kZero};
+    bool counts = x + e - skew != without;
+    if (q) {
+      const float fq = elem_of<TYPE>(vq, e);
+      lq = limbs(fq);
+      counts = lp.high > lq.high || (lp.high == lq.high && lp.low > lq.low);
+    }
+    if (counts) {
+      high += static_cast<int32_t>(lp.high - lq.high);
+      low += static_cast<int32_t>(lp.low - lq.low);
+    }
+  }
+  // One warp's weights of a step (kGroups x 32 x kPer elements from x0).
+  __device__ __forceinline__ void load_step(int x0, uint4 (&vp)[kGroups], uint4 (&vq)[kGroups]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int x = x0 + (k * 32 + lane) * E::kPer;
+      vp[k] = load(p, true, x);
+      vq[k] = q ? load(q, q_wide, x) : make_uint4(0, 0, 0, 0);
+    }
   }
 };
+
+__device__ __forceinline__ uint64_t join(int32_t high, int32_t low) {
+  return static_cast<uint64_t>((static_cast<int64_t>(high) << 23) + low);
+}
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -56,104 +156,213 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// The row's weight from token v on to each warp's share: warp w has tokens
-// [w * share, (w + 1) * share).
-template <int TYPE>
-__device__ __forceinline__ uint64_t total_of(const Row<TYPE>& r, int vocab, int share,
-                                             uint64_t* sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int end = min(vocab, (warp + 1) * share);
-  uint64_t s = 0;
-  for (int v = warp * share + lane; v < end; v += 32) s += r.weight(v);
-  s = warp_sum(s);
-  __syncthreads();
-  if (lane == 0) sums[warp] = s;
-  __syncthreads();
-  uint64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) total += sums[w];
-  return total;
+__device__ __forceinline__ uint64_t warp_scan(uint64_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t remote_u64(const uint64_t* mine, int rank) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), there;
+  uint64_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(there) : "memory");
+  return v;
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const DraftArgs a) {
-  __shared__ uint64_t sums[kWarps];
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, int cluster) {
+  using E = Elem<TYPE>;
+  __shared__ uint64_t chunks[kMaxChunks];
+  __shared__ uint64_t totals[2];
   __shared__ int s_count;
-  const int i = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int len = a.lens ? min(max(a.lens[i], 0), a.drafts) : a.drafts;
-  constexpr int kSize = TYPE == MM3IDX_TYPE_FP32 ? 4 : 2;
-  const char* target = static_cast<const char*>(a.target) + i * a.t_req * kSize;
-  const char* draft = static_cast<const char*>(a.draft) + i * a.d_req * kSize;
+  const int rank = cluster_rank(), i = blockIdx.x / cluster;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const char* target = static_cast<const char*>(a.target) + i * a.t_req * E::kSize;
+  const char* draft = static_cast<const char*>(a.draft) + i * a.d_req * E::kSize;
+  const int32_t* tokens = a.tokens + i * a.tok_stride;
   if (warp == 0) {
+    const int len = a.lens ? min(max(__ldg(a.lens + i), 0), a.drafts) : a.drafts;
     bool ok = true;
-    if (lane < len) {
-      const int d = a.tokens[i * a.tok_stride + lane];
-      if (d < 0 || d >= a.vocab) {
-        atomicOr(a.status, MM3IDX_DEV_BAD_TOKEN);
-        ok = false;
-      } else {
-        const float p = prob_at<TYPE>(target, lane * a.t_row + d);
-        const float q = a.draft ? prob_at<TYPE>(draft, lane * a.d_row + d) : 1.0f;
-        ok = static_cast<double>(a.u[i * a.u_stride + lane]) * q < static_cast<double>(p);
+    if (lane < a.drafts) {              // loaded for all, judged up to len
+      const int d = __ldg(tokens + lane);
+      const float u = __ldg(a.u + i * a.u_stride + lane);
+      if (lane < len) {
+        if (d < 0 || d >= a.vocab) {
+          atomicOr(a.status, MM3IDX_DEV_BAD_TOKEN);
+          ok = false;
+        } else {
+          const float p = prob_at<TYPE>(target, lane * a.t_row + d);
+          const float q = a.draft ? prob_at<TYPE>(draft, lane * a.d_row + d) : 1.0f;
+          ok = static_cast<double>(u) * q < static_cast<double>(p);
+        }
       }
     }
     const unsigned no = __ballot_sync(0xffffffffu, !ok);
-    if (lane == 0) s_count = no ? __ffs(no) - 1 : len;
+    // the rejected draft, or minus 1 minus the length when all are accepted
+    if (lane == 0) s_count = no ? __ffs(no) - 1 : -1 - len;
   }
   __syncthreads();
-  const int count = s_count;
-  Row<TYPE> r{target + count * a.t_row * kSize, nullptr, -1};
-  if (count < len) {
-    if (a.draft) r.q = draft + count * a.d_row * kSize;
-    else r.without = a.tokens[i * a.tok_stride + count];
-  }
-  const int share = (a.vocab + kWarps - 1) / kWarps;
-  uint64_t total = total_of(r, a.vocab, share, sums);
-  if (total == 0 && count < len) {
-    r = Row<TYPE>{r.p, nullptr, -1};
-    total = total_of(r, a.vocab, share, sums);
-  }
-  // The warp whose share holds the point finds it.
-  const uint64_t x = target_of(a.u[i * a.u_stride + a.drafts], total);
-  uint64_t before = 0;
-  int owner = -1;
-  for (int w = 0; w < kWarps && owner < 0; ++w) {
-    if (before + sums[w] > x) owner = w;
-    else before += sums[w];
-  }
-  int32_t* out = a.out + i * a.out_stride;
-  if (threadIdx.x == 0) {
-    a.accepted[i] = count;
-    for (int j = 0; j < count; ++j) out[j] = a.tokens[i * a.tok_stride + j];
-    for (int j = count + 1; j <= a.drafts; ++j) out[j] = -1;
-    if (owner < 0) out[count] = a.vocab - 1;
-  }
-  if (warp != owner) return;
-  const int end = min(a.vocab, (warp + 1) * share);
-  for (int v0 = warp * share; v0 < end; v0 += 32) {
-    const int v = v0 + lane;
-    uint64_t incl = v < end ? r.weight(v) : 0;
+  const bool rejected = s_count >= 0;
+  const int count = rejected ? s_count : -1 - s_count;
+  const char* p = target + count * a.t_row * E::kSize;
+  const char* q = rejected && a.draft ? draft + count * a.d_row * E::kSize : nullptr;
+  const int without = rejected && !a.draft ? __ldg(tokens + count) : -1;
+  const float u = __ldg(a.u + i * a.u_stride + a.drafts);
+
+  for (int pass = 0;; ++pass) {
+    const Row<TYPE> r(p, pass ? nullptr : q, pass ? -1 : without, a.vocab);
+    // This CTA's part, in whole warp steps, and its chunks of whole steps.
+    const int steps = (r.end + E::kStep - 1) / E::kStep;
+    const int part = (steps + cluster - 1) / cluster;
+    const int s0 = min(rank * part, steps), s1 = min(s0 + part, steps);
+    const int per = (part + kMaxChunks - 1) / kMaxChunks;
+    const int n = (s1 - s0 + per - 1) / per;
+    for (int c = warp; c < n; c += kWarps) {
+      uint64_t sum = 0;   // unsigned: wraps as the signed low sums need
+      for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1); ++s) {
+        uint4 vp[kGroups], vq[kGroups];
+        r.load_step(s * E::kStep, vp, vq);
+        int32_t high = 0, low = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+        for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+          for (int e = 0; e < E::kPer; ++e)
+            r.add(vp[k], vq[k], s * E::kStep + (k * 32 + lane) * E::kPer, e, high, low);
+        sum += join(high, low);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) chunks[c] = sum;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > x);
-    if (hit) {
-      if (lane == 0) out[count] = v0 + __ffs(hit) - 1;
-      return;
+    __syncthreads();
+    // Chunk sums to sums up to and with each; the part's total to the others.
+    if (warp == 0) {
+      uint64_t before = 0;
+      for (int c0 = 0; c0 < n; c0 += 32) {
+        const uint64_t x = warp_scan(c0 + lane < n ? chunks[c0 + lane] : 0) + before;
+        if (c0 + lane < n) chunks[c0 + lane] = x;
+        before = __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) totals[pass] = before;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    // (every warp for itself: lane k asks rank k)
+    const uint64_t theirs = lane < cluster ? remote_u64(&totals[pass], lane) : 0;
+    const uint64_t upto = warp_scan(theirs);
+    const uint64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    if (total == 0 && rejected && pass == 0) continue;     // nothing left: the target's own row
+    const uint64_t mine = __shfl_sync(0xffffffffu, theirs, rank);
+    const uint64_t before = __shfl_sync(0xffffffffu, upto, rank) - mine;
+    const uint64_t x = point_of(u, total);
+    int32_t* out = a.out + i * a.out_stride;
+    if (rank == 0 && warp == 1) {
+      if (lane == 0) a.accepted[i] = count;
+      if (lane <= a.drafts && lane != count) out[lane] = lane < count ? __ldg(tokens + lane) : -1;
+      if (lane == 0 && total == 0) out[count] = a.vocab - 1;
+    }
+    if (warp == 0 && x >= before && x < before + mine) {
+      // The first chunk whose sum, with all before it, is above the point.
+      int c = 0;
+      uint64_t below = before;
+      for (int c0 = 0; c0 < n; c0 += 32) {
+        const uint64_t y = c0 + lane < n ? chunks[c0 + lane] : 0;
+        const unsigned hit = __ballot_sync(0xffffffffu, c0 + lane < n && before + y > x);
+        if (hit) {
+          c = c0 + __ffs(hit) - 1;
+          if (c > 0) below = before + chunks[c - 1];
+          break;
+        }
+      }
+      for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1); ++s) {
+        uint4 vp[kGroups], vq[kGroups];
+        r.load_step(s * E::kStep, vp, vq);
+        int found = -1;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          const int x0 = s * E::kStep + (k * 32 + lane) * E::kPer;
+          uint64_t w[E::kPer], own = 0;
+#pragma unroll
+          for (int e = 0; e < E::kPer; ++e) {
+            int32_t high = 0, low = 0;
+            r.add(vp[k], vq[k], x0, e, high, low);
+            own += w[e] = join(high, low);
+          }
+          const uint64_t incl = warp_scan(own);
+          uint64_t at = below + incl - own;
+          const unsigned hit = __ballot_sync(0xffffffffu, found < 0 && below + incl > x);
+          if (hit && lane == __ffs(hit) - 1) {
+            int e = 0;
+#pragma unroll
+            for (int y = 0; y < E::kPer; ++y) {
+              at += w[y];
+              if (at <= x) e = y + 1;
+            }
+            out[count] = x0 + e - r.skew;
+          }
+          if (hit) found = 0;
+          below += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (found >= 0) break;
+      }
+    }
+    break;
   }
+  cluster_arrive();      // no CTA leaves while another may read its total
+  cluster_wait();
+}
+
+template <int TYPE>
+cudaError_t launch_t(const DraftArgs& a, int cluster, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(verify_kernel<TYPE>,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_reqs) * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<TYPE>, a, cluster);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const DraftArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
-  if (a.type == MM3IDX_TYPE_FP32) verify_kernel<MM3IDX_TYPE_FP32><<<a.num_reqs, kThreads, 0, s>>>(a);
-  else if (a.type == MM3IDX_TYPE_BF16) verify_kernel<MM3IDX_TYPE_BF16><<<a.num_reqs, kThreads, 0, s>>>(a);
-  else verify_kernel<MM3IDX_TYPE_FP16><<<a.num_reqs, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // CTAs a request: enough to fill the card four deep, each with two steps a
+  // warp at least.
+  int cluster = 1;
+  const int most = a.vocab / (4096 * 2);
+  while (cluster < kMaxCluster && cluster < most && static_cast<int64_t>(a.num_reqs) * cluster < 4 * sms)
+    cluster *= 2;
+  if (a.type == MM3IDX_TYPE_FP32) return launch_t<MM3IDX_TYPE_FP32>(a, cluster, s);
+  if (a.type == MM3IDX_TYPE_BF16) return launch_t<MM3IDX_TYPE_BF16>(a, cluster, s);
+  return launch_t<MM3IDX_TYPE_FP16>(a, cluster, s);
 }
 
 }  // namespace mm3idx

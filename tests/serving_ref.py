@@ -162,7 +162,7 @@ def evict_ref(acc, lens, tables, *, budget, init, local, max_seq_len, weights=No
 
 
 def verify_ref(target, tokens, u, draft=None, lens=None):
-    """(tokens, accepted) as lists, in exact integers of 2^-52 where the library's are, for
+    """(tokens, accepted) as lists, in exact integers of 2^-46 where the library's are, for
     probabilities from 0 to 1."""
     reqs, rows, vocab = target.shape
     k = rows - 1
@@ -170,7 +170,7 @@ def verify_ref(target, tokens, u, draft=None, lens=None):
     def fixed(x):                       # 64-bit floats hold every value exactly
         x = x.to(F64)
         x = torch.where(torch.isnan(x), torch.zeros_like(x), x).clamp(0, 1)
-        return torch.round(x * 2.0 ** 52).to(torch.int64)
+        return torch.round(x * 2.0 ** 46).to(torch.int64)
 
     out, accepted = [], []
     for i in range(reqs):

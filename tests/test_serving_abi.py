@@ -135,7 +135,7 @@ def drafts(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(num_reqs=-1), -1), (dict(vocab=0), -16), (dict(drafts=-1), -16), (dict(drafts=32), -16),
+    (dict(num_reqs=-1), -1), (dict(vocab=0), -16), (dict(vocab=(1 << 30) + 1), -16), (dict(drafts=-1), -16), (dict(drafts=32), -16),
     (dict(type=3), -1), (dict(target=None), -1), (dict(tokens=None), -1), (dict(uniforms=None), -1),
     (dict(out=None), -1), (dict(accepted=None), -1), (dict(target=FAKE + 2), -1),
     (dict(type=0, draft=FAKE + 1), -1), (dict(target_row_stride=99), -16),
