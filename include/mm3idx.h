@@ -505,9 +505,9 @@ typedef struct mm3idx_weights {
 /*
  * mm3idx_accumulate_weights -- acc[i, b] = decay * acc[i, b] + the sum of
  * request i's weights of block b, in place, for its blocks
- * b < cdiv(seq_lens[i], 128); the other columns are left as they are.  Summed in 64 bits and rounded
- * once, so the result does not depend on an order; an id given twice counts
- * twice, one outside the request's blocks is ignored.
+ * b < cdiv(seq_lens[i], 128); the other columns are left as they are.  Summed
+ * in twice fp32's digits and rounded once; an id given twice counts twice,
+ * one outside the request's blocks is ignored.
  */
 int mm3idx_accumulate_weights(const mm3idx_weights_t *w, void *stream);
 

@@ -241,7 +241,8 @@ int mm3idx_accumulate_weights(const mm3idx_weights_t* w, void* stream) {
   int sms = 0;
   int32_t* status = nullptr;
   if ((rc = library_device(&sms, &status))) return rc;
-  return cuda_status(launch_accumulate(weight_args(w, status), static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_accumulate(weight_args(w, status), w->acc, w->acc_stride,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 int mm3idx_evict_blocks(const mm3idx_weights_t* w, const mm3idx_eviction_t* e, void* stream) {

@@ -2,12 +2,25 @@
 // the lightest of them (include/mm3idx.h, mm3idx_accumulate_weights,
 // mm3idx_evict_blocks).
 //
-// One CTA per request.  The weights are ordered by the unsigned image of
-// their fp32 bits (ordered_bits), so the threshold, the weight of the last
-// block that stays, is found bit by bit from the top: 32 counts of the
-// weights at or above a trial value.  Of the blocks at the threshold the ones
-// with the lowest ids stay.  Both the order and the counts are whole numbers:
-// the result depends on nothing but the weights.
+// Mathematics.  acc' = decay acc + sum of the step's weights, carried as an
+// unevaluated sum of two floats (products by fma, sums by the two-sum of Knuth),
+// exact to about 2^-46, then rounded once to fp32: the order of the terms does
+// not show.  (fp64 instructions would do the same at a sixtieth of the rate:
+// 128 requests of 8192 blocks took 52 us with them, most of it there.)  The
+// weights are ordered by the unsigned image of their bits (ordered_bits), and
+// the weight of the last block that stays is found from the top, two bits a
+// round: how many blocks are at or above each of three trial values.  Rounds
+// start at the highest bit in which any two weights differ and stop when a
+// count meets the number of places; of blocks at the threshold the lowest ids
+// stay.  Whole numbers throughout: the result depends on the weights alone.
+//
+// What bounds it.  A few bytes a block: latency, of one round of loads and of
+// the rounds of counts.  One CTA takes a request; every load is issued before
+// the first is used, and a thread keeps its blocks' weights and table entries
+// in registers (blocks kThreads apart, so that a warp's accesses are one line:
+// 16 neighbouring blocks a thread took 39 us for 128 x 8192 blocks), so a round
+// is a few compares, one warp reduction and one barrier.  Wider tables than the registers hold (kFastWidth) go
+// through global memory.
 #include "../../include/mm3idx.h"
 #include "ptx.cuh"
 #include "serving.h"
@@ -15,148 +28,445 @@
 namespace mm3idx {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kEntries = MM3IDX_MAX_WEIGHT_ENTRIES;
+constexpr int kWideThreads = 1024;
+constexpr int kSumThreads = 256;
+constexpr int kMaxItems = 8;
+constexpr int kFastThreads = 1024;
+constexpr int kFastWidth = kMaxItems * kFastThreads;   // blocks: a million tokens
 
 // The block's place in the weight order: higher is heavier, NaN above all.
 __device__ __forceinline__ uint32_t rank_bits(float w) {
   return w != w ? 0xFFFFFFFFu : ordered_bits(w);
 }
 
-struct Shared {
-  int32_t ids[kEntries];
-  float w[kEntries];
-  uint32_t touched[(0xFFFF + 31) / 32];  // blocks that the ids name, a bit each
-  int sums[kWarps];
-  int total;
+// high + low, a sum in about twice fp32's digits.
+struct Sum {
+  float high, low;
+  // decay * x, decay given as a sum of two floats
+  __device__ __forceinline__ Sum(float x, float decay_high, float decay_low) {
+    high = __fmul_rn(x, decay_high);
+    low = __fmaf_rn(x, decay_low, __fmaf_rn(x, decay_high, -high));
+  }
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(high, x), b = __fsub_rn(s, high);
+    low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(x, b)));
+    high = s;
+  }
+  // (an infinite or NaN sum has no second part)
+  __device__ __forceinline__ float value() const {
+    return isfinite(high) ? __fadd_rn(high, low) : high;
+  }
 };
 
-// Sum over the CTA, on every thread (called by all of them).
-__device__ __forceinline__ int block_sum(int x, Shared& sh) {
-  x = __reduce_add_sync(0xffffffffu, x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  return __reduce_add_sync(0xffffffffu, sh.sums[threadIdx.x & 31]);
+struct Decay {
+  float high, low;
+  __device__ __forceinline__ explicit Decay(double d)
+      : high(static_cast<float>(d)), low(static_cast<float>(d - static_cast<double>(high))) {}
+};
+
+// The step's entries (query row, place) of a request, in shared memory.
+struct Entries {
+  int32_t id[kEntries];
+  float w[kEntries];
+};
+
+__device__ __forceinline__ int load_entries(const WeightArgs& a, int i, Entries& en) {
+  const int count = a.w ? a.query_len * a.topk : 0, padded = (count + 3) & ~3;
+  const int64_t row0 = static_cast<int64_t>(i) * a.query_len;
+  for (int e = threadIdx.x; e < padded; e += blockDim.x) {
+    const int64_t row = row0 + e / a.topk;
+    const int k = e % a.topk;
+    en.id[e] = e < count ? __ldg(a.ids + row * a.ids_stride + k) : -1;
+    en.w[e] = e < count ? __ldg(a.w + row * a.w_stride + k) : 0.0f;
+  }
+  return padded;
 }
 
-// Sum over the threads below this one, and over all (called by all threads).
-__device__ __forceinline__ int block_scan(int x, Shared& sh, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Adds to `s` every entry of e's block from e on, in order; false if an
+// earlier entry has that block (which then is its to sum).
+__device__ __forceinline__ bool sum_block(const Entries& en, int count, int e, Sum& s) {
+  const int b = en.id[e];
+  bool first = true;
+  for (int x = 0; x < count; x += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(en.id + x);
+    const int ids[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ids[k] != b) continue;
+      if (x + k < e) first = false;
+      else s.add(en.w[x + k]);
+    }
+  }
+  return first;
+}
+
+__device__ __forceinline__ int request_len(const WeightArgs& a, int i, bool report) {
+  const int raw = __ldg(a.seq_lens + i);
+  if (report && (raw > a.max_seq_len || raw < 0))
+    atomicOr(a.status, raw < 0 ? MM3IDX_DEV_SEQ_TOO_SHORT : MM3IDX_DEV_SEQ_TOO_LONG);
+  return min(max(raw, 0), a.max_seq_len);
+}
+
+__device__ __forceinline__ int blocks_of(int len) { return (len + kBlock - 1) / kBlock; }
+
+// dst = the weights brought up to date: kSumThreads blocks a CTA.
+__global__ void __launch_bounds__(kSumThreads)
+    accumulate_kernel(const WeightArgs a, float* dst, int64_t dst_stride) {
+  __shared__ __align__(16) Entries en;
+  __shared__ int touched[kSumThreads];
+  const int i = blockIdx.x, b0 = blockIdx.y * kSumThreads, b = b0 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n = blocks_of(request_len(a, i, threadIdx.x == 0 && b0 == 0));
+  if (b0 >= n) return;
+  const Decay d(a.decay);
+  const float* acc = a.acc + i * a.acc_stride;
+  float* out = dst + i * dst_stride;
+  const float old = b < n ? acc[b] : 0.0f;
+  Sum s(old, d.high, d.low);
+  if (a.ids && a.w) {
+    const int count = load_entries(a, i, en);
+    touched[threadIdx.x] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < count; e += kSumThreads) {
+      const int at = en.id[e];
+      if (at < b0 || at >= min(n, b0 + kSumThreads)) continue;
+      Sum t(acc[at], d.high, d.low);
+      if (!sum_block(en, count, e, t)) continue;
+      touched[at - b0] = 1;
+      out[at] = t.value();
+    }
+    __syncthreads();
+    if (b >= n || touched[threadIdx.x]) return;
+  } else if (a.w && b < n) {
+    const float* w = a.w + static_cast<int64_t>(i) * a.query_len * a.w_stride + b;
+    for (int j = 0; j < a.query_len; ++j) s.add(__ldg(w + j * a.w_stride));
+  }
+  if (b < n) out[b] = s.value();
+}
+
+// ------------------------------------------------------------ block-wide sums
+
+// Packed sums over the warps; buffers alternate, so one barrier a call.
+struct Exchange {
+  uint32_t word[2][32];
+  uint32_t top[32], bottom[32];
+};
+
+// Exclusive sum of x over the threads before this one, and the total.
+__device__ __forceinline__ int block_scan(int x, Exchange& ex, int turn, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
+  if (lane == 31) ex.word[turn & 1][warp] = incl;
   __syncthreads();
-  if (lane == 31) sh.sums[warp] = incl;
-  __syncthreads();
-  const int s = sh.sums[lane];
+  const int s = lane < warps ? static_cast<int>(ex.word[turn & 1][lane]) : 0;
   total = __reduce_add_sync(0xffffffffu, s);
   return incl - x + __reduce_add_sync(0xffffffffu, lane < warp ? s : 0);
 }
 
-__device__ __forceinline__ int request_len(const WeightArgs& a, int i) {
-  const int raw = a.seq_lens[i];
-  if (threadIdx.x == 0 && (raw > a.max_seq_len || raw < 0))
-    atomicOr(a.status, raw < 0 ? MM3IDX_DEV_SEQ_TOO_SHORT : MM3IDX_DEV_SEQ_TOO_LONG);
-  return min(max(raw, 0), a.max_seq_len);
-}
-
-// dst[0..n) = the weights of request i brought up to date (dst may be acc).
-__device__ __forceinline__ void accumulate(const WeightArgs& a, int i, int n, float* dst,
-                                           Shared& sh) {
-  const float* acc = a.acc + i * a.acc_stride;
-  const double decay = a.decay;
-  const int64_t row0 = static_cast<int64_t>(i) * a.query_len;
-  const int rows = a.w ? a.query_len : 0;
-  if (!a.ids) {
-    for (int b = threadIdx.x; b < n; b += kThreads) {
-      double s = decay * acc[b];
-      for (int j = 0; j < rows; ++j) s += a.w[(row0 + j) * a.w_stride + b];
-      dst[b] = static_cast<float>(s);
+// at[k] = how many of the CTA's flags come before this thread's k-th, blocks
+// in order (the k-th block of thread t is k * blockDim.x + t).
+template <int ITEMS>
+__device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at)[ITEMS]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const unsigned before = (1u << lane) - 1u;
+  __syncthreads();                       // `counts` may still be read
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const unsigned set = __ballot_sync(0xffffffffu, (flags >> k) & 1u);
+    at[k] = __popc(set & before);
+    if (lane == 0) counts[k * warps + warp] = __popc(set);
+  }
+  __syncthreads();
+  if (warp == 0) {                       // exclusive sums of ITEMS * warps <= 256 counts
+    constexpr int kEach = ITEMS;
+    int c[kEach], sum = 0;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int p = lane * kEach + x;
+      c[x] = p < ITEMS * warps ? counts[p] : 0;
+      sum += c[x];
     }
-    return;
-  }
-  // An entry whose id appears for the first time sums all entries of that id.
-  const int entries = rows * a.topk;
-  for (int k = threadIdx.x; k < (n + 31) / 32; k += kThreads) sh.touched[k] = 0;
-  for (int e = threadIdx.x; e < entries; e += kThreads) {
-    const int64_t row = row0 + e / a.topk;
-    const int b = a.ids[row * a.ids_stride + e % a.topk];
-    sh.ids[e] = b >= 0 && b < n ? b : -1;
-    sh.w[e] = a.w[row * a.w_stride + e % a.topk];
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < entries; e += kThreads) {
-    const int b = sh.ids[e];
-    bool first = b >= 0;
-    for (int x = 0; x < e && first; ++x) first = sh.ids[x] != b;
-    if (!first) continue;
-    double s = decay * acc[b];
-    for (int x = e; x < entries; ++x)
-      if (sh.ids[x] == b) s += sh.w[x];
-    dst[b] = static_cast<float>(s);
-    atomicOr(&sh.touched[b >> 5], 1u << (b & 31));
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int p = lane * kEach + x;
+      if (p < ITEMS * warps) counts[p] = run;
+      run += c[x];
+    }
   }
   __syncthreads();
-  if (a.decay != 1.0 || dst != acc)
-    for (int b = threadIdx.x; b < n; b += kThreads)
-      if (!((sh.touched[b >> 5] >> (b & 31)) & 1u)) dst[b] = static_cast<float>(decay * acc[b]);
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) at[k] += counts[k * warps + warp];
 }
 
-__global__ void __launch_bounds__(kThreads) accumulate_kernel(const WeightArgs a) {
-  __shared__ Shared sh;
-  const int i = blockIdx.x;
-  accumulate(a, i, (request_len(a, i) + kBlock - 1) / kBlock, a.acc + i * a.acc_stride, sh);
+// The threshold and the places at it: `picks` of the keys for which `each`
+// calls back stay, those above `cut` and the first `ties` at it.  `each(f)`
+// applies f to this thread's keys (no more than 31); called by all threads.
+template <class Each>
+__device__ __forceinline__ void threshold(int picks, Exchange& ex, int& turn, Each each,
+                                          uint32_t& cut, int& ties) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  cut = 0xFFFFFFFFu;
+  ties = 0;
+  if (picks == 0) return;
+  uint32_t top = 0, bottom = 0xFFFFFFFFu;
+  each([&](uint32_t r) {
+    top = max(top, r);
+    bottom = min(bottom, r);
+  });
+  top = __reduce_max_sync(0xffffffffu, top);
+  bottom = __reduce_min_sync(0xffffffffu, bottom);
+  if (lane == 0) {
+    ex.top[warp] = top;
+    ex.bottom[warp] = bottom;
+  }
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, lane < warps ? ex.top[lane] : 0u);
+  bottom = __reduce_min_sync(0xffffffffu, lane < warps ? ex.bottom[lane] : 0xFFFFFFFFu);
+  cut = top;
+  ties = picks;
+  if (top == bottom) return;
+  int shift = (31 - __clz(top ^ bottom)) & ~1, above = 0;
+  cut = shift == 30 ? 0u : top & ~((4u << shift) - 1u);
+  for (; shift >= 0; shift -= 2) {
+    const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
+    uint32_t c = 0;
+    each([&](uint32_t r) {
+      c += (r >= t1 ? 1u : 0u) + (r >= t2 ? 1u << 10 : 0u) + (r >= t3 ? 1u << 20 : 0u);
+    });
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) ex.word[turn & 1][warp] = c;
+    __syncthreads();
+    c = lane < warps ? ex.word[turn & 1][lane] : 0u;
+    ++turn;
+    const int c1 = __reduce_add_sync(0xffffffffu, c & 1023u);
+    const int c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
+    const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
+    int here;
+    if (c3 >= picks) {
+      cut = t3;
+      here = c3;
+    } else if (c2 >= picks) {
+      cut = t2;
+      here = c2;
+      above = c3;
+    } else if (c1 >= picks) {
+      cut = t1;
+      here = c1;
+      above = c2;
+    } else {
+      here = 0;
+      above = c1;
+    }
+    if (here == picks) {       // exactly the keys from cut on
+      --cut;
+      ties = 0;
+      return;
+    }
+  }
+  ties = picks - above;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e) {
-  __shared__ Shared sh;
-  const int i = blockIdx.x;
-  const int seq = request_len(e.w, i), n = (seq + kBlock - 1) / kBlock;
-  float* acc = e.acc_out + i * e.acc_out_stride;   // up to date here, then compacted in place
-  accumulate(e.w, i, n, acc, sh);
-  __syncthreads();
+// ---------------------------------------------------------------- eviction
+
+// Columns behind the kept blocks, and the new length.
+__device__ __forceinline__ void finish(const EvictArgs& e, int i, int seq, int n, int kept) {
+  const int room = max(1, e.width - e.budget);
+  float* acc = e.acc_out + i * e.acc_out_stride;
+  for (int c = kept + threadIdx.x; c < max(e.width, e.budget); c += blockDim.x) {
+    if (c < e.width) acc[c] = 0.0f;
+    if (c >= e.budget) continue;
+    if (e.ids) e.ids[i * e.ids_stride + c] = -1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (e.t[k].in) e.t[k].out[i * e.t[k].out_stride + c] = -1;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (e.t[k].in && e.t[k].freed)
+      for (int c = n - kept + threadIdx.x; c < room; c += blockDim.x)
+        e.t[k].freed[i * e.t[k].freed_stride + c] = -1;
+  if (threadIdx.x == 0) e.seq_out[i] = seq - kBlock * (n - kept);
+}
+
+// ITEMS blocks a thread, blockDim.x apart.
+template <int ITEMS>
+__global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) {
+  __shared__ Exchange ex;
+  __shared__ __align__(16) Entries en;
+  __shared__ uint32_t touched[kFastWidth / 32];
+  __shared__ int counts[kMaxItems * kFastThreads / 32];
+  extern __shared__ float staged[];              // sparse steps: the weights by block
+  const int i = blockIdx.x, T = blockDim.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const WeightArgs& a = e.w;
+  const float* acc = a.acc + i * a.acc_stride;
+  const int seq = request_len(a, i, threadIdx.x == 0), n = blocks_of(seq);
+  // Up to e.width, not n: none of these loads waits for the length.
+  float w[ITEMS];
+  int32_t entry[2][ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int b = k * T + threadIdx.x;
+    const bool in = b < e.width;
+    w[k] = in ? __ldcg(acc + b) : 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      entry[t][k] = in && e.t[t].in ? __ldcg(e.t[t].in + i * e.t[t].in_stride + b) : 0;
+  }
+  const Decay d(a.decay);
+  if (a.w && a.ids) {
+    const int count = load_entries(a, i, en);
+    for (int k = threadIdx.x; k < (e.width + 31) / 32; k += T) touched[k] = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (k * T + threadIdx.x < e.width) staged[k * T + threadIdx.x] = w[k];
+    __syncthreads();
+    for (int x = threadIdx.x; x < count; x += T) {
+      const int b = en.id[x];
+      if (b < 0 || b >= n) continue;
+      Sum s(staged[b], d.high, d.low);
+      if (!sum_block(en, count, x, s)) continue;
+      staged[b] = s.value();       // no other thread has this block
+      atomicOr(&touched[b >> 5], 1u << (b & 31));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int b = k * T + threadIdx.x;
+      if (b >= e.width) continue;
+      const bool fresh = (touched[b >> 5] >> (b & 31)) & 1u;
+      w[k] = fresh ? staged[b] : Sum(w[k], d.high, d.low).value();
+    }
+  } else {
+    float x0[ITEMS];                             // the first row's, all in flight at once
+    const float* x = a.w + static_cast<int64_t>(i) * a.query_len * a.w_stride + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      x0[k] = a.w && k * T + threadIdx.x < e.width ? __ldg(x + k * T) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      Sum s(w[k], d.high, d.low);
+      if (a.w && k * T + threadIdx.x < e.width) {
+        s.add(x0[k]);
+        for (int j = 1; j < a.query_len; ++j) s.add(__ldg(x + j * a.w_stride + k * T));
+      }
+      w[k] = s.value();
+    }
+  }
   const int kept = min(n, e.budget), f_lo = e.init_blocks, l_lo = n - e.local_blocks;
-  // The threshold among the blocks [f_lo, l_lo): `picks` of them stay.
-  const int picks = kept - (n - max(0, l_lo - f_lo));
-  uint32_t cut = 0;       // weights above it stay, and the first `ties` of those at it
-  int ties = 0;
-  if (n > e.budget) {
+  uint32_t cut = 0;
+  int ties = 0, turn = 0;
+  const bool full = n > e.budget;
+  if (full)
+    threshold(kept - (n - max(0, l_lo - f_lo)), ex, turn,
+              [&](auto f) {
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k) {
+                  const int b = k * T + threadIdx.x;
+                  if (b >= f_lo && b < l_lo) f(rank_bits(w[k]));
+                }
+              },
+              cut, ties);
+  // Which blocks stay, and the columns they move to.
+  uint32_t stays = 0, tied = 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int b = k * T + threadIdx.x;
+    const bool open = full && b >= f_lo && b < l_lo;
+    const uint32_t r = rank_bits(w[k]);
+    if (b < n && (!open || r > cut)) stays |= 1u << k;
+    if (open && r == cut) tied |= 1u << k;
+  }
+  int at[ITEMS];
+  if (ties > 0) {
+    block_rank<ITEMS>(tied, counts, at);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (((tied >> k) & 1u) && at[k] < ties) stays |= 1u << k;
+  }
+  // (its barriers also part the loads of every thread from the stores below)
+  block_rank<ITEMS>(stays, counts, at);
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int b = k * T + threadIdx.x;
+    if (b >= n) continue;
+    const bool stay = (stays >> k) & 1u;
+    if (stay) {
+      if (e.ids) e.ids[i * e.ids_stride + at[k]] = b;
+      e.acc_out[i * e.acc_out_stride + at[k]] = w[k];
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!e.t[t].in) continue;
+      if (stay) e.t[t].out[i * e.t[t].out_stride + at[k]] = entry[t][k];
+      else if (e.t[t].freed) e.t[t].freed[i * e.t[t].freed_stride + b - at[k]] = entry[t][k];
+    }
+  }
+  finish(e, i, seq, n, kept);
+}
+
+// Any width; the weights are up to date in acc_out and compacted in place.
+__global__ void __launch_bounds__(kWideThreads) evict_wide_kernel(const EvictArgs e) {
+  __shared__ Exchange ex;
+  const int i = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int seq = request_len(e.w, i, false), n = blocks_of(seq);
+  float* acc = e.acc_out + i * e.acc_out_stride;
+  const int kept = min(n, e.budget), f_lo = e.init_blocks, l_lo = n - e.local_blocks;
+  uint32_t cut = 0;
+  int ties = 0, turn = 0;
+  const bool full = n > e.budget;
+  if (full) {
+    // one bit a round: a thread's count has no bound that a packed field holds
+    const int picks = kept - (n - max(0, l_lo - f_lo));
+    int total;
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t trial = cut | (1u << bit);
       int c = 0;
-      for (int b = f_lo + threadIdx.x; b < l_lo; b += kThreads) c += rank_bits(acc[b]) >= trial;
-      if (block_sum(c, sh) >= picks) cut = trial;
+      for (int b = f_lo + threadIdx.x; b < l_lo; b += kWideThreads) c += rank_bits(acc[b]) >= trial;
+      block_scan(c, ex, turn++, total);
+      if (total >= picks) cut = trial;
     }
     int c = 0;
-    for (int b = f_lo + threadIdx.x; b < l_lo; b += kThreads) c += rank_bits(acc[b]) > cut;
-    ties = picks - block_sum(c, sh);
+    for (int b = f_lo + threadIdx.x; b < l_lo; b += kWideThreads) c += rank_bits(acc[b]) > cut;
+    block_scan(c, ex, turn++, total);
+    ties = picks - total;
   }
-  // Compaction, kThreads blocks at a time: a kept block moves to a column at
-  // or before its own, so in place each chunk is read before it is written.
+  // kWideThreads blocks at a time: a kept block moves to a column at or before
+  // its own, so each chunk is read before it is written.
   int done = 0, gone = 0, tied = 0;
-  for (int b0 = 0; b0 < n; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
+  for (int c0 = 0; c0 < n; c0 += kWideThreads) {
+    const int b = c0 + threadIdx.x;
     const float w = b < n ? acc[b] : 0.0f;
-    const bool free = b >= f_lo && b < l_lo && n > e.budget;
+    const bool open = b >= f_lo && b < l_lo && full;
     const uint32_t r = rank_bits(w);
-    int all;
-    const int tie_at = tied + block_scan(free && r == cut, sh, all);
-    tied += all;
-    const bool stays = b < n && (!free || r > cut || (r == cut && tie_at < ties));
-    const int at = done + block_scan(stays, sh, all);
-    const int gone_at = gone + b - b0 - (at - done);
-    done += all;
-    gone += min(kThreads, n - b0) - all;
     int32_t entry[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (e.t[k].in && b < n) entry[k] = e.t[k].in[i * e.t[k].in_stride + b];
-    __syncthreads();
+    int all;
+    const int tie_at = tied + block_scan(open && r == cut, ex, turn++, all);
+    tied += all;
+    const bool stays = b < n && (!open || r > cut || (r == cut && tie_at < ties));
+    const int at = done + block_scan(stays, ex, turn++, all);
+    const int gone_at = gone + b - c0 - (at - done);
+    done += all;
+    gone += min(kWideThreads, n - c0) - all;
     if (stays) {
       if (e.ids) e.ids[i * e.ids_stride + at] = b;
       acc[at] = w;
@@ -169,32 +479,48 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e) {
     }
   }
   __syncthreads();
-  const int room = max(1, e.width - e.budget);
-  for (int c = threadIdx.x; c < max(e.width, e.budget); c += kThreads) {
-    if (c >= kept && c < e.width) acc[c] = 0.0f;
-    if (c >= kept && c < e.budget && e.ids) e.ids[i * e.ids_stride + c] = -1;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!e.t[k].in) continue;
-      if (c >= kept && c < e.budget) e.t[k].out[i * e.t[k].out_stride + c] = -1;
-      if (c >= n - kept && c < room && e.t[k].freed)
-        e.t[k].freed[i * e.t[k].freed_stride + c] = -1;
-    }
-  }
-  if (threadIdx.x == 0) e.seq_out[i] = seq - kBlock * (n - kept);
+  finish(e, i, seq, n, kept);
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int ITEMS>
+cudaError_t launch_items(const EvictArgs& a, cudaStream_t s) {
+  const int threads = ((a.width + ITEMS - 1) / ITEMS + 31) / 32 * 32;
+  return launch(evict_kernel<ITEMS>, dim3(a.w.num_reqs), threads,
+                a.w.w && a.w.ids ? static_cast<size_t>(a.width) * 4 : 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_accumulate(const WeightArgs& a, cudaStream_t s) {
-  if (!a.w && a.decay == 1.0) return cudaSuccess;
-  accumulate_kernel<<<a.num_reqs, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_accumulate(const WeightArgs& a, float* dst, int64_t dst_stride, cudaStream_t s) {
+  const int chunks = ((a.max_seq_len + kBlock - 1) / kBlock + kSumThreads - 1) / kSumThreads;
+  return launch(accumulate_kernel, dim3(a.num_reqs, chunks), kSumThreads, 0, s, a, dst, dst_stride);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-  evict_kernel<<<a.w.num_reqs, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // As many threads as it takes, up to kFastThreads, then more blocks a thread.
+  if (a.width <= kFastThreads) return launch_items<1>(a, s);
+  if (a.width <= 2 * kFastThreads) return launch_items<2>(a, s);
+  if (a.width <= 4 * kFastThreads) return launch_items<4>(a, s);
+  if (a.width <= kFastWidth) return launch_items<8>(a, s);
+  const cudaError_t e = launch_accumulate(a.w, a.acc_out, a.acc_out_stride, s);
+  if (e != cudaSuccess) return e;
+  return launch(evict_wide_kernel, dim3(a.w.num_reqs), kWideThreads, 0, s, a);
 }
 
 }  // namespace mm3idx

@@ -53,6 +53,9 @@ CASES = [
     ([20000, 19999, 100, 12345], 1, 0, 41, 3, 5, 0.0, True),
     ([128 * 5000, 128 * 1025 - 1, 128 * 1024], 1, 0, 1024, 4, 8, 0.99, False),
     ([128 * 9000 + 1, 77], 8, 32, 2050, 1, 2, 0.99, False),
+    ([128 * 8200, 128 * 8193 - 5, 40], 2, 0, 700, 2, 3, 0.7, True),
+    ([128 * 512, 128 * 513], 1, 0, 300, 1, 1, 1.0, True),
+    ([128 * 512], 1, 8, 511, 1, 1, 1.0, False),
 ]
 
 
