@@ -758,7 +758,8 @@ def _allocating_on(stream):
 
 def _row_stride(t):
     """Elements between the rows of a 2-D tensor (free when it has one row)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, columns = t.shape
+    return t.stride(0) if rows > 1 else max(columns, 1)
 
 
 def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, num_reqs: int,
@@ -972,19 +973,19 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
     gone = max(1, width - budget)
     if out is None:
         with _allocating_on(stream):
-            # one buffer, a range of columns each
-            sizes = [budget, gone] if in_place else [budget, gone, budget]
+            i32 = {"dtype": torch.int32, "device": dev}
+            ids, freed = torch.empty((reqs, budget), **i32), torch.empty((reqs, gone), **i32)
+            table, table2, freed2 = block_table, second, None
+            new_lens, new_acc = seq_lens, acc
             if second is not None:
-                sizes += [gone] if in_place else [gone, budget]
-            parts = torch.empty((reqs, sum(sizes)), dtype=torch.int32, device=dev).split(sizes, 1)
-            if in_place:
-                out = Eviction(parts[0], seq_lens, acc, block_table, parts[1], second,
-                               None if second is None else parts[2])
-            else:
-                out = Eviction(parts[0], torch.empty_like(seq_lens),
-                               torch.empty((reqs, width), dtype=torch.float32, device=dev),
-                               parts[2], parts[1],
-                               *(() if second is None else (parts[4], parts[3])))
+                freed2 = torch.empty((reqs, gone), **i32)
+            if not in_place:
+                table = torch.empty((reqs, budget), **i32)
+                if second is not None:
+                    table2 = torch.empty((reqs, budget), **i32)
+                new_lens = torch.empty((reqs,), **i32)
+                new_acc = torch.empty((reqs, width), dtype=torch.float32, device=dev)
+            out = Eviction(ids, new_lens, new_acc, table, freed, table2, freed2)
     else:
         _need(not in_place, "out and in_place exclude each other")
         _need((out.attention_block_table is None) == (out.attention_freed is None)
@@ -1000,16 +1001,15 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
                   (out.attention_block_table, budget), (out.attention_freed, gone))),
               "out must be an Eviction of these shapes")
 
-    def table(old, new, freed):
-        return (old.data_ptr(), _row_stride(old), new.data_ptr(), _row_stride(new),
-                freed.data_ptr(), _row_stride(freed))
-
+    ids, new_lens, new_acc, table, freed, table2, freed2 = out
     e = _eviction_image(
-        budget, init_blocks, local_blocks, *table(block_table, out.block_table, out.freed),
+        budget, init_blocks, local_blocks, block_table.data_ptr(), _row_stride(block_table),
+        table.data_ptr(), _row_stride(table), freed.data_ptr(), _row_stride(freed),
         *((0,) * 6 if second is None else
-          table(second, out.attention_block_table, out.attention_freed)),
-        out.ids.data_ptr(), _row_stride(out.ids), out.weights.data_ptr(),
-        _row_stride(out.weights), out.seq_lens.data_ptr())
+          (second.data_ptr(), _row_stride(second), table2.data_ptr(), _row_stride(table2),
+           freed2.data_ptr(), _row_stride(freed2))),
+        ids.data_ptr(), _row_stride(ids), new_acc.data_ptr(), _row_stride(new_acc),
+        new_lens.data_ptr())
     with _on(dev):
         _check(lib.mm3idx_evict_blocks(w, e, _stream(dev, stream)), "mm3idx_evict_blocks")
     return out

@@ -29,7 +29,9 @@
 //     query_len) are rows of 16-row matrix products (mma.sync m16n8k16: with
 //     this few rows the kernel needs a tenth of even that rate, and a warp
 //     that owns its scores needs no exchange with others inside the loop).
-//     Warp w owns 16-row tile w % RT and token group w / RT of each tile.
+//     A warp owns one of RT 16-row tiles and one part of the tokens: of every
+//     tile, or with few rows of every second one, so that it has at least two
+//     16-token slices to overlap.
 //   * The reference m moves only when a score passes it by 8 (a factor of 256
 //     in the weights, which fp32 sums and 16-bit weights hold without loss),
 //     so the accumulators are rarely rescaled.
@@ -55,7 +57,11 @@ namespace attn {
 constexpr int kConsumers = 8;                    // warps
 constexpr int kProducer = kConsumers;            // warp index
 constexpr int kWeigher = kConsumers + 1;         // warp that writes the tiles' weights
-constexpr int kThreads = (kConsumers + 2) * 32;
+constexpr int kThreads = (kConsumers + 4) * 32;  // three warpgroups, the last one half empty
+// Registers a thread: the launch's, and the split of them (setmaxnreg) between
+// the consumers' two warpgroups and the third, whose sum is the launch's.
+constexpr int kRegsLaunch = 168, kRegsConsumer = 216, kRegsOther = 72;
+static_assert(2 * kRegsConsumer + kRegsOther == 3 * kRegsLaunch, "register split");
 constexpr int kTile = kBlock;                    // tokens of a tile
 constexpr int kRedStride = 40;                   // floats of a 32-column row in the join buffer
 constexpr float kLog2e = 1.4426950408889634f;
@@ -76,13 +82,17 @@ struct Cfg {
   static constexpr int kHalf = kTile * kRow;
   static constexpr int kSlot = kHalves * kHalf;
   static constexpr int kSlots = kSlot == 32768 ? 6 : kSlot == 16384 ? 12 : 16;  // even: keys, values
+  // Barriers per kind.  A slot that warps take turns at (every second tile is
+  // one group's) has one barrier a group: a group that skips a slot's phase
+  // cannot tell the phase before it from the phase after it by their parity.
+  static constexpr int kBars = kSlots / 2 % 2 ? 2 * kSlots : kSlots;
   static constexpr uint32_t kSwizzle = kRow == 128 ? 0x70 : 0x30;
   static constexpr int oRed = kSlots * kSlot;
   static constexpr int oMl = oRed + kConsumers * 16 * kRedStride * 4;
   static constexpr int oFin = oMl + kConsumers * 16 * 8;
   static constexpr int oSlice = oFin + 64 * 8;
   static constexpr int oBar = oSlice + kSlots / 2 * kConsumers * 16 * 4;
-  static constexpr int oMask = oBar + 3 * kSlots * 8;
+  static constexpr int oMask = oBar + 3 * kBars * 8;
   static constexpr int oMisc = oMask + kSlots * 4;
   static constexpr int kSmem = oMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -285,6 +295,18 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Every lane's view of a phase's end; the bounded wait where it is not there yet.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -362,11 +384,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const AttentionArgs a) {
   using C = Cfg<KV, D>;
-  constexpr int S = C::kSlots;
+  constexpr int S = C::kSlots, NB = C::kBars;       // data slots; barriers (a multiple of them)
   constexpr bool kByte = C::kByte;
   constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
-  constexpr int TG = kConsumers / RT;               // token groups of a tile
-  constexpr int NS = RT;                            // 16-token slices of a warp
+  constexpr int TJ = kConsumers / RT;               // warps that share a row tile
+  constexpr int ALT = RT == 1 ? 2 : 1;              // a warp takes every ALT-th tile
+  static_assert(NB / 2 % ALT == 0, "a barrier belongs to one group of warps");
+  constexpr int TG = TJ / ALT;                      // token groups of a tile
+  constexpr int NS = 8 / TG;                        // 16-token slices of a warp
   constexpr int NT = D / 8;                         // output tiles of 8 columns
   constexpr int KS = D / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -377,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* fin = reinterpret_cast<float2*>(sm + C::oFin);   // [row of the task]
   float* slice = reinterpret_cast<float*>(sm + C::oSlice); // [slot / 2][warp][16]
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::oBar);
-  uint64_t* empty = full + S;
-  uint64_t* done = empty + S;                              // value slots: the tile's weights are there
+  uint64_t* empty = full + NB;
+  uint64_t* done = empty + NB;                             // values' barriers: the tile's weights are there
   uint32_t* mask = reinterpret_cast<uint32_t*>(sm + C::oMask);
   Misc* misc = reinterpret_cast<Misc*>(sm + C::oMisc);
   volatile int* abort_flag = &misc->abort;
@@ -386,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool weigh = a.tile_lse != nullptr;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < NB; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kConsumers + ((s & 1) && weigh ? 1 : 0));
-      mbar_init(&done[s], kConsumers);
+      mbar_init(&empty[s], kConsumers / ALT + ((s & 1) && weigh ? 1 : 0));
+      mbar_init(&done[s], kConsumers / ALT);
     }
     misc->abort = 0;
     fence_barrier_init();
@@ -407,12 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walker walk(misc);
   Segment sg;
 
-  if (warp == kProducer) {
+  if (warp >= kConsumers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kProducer) {
     // ---------------------------------------------------------- producer
     const int per = kTile >> a.page_shift;       // pages of a tile
     const int batch = 32 / per;                  // tiles whose page ids one register holds
     const int box = C::kRow << a.page_shift;
-    uint32_t slot = 0, round = 0, items = 0;
+    uint32_t slot = 0, bar = 0, items = 0;        // items: copies of a tile's keys or values
+    uint32_t wait = 0, wait_phase = 0;            // the barrier of the item S before
     bool ok = true;
     while (ok && walk.next(a, sg)) {
       const int head = (sg.task % a.tasks) / a.row_tiles;
@@ -437,23 +465,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = __popc(good) * C::kHalves * box;
 #pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          if (round > 0) ok = warp_wait(&empty[slot], (round - 1) & 1, abort_flag);
-          if (!ok) break;
+          if (items >= S) {
+            ok = warp_wait(&empty[wait], wait_phase, abort_flag);
+            if (!ok) break;
+            if (++wait == NB) {
+              wait = 0;
+              wait_phase ^= 1;
+            }
+          }
           if (lane == 0) {
             mask[slot] = good;
-            if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
-            else mbar_arrive(&full[slot]);
+            if (bytes) mbar_arrive_expect_tx(&full[bar], bytes);
+            else mbar_arrive(&full[bar]);
           }
           __syncwarp();
           if (issue)
             tma_load_4d(smem_u32(sm) + slot * C::kSlot + half * C::kHalf + p * box,
-                        kv ? &vmap : &kmap, &full[slot], half * (C::kRow / C::kElem), 0, head,
+                        kv ? &vmap : &kmap, &full[bar], half * (C::kRow / C::kElem), 0, head,
                         page);
           ++items;
-          if (++slot == S) {
-            slot = 0;
-            ++round;
-          }
+          if (++slot == S) slot = 0;
+          if (++bar == NB) bar = 0;
         }
       }
     }
@@ -463,20 +495,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t k = 0; k < pending; ++k) {
         const uint32_t idx = items - 1 - k;
         int dummy = 0;
-        mbar_wait(&full[idx % S], (idx / S) & 1, &dummy);
+        mbar_wait(&full[idx % NB], (idx / NB) & 1, &dummy);
       }
     }
     __syncwarp();
-  } else if (warp == kWeigher) {
+    } else if (warp == kWeigher) {
     // ------------------------------------- log-sum-exp of each tile's rows
     if (weigh) {
-      uint32_t slot = 1, round = 0;
+      uint32_t slot = 1, bar = 1, phase = 0, turn = 0;
       bool ok = true;
       while (ok && walk.next(a, sg)) {
-        for (int b = sg.b0; b < sg.b1 && ok; ++b) {
-          ok = warp_wait(&done[slot], round & 1, abort_flag);
+        for (int b = sg.b0; b < sg.b1 && ok; ++b, turn = (turn + 1) % ALT) {
+          ok = warp_wait(&done[bar], phase, abort_flag);
           if (!ok) break;
-          const float* from = slice + (slot >> 1) * kConsumers * 16;
+          const float* from = slice + ((slot >> 1) * kConsumers + turn * TG * RT) * 16;
           float* to = a.tile_lse + (static_cast<int64_t>(sg.task) * a.w_width + b) * (RT * 16);
           for (int r = lane; r < RT * 16; r += 32) {
             float x[TG], top = -INFINITY, sum = 0.0f;
@@ -491,23 +523,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             to[r] = ref + lg2(sum);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (lane == 0) mbar_arrive(&empty[bar]);
           slot += 2;
-          if (slot > S) {
-            slot = 1;
-            ++round;
+          if (slot > S) slot = 1;
+          bar += 2;
+          if (bar > NB) {
+            bar = 1;
+            phase ^= 1;
           }
         }
       }
     }
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
     // ---------------------------------------------------------- consumers
     const int c = lane & 3, g = lane >> 2;
-    const int rt = warp % RT, tg = warp / RT;
+    const int rt = warp % RT, tj = warp / RT, tg = tj % TG, alt = tj / TG;
     const uint32_t ring = smem_u32(sm);
     State<KV, D> st;
-    uint32_t slot = 0, phase = 0;
+    uint32_t slot = 0, bar = 0, phase = 0, turn = 0;
     bool dead = false;       // a wait gave up: go through the motions to the end
+    const bool rest = !kByte || a.q_type == MM3IDX_TYPE_FP16;   // weights as pairs
+
+    // Offsets of this lane in a slot for slice 0 of its tokens.  A 16-byte
+    // piece p of a row lies at p xor (row mod 8) (swizzled copies); slices and
+    // k-steps only add rows or flip bits of p, so the rest are constants.
+    auto twisted = [](uint32_t off) { return off ^ ((off >> 3) & C::kSwizzle); };
+    const uint32_t first = tg * NS * 16;
+    uint32_t koff, voff0, voff1 = 0;
+    if constexpr (!kByte) {
+      koff = twisted((first + ((lane >> 4) << 3) + (lane & 7)) * C::kRow + ((lane >> 3) & 1) * 16);
+      voff0 = twisted((first + (lane & 15)) * C::kRow + (lane >> 4) * 16);
+    } else {
+      koff = twisted((first + g) * C::kRow + c * (D / 4));
+      voff0 = twisted((first + 2 * c) * C::kRow + g * 4);
+      voff1 = twisted((first + 2 * c + 1) * C::kRow + g * 4);
+    }
 
     // Rows of empty requests.
     {
@@ -614,71 +666,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       st.l0 = st.l1 = 0.0f;
 
       for (int b = sg.b0; b < sg.b1; ++b) {
+        if constexpr (ALT > 1) {
+          const bool mine = turn == alt;
+          turn = (turn + 1) % ALT;
+          if (!mine) {
+            slot += 2;
+            if (slot == S) slot = 0;
+            bar += 2;
+            if (bar == NB) {
+              bar = 0;
+              phase ^= 1;
+            }
+            continue;
+          }
+        }
         // ------------------------------------------------------- scores
-        if (!dead) dead = !warp_wait(&full[slot], phase, abort_flag);
+        if (!dead) dead = !all_wait(&full[bar], phase, abort_flag);
         const uint32_t pages = mask[slot];
-        const uint32_t kbase = ring + slot * C::kSlot;
-        const int t0 = b * kTile;
-        float s[NS][8];
-        bool act[NS];
+        const uint32_t kbase = ring + slot * C::kSlot + koff;
+        const int t0 = b * kTile + static_cast<int>(first);
+        // Slices that any row of this warp sees; in a tile that all rows see
+        // whole, all of them.
+        const bool inside = !idle && !dead && t0 + NS * 16 <= lim_lo &&
+                            pages == (0xffffffffu >> (32 - (kTile >> a.page_shift)));
+        uint32_t act = (1u << NS) - 1u;
+        if (!inside) {
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            if (idle || dead || t0 + n * 16 >= lim_hi ||
+                !((pages >> ((first + n * 16) >> a.page_shift)) & 1u))
+              act &= ~(1u << n);
+        }
+        float s[NS][2][4];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          const int ts = (tg * NS + n) * 16;
-          act[n] = !idle && !dead && t0 + ts < lim_hi && ((pages >> (ts >> a.page_shift)) & 1u);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[n][e] = 0.0f;
-          if (act[n]) {
-            float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&s[n][0]);
-            float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&s[n][4]);
-            if constexpr (!kByte) {
-              const int tok = ts + ((lane >> 4) << 3) + (lane & 7);
-              const uint32_t row = kbase + tok * C::kRow;
+          for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.0f;
+          if (!((act >> n) & 1u)) continue;
+          if constexpr (!kByte) {
 #pragma unroll
-              for (int ks = 0; ks < KS; ++ks) {
-                const int ch = ks * 2 + ((lane >> 3) & 1);
-                uint32_t r[4];
-                ldmatrix4(row + (ch >> 3) * C::kHalf + (((ch & 7) ^ (tok & 7)) << 4), r);
-                mma<kBf>(lo, q[ks], r[0], r[1]);
-                mma<kBf>(hi, q[ks], r[2], r[3]);
-              }
-            } else {
+            for (int ks = 0; ks < KS; ++ks) {
+              uint32_t r[4];
+              ldmatrix4((kbase ^ ((2 * ks & 7) << 4)) + (ks >> 2) * C::kHalf + n * 16 * C::kRow, r);
+              mma<kBf>(s[n][0], q[ks], r[0], r[1]);
+              mma<kBf>(s[n][1], q[ks], r[2], r[3]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint32_t off = (ts + 8 * x + g) * C::kRow + c * (D / 4);
-                const uint32_t twist = (off >> 3) & C::kSwizzle;
+                const uint4 w = lds128((kbase ^ (16 * u)) + (n * 16 + 8 * x) * C::kRow);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int u = 0; u < D / 64; ++u) {
-                  const uint4 w = lds128(kbase + ((off + 16 * u) ^ twist));
-                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    mma<false>(x ? hi : lo, q[u * 4 + e], widen_lo(ww[e]), widen_hi(ww[e]));
-                }
+                for (int e = 0; e < 4; ++e)
+                  mma<false>(s[n][x], q[u * 4 + e], widen_lo(ww[e]), widen_hi(ww[e]));
               }
             }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        ++slot;      // the values' slot (kSlots is even)
+        if (lane == 0) mbar_arrive(&empty[bar]);
+        ++slot;      // the values' (both counts are even)
+        ++bar;
 
         // ------------------------------------------------------ softmax
-        float top_a = -INFINITY, top_b = -INFINITY;
+        if (!inside) {
+          // tokens that a row does not see: -inf before the (positive) scale
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          const int t = t0 + (tg * NS + n) * 16 + 2 * c;
-          const bool whole = act[n] && t0 + (tg * NS + n) * 16 + 16 <= lim_lo;
+          for (int n = 0; n < NS; ++n) {
+            const bool on = (act >> n) & 1u;
+            const int t = t0 + n * 16 + 2 * c;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool first = (e & 2) == 0;
-            const int tok = t + (e & 1) + ((e & 4) ? 8 : 0);
-            float x = s[n][e] * (first ? sc_a : sc_b);
-            if (!whole && (!act[n] || tok >= (first ? lim_a : lim_b))) x = -INFINITY;
-            s[n][e] = x;
-            if (first) top_a = fmaxf(top_a, x);
-            else top_b = fmaxf(top_b, x);
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!on || t + 8 * x + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][x][e] = -INFINITY;
           }
         }
+        float top_a = -INFINITY, top_b = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            top_a = max3(top_a, s[n][x][0], s[n][x][1]);
+            top_b = max3(top_b, s[n][x][2], s[n][x][3]);
+          }
+        top_a *= sc_a;
+        top_b *= sc_b;
         if (__any_sync(0xffffffffu, top_a > st.m0 + kRaise || top_b > st.m1 + kRaise)) {
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
@@ -705,25 +780,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t p[NS][4], pr[NS][4];
         float sum_a = 0.0f, sum_b = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          float w[8];
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = ex2(s[n][e] - ((e & 2) ? ref_b : ref_a));
-          sum_a += (w[0] + w[1]) + (w[4] + w[5]);
-          sum_b += (w[2] + w[3]) + (w[6] + w[7]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[n][k] = pack2<kBf>(w[2 * k], w[2 * k + 1]);
-            if constexpr (!kByte) pr[n][k] = pack2_rest<kBf>(w[2 * k], w[2 * k + 1], p[n][k]);
+          for (int x = 0; x < 2; ++x) {
+            const float w0 = ex2(fmaf(s[n][x][0], sc_a, -ref_a));
+            const float w1 = ex2(fmaf(s[n][x][1], sc_a, -ref_a));
+            const float w2 = ex2(fmaf(s[n][x][2], sc_b, -ref_b));
+            const float w3 = ex2(fmaf(s[n][x][3], sc_b, -ref_b));
+            sum_a += w0 + w1;
+            sum_b += w2 + w3;
+            p[n][2 * x] = pack2<kBf>(w0, w1);
+            p[n][2 * x + 1] = pack2<kBf>(w2, w3);
+            if (rest) {
+              pr[n][2 * x] = pack2_rest<kBf>(w0, w1, p[n][2 * x]);
+              pr[n][2 * x + 1] = pack2_rest<kBf>(w2, w3, p[n][2 * x + 1]);
+            }
           }
-        }
         st.l0 += sum_a;
         st.l1 += sum_b;
+
         // ------------------------------------------------------- values
-        if (!dead) dead = !warp_wait(&full[slot], phase, abort_flag);
+        if (!dead) dead = !all_wait(&full[bar], phase, abort_flag);
         const uint32_t vbase = ring + slot * C::kSlot;
-        // (the values' arrival says that the slot's last weights were read)
         if (weigh) {
+          // (the values' arrival says that the slot's last weights were read)
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
             sum_a += __shfl_xor_sync(0xffffffffu, sum_a, o);
@@ -735,29 +815,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             to[g + 8] = ref_b + lg2(sum_b);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&done[slot]);
+          if (lane == 0) mbar_arrive(&done[bar]);
         }
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          if (!act[n] || dead) continue;
-          const int ts = (tg * NS + n) * 16, t = t0 + ts + 2 * c;
-          const bool edge = t0 + ts + 16 > lim_lo;
+          if (!((act >> n) & 1u) || dead) continue;
           // B operands of output tiles 2u, 2u+1 (16-bit) or 4u .. 4u+3 (e4m3)
-          auto load_v = [&](int u, uint32_t* r) {
+          constexpr int TU = kByte ? 4 : 2;
+          auto load_v = [&](int u, uint32_t(&r)[2 * TU]) {
             if constexpr (!kByte) {
-              const int tok = ts + (lane & 15);
-              const int ch = u * 2 + (lane >> 4);
-              uint32_t x[4];
-              ldmatrix4_trans(vbase + tok * C::kRow + (ch >> 3) * C::kHalf +
-                                  (((ch & 7) ^ (tok & 7)) << 4), x);
-              r[0] = x[0]; r[1] = x[1]; r[2] = x[2]; r[3] = x[3];
+              ldmatrix4_trans(((vbase + voff0) ^ ((2 * u & 7) << 4)) + (u >> 2) * C::kHalf +
+                                  n * 16 * C::kRow, r);
             } else {
+              const uint32_t even = (vbase + voff0) ^ (u * 32), odd = (vbase + voff1) ^ (u * 32);
               uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t off = (ts + 2 * c + (k & 1) + (k >> 1) * 8) * C::kRow + u * 32 + g * 4;
-                w[k] = lds32(vbase + (off ^ ((off >> 3) & C::kSwizzle)));
-              }
+              w[0] = lds32(even + n * 16 * C::kRow);
+              w[1] = lds32(odd + n * 16 * C::kRow);
+              w[2] = lds32(even + (n * 16 + 8) * C::kRow);
+              w[3] = lds32(odd + (n * 16 + 8) * C::kRow);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const uint32_t x = __byte_perm(w[2 * k], w[2 * k + 1], 0x5140);
@@ -769,22 +844,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           };
-          constexpr int TU = kByte ? 4 : 2;       // output tiles of one load
-          if (!edge) {
+          if (inside || t0 + n * 16 + 16 <= lim_lo) {
 #pragma unroll
             for (int u = 0; u < NT / TU; ++u) {
               uint32_t r[2 * TU];
               load_v(u, r);
 #pragma unroll
-              for (int k = 0; k < TU; ++k) {
-                mma<kBf>(st.o[u * TU + k], p[n], r[2 * k], r[2 * k + 1]);
-                if constexpr (!kByte) mma<kBf>(st.o[u * TU + k], pr[n], r[2 * k], r[2 * k + 1]);
+              for (int k = 0; k < TU; ++k) mma<kBf>(st.o[u * TU + k], p[n], r[2 * k], r[2 * k + 1]);
+              if (rest) {
+#pragma unroll
+                for (int k = 0; k < TU; ++k)
+                  mma<kBf>(st.o[u * TU + k], pr[n], r[2 * k], r[2 * k + 1]);
               }
             }
           } else {
             // The last tokens: values that a row does not see do not meet its
             // weights (0 times NaN), so the rows of each query token take
             // their product with the values behind its limit zeroed.
+            const int t = t0 + n * 16 + 2 * c;
             for (int j = j_lo; j <= j_hi; ++j) {
               const int end = shift + j;
               const uint32_t k0 = below(t, end), k1 = below(t + 8, end);
@@ -796,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < TU; ++k) {
                   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                   mma<kBf>(x, p[n], r[2 * k] & k0, r[2 * k + 1] & k1);
-                  if constexpr (!kByte) mma<kBf>(x, pr[n], r[2 * k] & k0, r[2 * k + 1] & k1);
+                  if (rest) mma<kBf>(x, pr[n], r[2 * k] & k0, r[2 * k + 1] & k1);
                   if (ja == j) {
                     st.o[u * TU + k][0] += x[0];
                     st.o[u * TU + k][1] += x[1];
@@ -811,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        if (++slot == S) {
-          slot = 0;
+        if (lane == 0) mbar_arrive(&empty[bar]);
+        if (++slot == S) slot = 0;
+        if (++bar == NB) {
+          bar = 0;
           phase ^= 1;
         }
       }
@@ -840,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         consumer_sync();
         float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < TG; ++t) {
+        for (int t = 0; t < TJ; ++t) {
           ma = fmaxf(ma, ml[(t * RT + rt) * 16 + g].x);
           mb = fmaxf(mb, ml[(t * RT + rt) * 16 + g + 8].x);
         }
@@ -851,9 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = threadIdx.x;
           float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-          for (int t = 0; t < TG; ++t) top = fmaxf(top, ml[(t * RT + (r >> 4)) * 16 + (r & 15)].x);
+          for (int t = 0; t < TJ; ++t) top = fmaxf(top, ml[(t * RT + (r >> 4)) * 16 + (r & 15)].x);
 #pragma unroll
-          for (int t = 0; t < TG; ++t) {
+          for (int t = 0; t < TJ; ++t) {
             const float2 x = ml[(t * RT + (r >> 4)) * 16 + (r & 15)];
             if (top != -INFINITY) sum += x.y * ex2(x.x - top);
           }
@@ -899,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (r >= rows) continue;
             float x = 0.0f, y = 0.0f;
 #pragma unroll
-            for (int t = 0; t < TG; ++t) {
+            for (int t = 0; t < TJ; ++t) {
               const float2 v = *reinterpret_cast<const float2*>(
                   red + ((t * RT + q2) * 16 + (threadIdx.x >> 4)) * kRedStride + col);
               x += v.x;
@@ -945,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) st.o[n][e] = 0.0f;
         const int rla = rt * 16 + g, rlb = rla + 8;
-        for (int t = first_cta + tg; t <= last_cta; t += TG) {
+        for (int t = first_cta + tj; t <= last_cta; t += TJ) {
           const long long share_lo = misc->total * t / misc->grid;
           const int64_t from = 2 * t + (sg.pos > share_lo ? 1 : 0);
           const float2 none = make_float2(-INFINITY, 0.0f);
@@ -994,6 +1072,13 @@ cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const At
   cudaError_t e = cudaFuncSetAttribute(attention_kernel<KV, D, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
+  // The register split waits for what the launch does not have: never launch
+  // a build that got fewer.
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, attention_kernel<KV, D, RT>) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
