@@ -33,7 +33,8 @@ int check_attention(const mm3idx_attention_t* a) {
     return MM3IDX_ERR_INVALID_ARGUMENT;
   if (cdiv(a->max_seq_len, kBlock) >= 0xFFFF) return MM3IDX_ERR_TOO_MANY_BLOCKS;
   if (!(a->sm_scale > 0.0f) || !std::isfinite(a->sm_scale) || !(a->k_scale > 0.0f) ||
-      !std::isfinite(a->k_scale) || !std::isfinite(a->v_scale))
+      !std::isfinite(a->k_scale) || !std::isfinite(a->v_scale) ||
+      !std::isnormal(a->sm_scale * a->k_scale))
     return MM3IDX_ERR_INVALID_ARGUMENT;
   const bool half = a->q_type == MM3IDX_TYPE_BF16 || a->q_type == MM3IDX_TYPE_FP16;
   if (!half || (a->kv_type != a->q_type && a->kv_type != MM3IDX_TYPE_E4M3) ||

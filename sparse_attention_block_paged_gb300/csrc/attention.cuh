@@ -55,8 +55,8 @@ namespace mm3idx {
 namespace attn {
 
 constexpr int kConsumers = 8;                    // warps
-constexpr int kProducer = kConsumers;            // warp index
-constexpr int kWeigher = kConsumers + 1;         // warp that writes the tiles' weights
+constexpr int kProducer = kConsumers;            // warp of the keys' copies; the next: the values'
+constexpr int kWeigher = kConsumers + 2;         // warp that writes the tiles' weights
 constexpr int kThreads = (kConsumers + 4) * 32;  // three warpgroups, the last one half empty
 // Registers a thread: the launch's, and the split of them (setmaxnreg) between
 // the consumers' two warpgroups and the third, whose sum is the launch's.
@@ -85,7 +85,7 @@ struct Cfg {
   // Barriers per kind.  A slot that warps take turns at (every second tile is
   // one group's) has one barrier a group: a group that skips a slot's phase
   // cannot tell the phase before it from the phase after it by their parity.
-  static constexpr int kBars = kSlots / 2 % 2 ? 2 * kSlots : kSlots;
+  static constexpr int kBars = kSlots / 2 % 4 ? 2 * kSlots : kSlots;
   static constexpr uint32_t kSwizzle = kRow == 128 ? 0x70 : 0x30;
   static constexpr int oRed = kSlots * kSlot;
   static constexpr int oMl = oRed + kConsumers * 16 * kRedStride * 4;
@@ -114,6 +114,13 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 // Positions of one task (request, kv head, 64-row tile) in the list.
 __device__ __forceinline__ long long task_slots(int len) {
   return len > 0 ? tiles_of(len) + kSegCost : 0;
+}
+
+// a / b of non-negative numbers, in 32 bits where they allow it (a 64-bit
+// division takes several hundred cycles).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 __device__ __forceinline__ void consumer_sync() {
@@ -154,7 +161,8 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
   const long long most = total / kMinShare;
   const int G = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
   const long long c = blockIdx.x;
-  const long long lo = c < G ? total * c / G : 0, hi = c < G ? total * (c + 1) / G : 0;
+  const long long lo = c < G ? quotient(total * c, G) : 0;
+  const long long hi = c < G ? quotient(total * (c + 1), G) : 0;
   if (tid == 0) {
     m->lo = lo;
     m->hi = hi;
@@ -170,12 +178,12 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
     const long long one = task_slots(request_len(a, i));
     const long long all = one * a.tasks;
     if (has_lo && P <= lo && lo < P + all) {
-      const int h = static_cast<int>((lo - P) / one);
+      const int h = static_cast<int>(quotient(lo - P, one));
       m->t0 = i * a.tasks + h;
       m->p0 = P + h * one;
     }
     if (has_hi && P <= hi - 1 && hi - 1 < P + all) {
-      const int h = static_cast<int>((hi - 1 - P) / one);
+      const int h = static_cast<int>(quotient(hi - 1 - P, one));
       m->tl = i * a.tasks + h;
       m->pl = P + h * one;
     }
@@ -234,7 +242,17 @@ struct Walker {
 
 // The CTA whose share holds position x.
 __device__ __forceinline__ int cta_of(long long x, long long total, int grid) {
-  return static_cast<int>(((x + 1) * grid - 1) / total);
+  return static_cast<int>(quotient((x + 1) * grid - 1, total));
+}
+
+// Arrivals at a task: the count before this one, back to 0 after `wrap`.
+__device__ __forceinline__ int ticket(unsigned int* p, unsigned int wrap) {
+  unsigned int old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(p), "r"(wrap)
+               : "memory");
+  return static_cast<int>(old);
 }
 
 // ------------------------------------------------------------- instructions
@@ -282,14 +300,12 @@ template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
   if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -388,7 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kByte = C::kByte;
   constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
   constexpr int TJ = kConsumers / RT;               // warps that share a row tile
-  constexpr int ALT = RT == 1 ? 2 : 1;              // a warp takes every ALT-th tile
+  // A warp takes every ALT-th tile, so that it has 32 tokens of a tile with
+  // 16-bit D = 128 and 64 where a tile is half the bytes (or RT = 4).
+  constexpr int ALT = (C::kSlot == 32768 ? 2 : 4) / RT > 1 ? (C::kSlot == 32768 ? 2 : 4) / RT : 1;
   static_assert(NB / 2 % ALT == 0, "a barrier belongs to one group of warps");
   constexpr int TG = TJ / ALT;                      // token groups of a tile
   constexpr int NS = 8 / TG;                        // 16-token slices of a warp
@@ -434,71 +452,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kProducer) {
-    // ---------------------------------------------------------- producer
-    const int per = kTile >> a.page_shift;       // pages of a tile
-    const int batch = 32 / per;                  // tiles whose page ids one register holds
-    const int box = C::kRow << a.page_shift;
-    uint32_t slot = 0, bar = 0, items = 0;        // items: copies of a tile's keys or values
-    uint32_t wait = 0, wait_phase = 0;            // the barrier of the item S before
-    bool ok = true;
-    while (ok && walk.next(a, sg)) {
-      const int head = (sg.task % a.tasks) / a.row_tiles;
-      const int32_t* table = a.table + static_cast<int64_t>(sg.req) * a.table_stride;
-      const int pages = (sg.len + (1 << a.page_shift) - 1) >> a.page_shift;
-      auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
-      int cur = ids_from(sg.b0 * per), nxt = ids_from(sg.b0 * per + 32), k = 0;
-      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++k) {
-        if (k == batch) {
-          k = 0;
-          cur = nxt;
-          nxt = ids_from(b * per + 32);
-        }
-        const int id = __shfl_sync(0xffffffffu, cur, (k * per + lane) & 31);
-        const bool need = lane < per && b * per + lane < pages;
-        const uint32_t good = __ballot_sync(0xffffffffu, need && id >= 0 && id < a.num_pages);
-        if (__ballot_sync(0xffffffffu, need) != good && lane == 0)
-          atomicOr(a.status, MM3IDX_DEV_BAD_PAGE);
-        const int p = lane / C::kHalves, half = lane % C::kHalves;
-        const int page = __shfl_sync(0xffffffffu, id, p);
-        const bool issue = lane < per * C::kHalves && ((good >> p) & 1u);
-        const uint32_t bytes = __popc(good) * C::kHalves * box;
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          if (items >= S) {
+    if (warp < kWeigher) {
+      // ------------------------------------------- producers: keys, values
+      const int kv = warp - kProducer;
+      const CUtensorMap* map = kv ? &vmap : &kmap;
+      const int per = kTile >> a.page_shift;       // pages of a tile
+      const int batch = 32 / per;                  // tiles whose page ids one register holds
+      const int box = C::kRow << a.page_shift;
+      uint32_t slot = kv, bar = kv, items = 0;
+      uint32_t wait = kv, wait_phase = 0;          // the barrier of the tile S / 2 before
+      bool ok = true;
+      while (ok && walk.next(a, sg)) {
+        const int head = (sg.task % a.tasks) / a.row_tiles;
+        const int32_t* table = a.table + static_cast<int64_t>(sg.req) * a.table_stride;
+        const int pages = (sg.len + (1 << a.page_shift) - 1) >> a.page_shift;
+        auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
+        int cur = ids_from(sg.b0 * per), nxt = ids_from(sg.b0 * per + 32), k = 0;
+        for (int b = sg.b0; b < sg.b1; ++b, ++k) {
+          if (k == batch) {
+            k = 0;
+            cur = nxt;
+            nxt = ids_from(b * per + 32);
+          }
+          const int id = __shfl_sync(0xffffffffu, cur, (k * per + lane) & 31);
+          const bool need = lane < per && b * per + lane < pages;
+          const uint32_t good = __ballot_sync(0xffffffffu, need && id >= 0 && id < a.num_pages);
+          if (__ballot_sync(0xffffffffu, need) != good && lane == 0)
+            atomicOr(a.status, MM3IDX_DEV_BAD_PAGE);
+          const int p = lane / C::kHalves, half = lane % C::kHalves;
+          const int page = __shfl_sync(0xffffffffu, id, p);
+          const bool issue = lane < per * C::kHalves && ((good >> p) & 1u);
+          const uint32_t bytes = __popc(good) * C::kHalves * box;
+          if (items >= S / 2) {
             ok = warp_wait(&empty[wait], wait_phase, abort_flag);
             if (!ok) break;
-            if (++wait == NB) {
-              wait = 0;
+            wait += 2;
+            if (wait >= NB) {
+              wait = kv;
               wait_phase ^= 1;
             }
           }
           if (lane == 0) {
-            mask[slot] = good;
+            if (kv == 0) mask[slot] = good;
             if (bytes) mbar_arrive_expect_tx(&full[bar], bytes);
             else mbar_arrive(&full[bar]);
           }
           __syncwarp();
           if (issue)
-            tma_load_4d(smem_u32(sm) + slot * C::kSlot + half * C::kHalf + p * box,
-                        kv ? &vmap : &kmap, &full[bar], half * (C::kRow / C::kElem), 0, head,
-                        page);
+            tma_load_4d(smem_u32(sm) + slot * C::kSlot + half * C::kHalf + p * box, map, &full[bar],
+                        half * (C::kRow / C::kElem), 0, head, page);
           ++items;
-          if (++slot == S) slot = 0;
-          if (++bar == NB) bar = 0;
+          slot += 2;
+          if (slot >= S) slot = kv;
+          bar += 2;
+          if (bar >= NB) bar = kv;
         }
       }
-    }
-    // Every copy that was started lands before the CTA can exit.
-    if (lane == 0) {
-      const uint32_t pending = items < S ? items : S;
-      for (uint32_t k = 0; k < pending; ++k) {
-        const uint32_t idx = items - 1 - k;
-        int dummy = 0;
-        mbar_wait(&full[idx % NB], (idx / NB) & 1, &dummy);
+      // Every copy that was started lands before the CTA can exit.
+      if (lane == 0) {
+        const uint32_t pending = items < S / 2 ? items : S / 2;
+        for (uint32_t k = 0; k < pending; ++k) {
+          const uint32_t idx = 2 * (items - 1 - k);
+          int dummy = 0;
+          mbar_wait(&full[idx % NB + kv], (idx / NB) & 1, &dummy);
+        }
       }
-    }
-    __syncwarp();
+      __syncwarp();
     } else if (warp == kWeigher) {
     // ------------------------------------- log-sum-exp of each tile's rows
     if (weigh) {
@@ -580,15 +599,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    while (walk.next(a, sg)) {
+    const int R = a.group * a.query_len;
+    // The queries of a segment, as they lie in memory: 16-bit caches, the A
+    // operands; e4m3, D/4 elements from c D/4 of rows g and g + 8.
+    uint32_t q[KS][4];
+    auto load_queries = [&](const Segment& s) {
+      const int sub = s.task % a.tasks, head = sub / a.row_tiles;
+      const int ra = (sub % a.row_tiles) * 64 + rt * 16 + g, rb = ra + 8;
+      const uint16_t* base = static_cast<const uint16_t*>(a.q) +
+                             static_cast<int64_t>(s.req) * a.query_len * a.q_tok +
+                             static_cast<int64_t>(head) * a.group * a.q_head;
+      auto row_at = [&](int r) {
+        r = min(r, R - 1);
+        return base + r / a.group * a.q_tok + r % a.group * a.q_head;
+      };
+      const uint16_t* qa = row_at(ra);
+      const uint16_t* qb = row_at(rb);
+      const bool va = ra < R, vb = rb < R;
+      if constexpr (!kByte) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int d = ks * 16 + 2 * c;
+          q[ks][0] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d)) : 0u;
+          q[ks][1] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d)) : 0u;
+          q[ks][2] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d + 8)) : 0u;
+          q[ks][3] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d + 8)) : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < KS / 2; ++u) {
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          const uint4 x = va ? __ldg(reinterpret_cast<const uint4*>(qa + c * (D / 4)) + u) : none;
+          const uint4 y = vb ? __ldg(reinterpret_cast<const uint4*>(qb + c * (D / 4)) + u) : none;
+          q[2 * u][0] = x.x; q[2 * u][1] = y.x; q[2 * u][2] = x.y; q[2 * u][3] = y.y;
+          q[2 * u + 1][0] = x.z; q[2 * u + 1][1] = y.z; q[2 * u + 1][2] = x.w; q[2 * u + 1][3] = y.w;
+        }
+      }
+    };
+
+    bool more = walk.next(a, sg);
+    if (more) load_queries(sg);
+    while (more) {
       const int sub = sg.task % a.tasks;                   // kv head and 64-row tile
       const int head = sub / a.row_tiles, row0 = (sub % a.row_tiles) * 64;
-      const int R = a.group * a.query_len;
       const int rows = min(64, R - row0);                  // of this task
       const int64_t tok0 = static_cast<int64_t>(sg.req) * a.query_len;
       // Row r of the kv head is query token r / group, query head r % group.
       const int ra = row0 + rt * 16 + g, rb = ra + 8;
-      const bool va = ra < R, vb = rb < R;
       const int ja = min(ra, R - 1) / a.group, jb = min(rb, R - 1) / a.group;
       const int shift = sg.len - a.query_len + 1;          // query token j sees [0, shift + j)
       const int j_lo = min(row0 + rt * 16, R - 1) / a.group;
@@ -597,66 +654,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
       const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
 
-      // Queries.
-      uint32_t q[KS][4];
       float sc_a = a.scale * kLog2e, sc_b = sc_a;
-      {
-        const uint16_t* qa = static_cast<const uint16_t*>(a.q) + (tok0 + ja) * a.q_tok +
-                             static_cast<int64_t>(head * a.group + min(ra, R - 1) % a.group) * a.q_head;
-        const uint16_t* qb = static_cast<const uint16_t*>(a.q) + (tok0 + jb) * a.q_tok +
-                             static_cast<int64_t>(head * a.group + min(rb, R - 1) % a.group) * a.q_head;
-        if constexpr (!kByte) {
+      if constexpr (kByte) {
+        // fp16 queries, each row scaled by the power of two that brings its
+        // largest element into [1, 2) (not at all where that is 0)
+        float top[2] = {0.0f, 0.0f}, down[2];
+        auto floats = [&](uint32_t w) {
+          if (a.q_type == MM3IDX_TYPE_BF16)
+            return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          return __half22float2(*reinterpret_cast<const __half2*>(&w));
+        };
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const int d = ks * 16 + 2 * c;
-            q[ks][0] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d)) : 0u;
-            q[ks][1] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d)) : 0u;
-            q[ks][2] = va ? __ldg(reinterpret_cast<const uint32_t*>(qa + d + 8)) : 0u;
-            q[ks][3] = vb ? __ldg(reinterpret_cast<const uint32_t*>(qb + d + 8)) : 0u;
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = floats(q[ks][e]);
+            top[e & 1] = max3(top[e & 1], fabsf(f.x), fabsf(f.y));
           }
-        } else {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint16_t* src = (x ? qb : qa) + c * (D / 4);
-            const bool valid = x ? vb : va;
-            float f[D / 4];
-            float top = 0.0f;
-#pragma unroll
-            for (int u = 0; u < D / 32; ++u) {
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (valid) w = __ldg(reinterpret_cast<const uint4*>(src) + u);
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float lo, hi;
-                if (a.q_type == MM3IDX_TYPE_BF16) {
-                  lo = __uint_as_float(ww[e] << 16);
-                  hi = __uint_as_float(ww[e] & 0xffff0000u);
-                } else {
-                  const __half2 h = *reinterpret_cast<const __half2*>(&ww[e]);
-                  lo = __low2float(h);
-                  hi = __high2float(h);
-                }
-                f[u * 8 + 2 * e] = lo;
-                f[u * 8 + 2 * e + 1] = hi;
-                top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
-              }
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e of the row's largest element (1 where that is 0)
-            const int e = min(static_cast<int>(__float_as_uint(top) >> 23), 253);
-            const float down = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-            const float up = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e) << 23);
-            if (x) sc_b *= up;
-            else sc_a *= up;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              q[ks][x] = pack2<false>(f[4 * ks] * down, f[4 * ks + 1] * down);
-              q[ks][2 + x] = pack2<false>(f[4 * ks + 2] * down, f[4 * ks + 3] * down);
-            }
-          }
+        for (int x = 0; x < 2; ++x) {
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+          const int e = min(static_cast<int>(__float_as_uint(top[x]) >> 23), 253);
+          down[x] = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          const float up = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+          if (x) sc_b *= up;
+          else sc_a *= up;
         }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = floats(q[ks][e]);
+            q[ks][e] = pack2<false>(f.x * down[e & 1], f.y * down[e & 1]);
+          }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -666,62 +697,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       st.l0 = st.l1 = 0.0f;
 
       for (int b = sg.b0; b < sg.b1; ++b) {
+        auto next_slot = [&] {      // to the next tile's keys
+          if (++slot >= S) slot = 0;
+          if (++bar >= NB) {
+            bar = 0;
+            phase ^= 1;
+          }
+        };
         if constexpr (ALT > 1) {
           const bool mine = turn == alt;
           turn = (turn + 1) % ALT;
           if (!mine) {
-            slot += 2;
-            if (slot == S) slot = 0;
-            bar += 2;
-            if (bar == NB) {
-              bar = 0;
-              phase ^= 1;
-            }
+            ++slot;
+            ++bar;
+            next_slot();
             continue;
           }
         }
         // ------------------------------------------------------- scores
         if (!dead) dead = !all_wait(&full[bar], phase, abort_flag);
+        const bool live = !idle && !dead;
         const uint32_t pages = mask[slot];
-        const uint32_t kbase = ring + slot * C::kSlot + koff;
         const int t0 = b * kTile + static_cast<int>(first);
-        // Slices that any row of this warp sees; in a tile that all rows see
-        // whole, all of them.
-        const bool inside = !idle && !dead && t0 + NS * 16 <= lim_lo &&
+        // Whether every row sees every token of this warp's part.
+        const bool inside = t0 + NS * 16 <= lim_lo &&
                             pages == (0xffffffffu >> (32 - (kTile >> a.page_shift)));
-        uint32_t act = (1u << NS) - 1u;
-        if (!inside) {
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-            if (idle || dead || t0 + n * 16 >= lim_hi ||
-                !((pages >> ((first + n * 16) >> a.page_shift)) & 1u))
-              act &= ~(1u << n);
-        }
         float s[NS][2][4];
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.0f;
-          if (!((act >> n) & 1u)) continue;
+        if (live) {
+          // All slices at once: 2 NS chains of products.  What lies behind the
+          // last token may be anything; its scores are replaced below.
+          const uint32_t kbase = ring + slot * C::kSlot + koff;
           if constexpr (!kByte) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              uint32_t r[4];
-              ldmatrix4((kbase ^ ((2 * ks & 7) << 4)) + (ks >> 2) * C::kHalf + n * 16 * C::kRow, r);
-              mma<kBf>(s[n][0], q[ks], r[0], r[1]);
-              mma<kBf>(s[n][1], q[ks], r[2], r[3]);
+              uint32_t r[NS][4];
+#pragma unroll
+              for (int n = 0; n < NS; ++n)
+                ldmatrix4((kbase ^ ((2 * ks & 7) << 4)) + (ks >> 2) * C::kHalf + n * 16 * C::kRow,
+                          r[n]);
+#pragma unroll
+              for (int n = 0; n < NS; ++n) {
+                mma<kBf>(s[n][0], q[ks], r[n][0], r[n][1]);
+                mma<kBf>(s[n][1], q[ks], r[n][2], r[n][3]);
+              }
             }
           } else {
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
+              uint4 w[NS][2];
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint4 w = lds128((kbase ^ (16 * u)) + (n * 16 + 8 * x) * C::kRow);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  mma<false>(s[n][x], q[u * 4 + e], widen_lo(ww[e]), widen_hi(ww[e]));
-              }
+                for (int x = 0; x < 2; ++x)
+                  w[n][x] = lds128((kbase ^ (16 * u)) + (n * 16 + 8 * x) * C::kRow);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint32_t k4 = e == 0 ? w[n][x].x : e == 1 ? w[n][x].y
+                                        : e == 2 ? w[n][x].z : w[n][x].w;
+                    mma<false>(s[n][x], q[u * 4 + e], widen_lo(k4), widen_hi(k4));
+                  }
             }
           }
         }
@@ -731,11 +773,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++bar;
 
         // ------------------------------------------------------ softmax
-        if (!inside) {
+        uint32_t act = (1u << NS) - 1u;          // slices with a token that some row sees
+        if (!inside || !live) {
           // tokens that a row does not see: -inf before the (positive) scale
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
-            const bool on = (act >> n) & 1u;
+            const bool on = live && t0 + n * 16 < lim_hi &&
+                            ((pages >> ((first + n * 16) >> a.page_shift)) & 1u);
+            if (!on) act &= ~(1u << n);
             const int t = t0 + n * 16 + 2 * c;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -817,63 +862,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&done[bar]);
         }
+        // B operands of output tiles 2u, 2u+1 (16-bit) or 4u .. 4u+3 (e4m3),
+        // 16 tokens from row `at` of this warp's part
+        constexpr int TU = kByte ? 4 : 2, NU = NT / TU, UG = kByte ? 2 : 4;
+        auto load_v = [&](int u, int at, uint32_t(&r)[2 * TU]) {
+          if constexpr (!kByte) {
+            ldmatrix4_trans(((vbase + voff0) ^ ((2 * u & 7) << 4)) + (u >> 2) * C::kHalf +
+                                at * C::kRow, r);
+          } else {
+            const uint32_t even = (vbase + voff0) ^ (u * 32), odd = (vbase + voff1) ^ (u * 32);
+            uint32_t w[4];
+            w[0] = lds32(even + at * C::kRow);
+            w[1] = lds32(odd + at * C::kRow);
+            w[2] = lds32(even + (at + 8) * C::kRow);
+            w[3] = lds32(odd + (at + 8) * C::kRow);
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          if (!((act >> n) & 1u) || dead) continue;
-          // B operands of output tiles 2u, 2u+1 (16-bit) or 4u .. 4u+3 (e4m3)
-          constexpr int TU = kByte ? 4 : 2;
-          auto load_v = [&](int u, uint32_t(&r)[2 * TU]) {
-            if constexpr (!kByte) {
-              ldmatrix4_trans(((vbase + voff0) ^ ((2 * u & 7) << 4)) + (u >> 2) * C::kHalf +
-                                  n * 16 * C::kRow, r);
-            } else {
-              const uint32_t even = (vbase + voff0) ^ (u * 32), odd = (vbase + voff1) ^ (u * 32);
-              uint32_t w[4];
-              w[0] = lds32(even + n * 16 * C::kRow);
-              w[1] = lds32(odd + n * 16 * C::kRow);
-              w[2] = lds32(even + (n * 16 + 8) * C::kRow);
-              w[3] = lds32(odd + (n * 16 + 8) * C::kRow);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t x = __byte_perm(w[2 * k], w[2 * k + 1], 0x5140);
-                const uint32_t y = __byte_perm(w[2 * k], w[2 * k + 1], 0x7362);
-                r[0 + k] = widen_lo(x);
-                r[2 + k] = widen_hi(x);
-                r[4 + k] = widen_lo(y);
-                r[6 + k] = widen_hi(y);
-              }
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = __byte_perm(w[2 * k], w[2 * k + 1], 0x5140);
+              const uint32_t y = __byte_perm(w[2 * k], w[2 * k + 1], 0x7362);
+              r[0 + k] = widen_lo(x);
+              r[2 + k] = widen_hi(x);
+              r[4 + k] = widen_lo(y);
+              r[6 + k] = widen_hi(y);
             }
-          };
-          if (inside || t0 + n * 16 + 16 <= lim_lo) {
+          }
+        };
+        if (live && inside) {
+          // Two slices and UG loads at a time, products on one accumulator
+          // eight apart.
 #pragma unroll
-            for (int u = 0; u < NT / TU; ++u) {
-              uint32_t r[2 * TU];
-              load_v(u, r);
+          for (int n = 0; n < NS; n += 2)
 #pragma unroll
-              for (int k = 0; k < TU; ++k) mma<kBf>(st.o[u * TU + k], p[n], r[2 * k], r[2 * k + 1]);
+            for (int u0 = 0; u0 < NU; u0 += UG) {
+              uint32_t r[2][UG][2 * TU];
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int u = 0; u < UG; ++u) load_v(u0 + u, (n + x) * 16, r[x][u]);
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int u = 0; u < UG; ++u)
+#pragma unroll
+                  for (int k = 0; k < TU; ++k)
+                    mma<kBf>(st.o[(u0 + u) * TU + k], p[n + x], r[x][u][2 * k], r[x][u][2 * k + 1]);
               if (rest) {
 #pragma unroll
-                for (int k = 0; k < TU; ++k)
-                  mma<kBf>(st.o[u * TU + k], pr[n], r[2 * k], r[2 * k + 1]);
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                  for (int u = 0; u < UG; ++u)
+#pragma unroll
+                    for (int k = 0; k < TU; ++k)
+                      mma<kBf>(st.o[(u0 + u) * TU + k], pr[n + x], r[x][u][2 * k],
+                               r[x][u][2 * k + 1]);
               }
             }
-          } else {
-            // The last tokens: values that a row does not see do not meet its
-            // weights (0 times NaN), so the rows of each query token take
-            // their product with the values behind its limit zeroed.
+        } else if (live) {
+          // The last tokens, or a page outside the cache: values that a row
+          // does not see do not meet its weights (0 times NaN), so the rows of
+          // each query token take their product with the values behind its
+          // limit zeroed.
+#pragma unroll 1
+          for (int n = 0; n < NS; ++n) {
+            if (!((act >> n) & 1u)) continue;
+            uint32_t pn[4], prn[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < NS; ++x)
+              if (x == n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  pn[e] = p[x][e];
+                  if (rest) prn[e] = pr[x][e];
+                }
+              }
             const int t = t0 + n * 16 + 2 * c;
+#pragma unroll 1
             for (int j = j_lo; j <= j_hi; ++j) {
               const int end = shift + j;
               const uint32_t k0 = below(t, end), k1 = below(t + 8, end);
 #pragma unroll
-              for (int u = 0; u < NT / TU; ++u) {
+              for (int u = 0; u < NU; ++u) {
                 uint32_t r[2 * TU];
-                load_v(u, r);
+                load_v(u, n * 16, r);
 #pragma unroll
                 for (int k = 0; k < TU; ++k) {
                   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma<kBf>(x, p[n], r[2 * k] & k0, r[2 * k + 1] & k1);
-                  if (rest) mma<kBf>(x, pr[n], r[2 * k] & k0, r[2 * k + 1] & k1);
+                  mma<kBf>(x, pn, r[2 * k] & k0, r[2 * k + 1] & k1);
+                  if (rest) mma<kBf>(x, prn, r[2 * k] & k0, r[2 * k + 1] & k1);
                   if (ja == j) {
                     st.o[u * TU + k][0] += x[0];
                     st.o[u * TU + k][1] += x[1];
@@ -889,176 +964,185 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[bar]);
-        if (++slot == S) slot = 0;
-        if (++bar == NB) {
-          bar = 0;
-          phase ^= 1;
-        }
+        next_slot();
       }
+      // The next segment's queries are under way during the join.
+      Segment after;
+      more = walk.next(a, after);
+      if (more) load_queries(after);
 
       // ------------------------------------------------ join of the warps
-      // Quad sums of l, then the warps' triples through shared memory.  A
-      // first pass writes the result, or this CTA's partial one; the last CTA
-      // of a shared task then joins the partial ones in a second pass.
+      // Quad sums of l, then the warps' triples through shared memory, 32
+      // columns at a time: the result, or this CTA's partial one.
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
         st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
       }
       const bool whole = sg.b0 == 0 && sg.b1 == sg.nb;
-      const long long pb = sg.pos + kSegCost;
-      const int first_cta = cta_of(pb, misc->total, misc->grid);
-      const int last_cta = cta_of(pb + sg.nb - 1, misc->total, misc->grid);
-      bool final = whole;
-      for (int pass = 0; pass < 2; ++pass) {
-        if (c == 0) {
-          ml[warp * 16 + g] = make_float2(st.m0, st.l0);
-          ml[warp * 16 + g + 8] = make_float2(st.m1, st.l1);
-        }
-        consumer_sync();
-        float ma = -INFINITY, mb = -INFINITY;
+      if (c == 0) {
+        ml[warp * 16 + g] = make_float2(st.m0, st.l0);
+        ml[warp * 16 + g + 8] = make_float2(st.m1, st.l1);
+      }
+      consumer_sync();
+      float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < TJ; ++t) {
+        ma = fmaxf(ma, ml[(t * RT + rt) * 16 + g].x);
+        mb = fmaxf(mb, ml[(t * RT + rt) * 16 + g + 8].x);
+      }
+      const float fa = ma == -INFINITY ? 0.0f : ex2(st.m0 - ma);
+      const float fb = mb == -INFINITY ? 0.0f : ex2(st.m1 - mb);
+      const int64_t part = 2 * blockIdx.x + (sg.pos > walk.lo ? 1 : 0);
+      const int heads = a.kv_heads * a.group;
+      if (threadIdx.x < RT * 16) {
+        const int r = threadIdx.x;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TJ; ++t) top = fmaxf(top, ml[(t * RT + (r >> 4)) * 16 + (r & 15)].x);
 #pragma unroll
         for (int t = 0; t < TJ; ++t) {
-          ma = fmaxf(ma, ml[(t * RT + rt) * 16 + g].x);
-          mb = fmaxf(mb, ml[(t * RT + rt) * 16 + g + 8].x);
+          const float2 x = ml[(t * RT + (r >> 4)) * 16 + (r & 15)];
+          if (top != -INFINITY) sum += x.y * ex2(x.x - top);
         }
-        const float fa = ma == -INFINITY ? 0.0f : ex2(st.m0 - ma);
-        const float fb = mb == -INFINITY ? 0.0f : ex2(st.m1 - mb);
-        const int slot_id = 2 * blockIdx.x + (sg.pos > walk.lo ? 1 : 0);
-        if (threadIdx.x < RT * 16) {
-          const int r = threadIdx.x;
-          float top = -INFINITY, sum = 0.0f;
+        if (r < rows) {
+          if (whole) {
+            const int64_t row = tok0 + (row0 + r) / a.group;
+            const int h = head * a.group + (row0 + r) % a.group;
+            const float lse2 = sum == 0.0f ? -INFINITY : top + lg2(sum);
+            if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
+            if (weigh) a.row_lse[row * heads + h] = lse2;
+          } else {
+            __stcg(a.part_ml + part * 64 + r, make_float2(top, sum));
+          }
+        }
+        fin[r].x = sum == 0.0f ? 0.0f : a.v_scale / sum;
+      }
+      // This thread's two columns of rows q2 * 16 + tid / 16.
+      uint16_t* out_at[RT];
 #pragma unroll
-          for (int t = 0; t < TJ; ++t) top = fmaxf(top, ml[(t * RT + (r >> 4)) * 16 + (r & 15)].x);
+      for (int q2 = 0; q2 < RT; ++q2) {
+        const int r = min(q2 * 16 + static_cast<int>(threadIdx.x >> 4), rows - 1);
+        out_at[q2] = static_cast<uint16_t*>(a.out) + (tok0 + (row0 + r) / a.group) * a.o_tok +
+                     (head * a.group + (row0 + r) % a.group) * a.o_head + (threadIdx.x & 15) * 2;
+      }
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        float* mine = red + warp * 16 * kRedStride;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+          if (u != ch) continue;             // static register indices
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float(&o)[4] = st.o[u * 4 + k];
+            if constexpr (!kByte) {
+              *reinterpret_cast<float2*>(mine + g * kRedStride + 8 * k + 2 * c) =
+                  make_float2(o[0] * fa, o[1] * fa);
+              *reinterpret_cast<float2*>(mine + (g + 8) * kRedStride + 8 * k + 2 * c) =
+                  make_float2(o[2] * fb, o[3] * fb);
+            } else {
+              mine[g * kRedStride + 8 * c + k] = o[0] * fa;
+              mine[g * kRedStride + 8 * c + 4 + k] = o[1] * fa;
+              mine[(g + 8) * kRedStride + 8 * c + k] = o[2] * fb;
+              mine[(g + 8) * kRedStride + 8 * c + 4 + k] = o[3] * fb;
+            }
+          }
+        }
+        consumer_sync();
+#pragma unroll
+        for (int q2 = 0; q2 < RT; ++q2) {
+          const int r = q2 * 16 + (threadIdx.x >> 4), col = (threadIdx.x & 15) * 2;
+          if (r >= rows) continue;
+          float2 v[TJ];
+#pragma unroll
+          for (int t = 0; t < TJ; ++t)
+            v[t] = *reinterpret_cast<const float2*>(
+                red + ((t * RT + q2) * 16 + (threadIdx.x >> 4)) * kRedStride + col);
+          float x = 0.0f, y = 0.0f;
 #pragma unroll
           for (int t = 0; t < TJ; ++t) {
-            const float2 x = ml[(t * RT + (r >> 4)) * 16 + (r & 15)];
-            if (top != -INFINITY) sum += x.y * ex2(x.x - top);
+            x += v[t].x;
+            y += v[t].y;
           }
-          if (final) {
-            if (r < rows) {
-              const int64_t row = tok0 + (row0 + r) / a.group;
-              const int h = head * a.group + (row0 + r) % a.group;
-              const float lse2 = sum == 0.0f ? -INFINITY : top + lg2(sum);
-              if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
-              if (weigh) a.row_lse[row * a.kv_heads * a.group + h] = lse2;
-            }
-            fin[r].x = sum == 0.0f ? 0.0f : a.v_scale / sum;
-          } else if (r < rows) {
-            __stcg(a.part_ml + static_cast<int64_t>(slot_id) * 64 + r, make_float2(top, sum));
+          if (whole) {
+            const float f = fin[r].x;
+            *reinterpret_cast<uint32_t*>(out_at[q2] + ch * 32) =
+                a.q_type == MM3IDX_TYPE_BF16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
+          } else {
+            __stcg(reinterpret_cast<float2*>(a.part_o + (part * 64 + r) * D + ch * 32 + col),
+                   make_float2(x, y));
           }
         }
+        consumer_sync();
+      }
+      if (!whole) {
+        // Publish; the last CTA of the task joins the partial results.  (The
+        // barrier orders the CTA's stores before thread 0's release.)
+        const long long pb = sg.pos + kSegCost;
+        const int first_cta = cta_of(pb, misc->total, misc->grid);
+        const int parts = cta_of(pb + sg.nb - 1, misc->total, misc->grid) - first_cta + 1;
+        if (threadIdx.x == 0)
+          misc->last = !dead && ticket(a.tickets + sg.task, parts - 1) == parts - 1;
+        consumer_sync();
+        if (misc->last) {
+          // A thread takes four columns of a row, the partial results in
+          // order, eight loads in flight.
+          const int64_t p0 = 2 * first_cta + (sg.pos > quotient(misc->total * first_cta, misc->grid));
+          auto part_of = [&](int t) { return t == 0 ? p0 : 2 * static_cast<int64_t>(first_cta + t); };
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          float* mine = red + warp * 16 * kRedStride;
+          for (int unit = threadIdx.x; unit < rows * (D / 4); unit += kConsumers * 32) {
+            const int r = unit / (D / 4), col = unit % (D / 4) * 4;
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int t0 = 0; t0 < parts; t0 += 8) {
+              float2 x[8];
+              float4 v[8];
 #pragma unroll
-          for (int u = 0; u < D / 32; ++u) {
-            if (u != ch) continue;             // static register indices
+              for (int k = 0; k < 8; ++k) {
+                if (t0 + k < parts) {
+                  const int64_t at = part_of(t0 + k) * 64 + r;
+                  x[k] = __ldcg(a.part_ml + at);
+                  v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+                } else {
+                  x[k] = make_float2(-INFINITY, 0.0f);
+                  v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+              }
+              float top = m;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float(&o)[4] = st.o[u * 4 + k];
-              if constexpr (!kByte) {
-                *reinterpret_cast<float2*>(mine + g * kRedStride + 8 * k + 2 * c) =
-                    make_float2(o[0] * fa, o[1] * fa);
-                *reinterpret_cast<float2*>(mine + (g + 8) * kRedStride + 8 * k + 2 * c) =
-                    make_float2(o[2] * fb, o[3] * fb);
-              } else {
-                mine[g * kRedStride + 8 * c + k] = o[0] * fa;
-                mine[g * kRedStride + 8 * c + 4 + k] = o[1] * fa;
-                mine[(g + 8) * kRedStride + 8 * c + k] = o[2] * fb;
-                mine[(g + 8) * kRedStride + 8 * c + 4 + k] = o[3] * fb;
+              for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+              if (top == -INFINITY) continue;
+              const float f = ex2(m - top);
+              m = top;
+              l *= f;
+              o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float w = ex2(x[k].x - top);
+                l += x[k].y * w;
+                o.x += v[k].x * w; o.y += v[k].y * w; o.z += v[k].z * w; o.w += v[k].w * w;
               }
             }
-          }
-          consumer_sync();
-#pragma unroll
-          for (int q2 = 0; q2 < RT; ++q2) {
-            const int r = q2 * 16 + (threadIdx.x >> 4), col = (threadIdx.x & 15) * 2;
-            if (r >= rows) continue;
-            float x = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int t = 0; t < TJ; ++t) {
-              const float2 v = *reinterpret_cast<const float2*>(
-                  red + ((t * RT + q2) * 16 + (threadIdx.x >> 4)) * kRedStride + col);
-              x += v.x;
-              y += v.y;
+            const int64_t row = tok0 + (row0 + r) / a.group;
+            const int h = head * a.group + (row0 + r) % a.group;
+            const float f = l == 0.0f ? 0.0f : a.v_scale / l;
+            uint2 w;
+            if (a.q_type == MM3IDX_TYPE_BF16)
+              w = make_uint2(pack2<true>(o.x * f, o.y * f), pack2<true>(o.z * f, o.w * f));
+            else
+              w = make_uint2(pack2<false>(o.x * f, o.y * f), pack2<false>(o.z * f, o.w * f));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
+                                      col) = w;
+            if (col == 0) {
+              const float lse2 = l == 0.0f ? -INFINITY : m + lg2(l);
+              if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
+              if (weigh) a.row_lse[row * heads + h] = lse2;
             }
-            if (final) {
-              const float f = fin[r].x;
-              const int64_t row = tok0 + (row0 + r) / a.group;
-              const int h = head * a.group + (row0 + r) % a.group;
-              uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
-                              ch * 32 + col;
-              *reinterpret_cast<uint32_t*>(out) = a.q_type == MM3IDX_TYPE_BF16
-                                                      ? pack2<true>(x * f, y * f)
-                                                      : pack2<false>(x * f, y * f);
-            } else {
-              __stcg(reinterpret_cast<float2*>(
-                         a.part_o + (static_cast<int64_t>(slot_id) * 64 + r) * D + ch * 32 + col),
-                     make_float2(x, y));
-            }
-          }
-          consumer_sync();
-        }
-        if (final) break;
-        // Publish; the last CTA of the task goes on with the partial results.
-        __threadfence();
-        consumer_sync();
-        if (threadIdx.x == 0) {
-          int last = 0;
-          if (!dead) {
-            const unsigned wrap = last_cta - first_cta;
-            last = atomicInc(a.tickets + sg.task, wrap) == wrap;
-            __threadfence();
-          }
-          misc->last = last;
-        }
-        consumer_sync();
-        if (!misc->last) break;
-        final = true;
-        st.m0 = st.m1 = -INFINITY;
-        st.l0 = st.l1 = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st.o[n][e] = 0.0f;
-        const int rla = rt * 16 + g, rlb = rla + 8;
-        for (int t = first_cta + tj; t <= last_cta; t += TJ) {
-          const long long share_lo = misc->total * t / misc->grid;
-          const int64_t from = 2 * t + (sg.pos > share_lo ? 1 : 0);
-          const float2 none = make_float2(-INFINITY, 0.0f);
-          const float2 xa = rla < rows ? __ldcg(a.part_ml + from * 64 + rla) : none;
-          const float2 xb = rlb < rows ? __ldcg(a.part_ml + from * 64 + rlb) : none;
-          const float na = fmaxf(st.m0, xa.x), nb = fmaxf(st.m1, xb.x);
-          const float ga = na == -INFINITY ? 0.0f : ex2(st.m0 - na);
-          const float gb = nb == -INFINITY ? 0.0f : ex2(st.m1 - nb);
-          const float ha = na == -INFINITY ? 0.0f : ex2(xa.x - na);
-          const float hb = nb == -INFINITY ? 0.0f : ex2(xb.x - nb);
-          st.m0 = na;
-          st.m1 = nb;
-          // one thread of a quad carries l: the quad sum is already done
-          st.l0 = st.l0 * ga + xa.y * ha;
-          st.l1 = st.l1 * gb + xb.y * hb;
-          const float* pa = a.part_o + (from * 64 + rla) * D;
-          const float* pb2 = a.part_o + (from * 64 + rlb) * D;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float2 va2 = make_float2(0.0f, 0.0f), vb2 = va2;
-            if constexpr (!kByte) {
-              if (rla < rows) va2 = __ldcg(reinterpret_cast<const float2*>(pa + n * 8 + 2 * c));
-              if (rlb < rows) vb2 = __ldcg(reinterpret_cast<const float2*>(pb2 + n * 8 + 2 * c));
-            } else {
-              const int d = (n >> 2) * 32 + 8 * c + (n & 3);
-              if (rla < rows) va2 = make_float2(__ldcg(pa + d), __ldcg(pa + d + 4));
-              if (rlb < rows) vb2 = make_float2(__ldcg(pb2 + d), __ldcg(pb2 + d + 4));
-            }
-            st.o[n][0] = st.o[n][0] * ga + va2.x * ha;
-            st.o[n][1] = st.o[n][1] * ga + va2.y * ha;
-            st.o[n][2] = st.o[n][2] * gb + vb2.x * hb;
-            st.o[n][3] = st.o[n][3] * gb + vb2.y * hb;
           }
         }
       }
+      sg = after;
     }
   }
   __syncthreads();

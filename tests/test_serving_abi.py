@@ -38,6 +38,7 @@ def attend(ws=FAKE, n=1 << 40, **kw):
     (dict(query_len=4, max_seq_len=3), -6), (dict(num_reqs=1 << 30, query_len=2), -1),
     (dict(max_seq_len=0xFFFF * 128), -5),
     (dict(sm_scale=0.0), -1), (dict(sm_scale=float("nan")), -1), (dict(k_scale=0.0), -1),
+    (dict(sm_scale=1e-30, k_scale=1e-10), -1), (dict(sm_scale=1e30, k_scale=1e30), -1),
     (dict(k_scale=float("inf")), -1), (dict(v_scale=float("nan")), -1),
     (dict(q_type=2), -13), (dict(q_type=3, kv_type=3), -13), (dict(kv_type=1), -13),
     (dict(kv_type=2), -13), (dict(q_heads=7), -13), (dict(kv_heads=0), -13),
