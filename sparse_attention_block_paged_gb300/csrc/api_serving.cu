@@ -218,7 +218,11 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   a.status = status;
   const int rows = a.group * a.query_len;
   a.row_tiles = static_cast<int32_t>(cdiv(rows, 64));
-  a.tasks = a.kv_heads * a.row_tiles;
+  // The most kv heads side by side that leave no more than one SM in 25 idle.
+  a.gang = 1;
+  for (int g = 2; g <= a.kv_heads && g <= sms; ++g)
+    if (a.kv_heads % g == 0 && sms / g * g * 25 >= sms * 24) a.gang = g;
+  a.tasks = a.kv_heads / a.gang * a.row_tiles;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.tickets = reinterpret_cast<unsigned int*>(ws + w.tickets);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -231,7 +235,8 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   if ((rc = make_cache_map(p, false, &kmap)) || (rc = make_cache_map(p, true, &vmap))) return rc;
   // One CTA an SM; no more than there can be tiles.
   const int64_t most = static_cast<int64_t>(p->num_reqs) * a.tasks * (cdiv(p->max_seq_len, kBlock) + 2);
-  const int grid = static_cast<int>(most < sms ? most : sms);
+  const int gangs = static_cast<int>(most < sms / a.gang ? most : sms / a.gang);
+  const int grid = gangs * a.gang;
   return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
 }
 

@@ -18,9 +18,13 @@
 // the group sizes in use, far below what the tensor cores need: the kernel is
 // a stream of pages from HBM.  So:
 //
-//   * Work partition.  The list of all (request, kv head, 128-token tile) is
-//     cut into equal shares on the device, one a CTA, one CTA an SM; lengths
-//     need no host round trip and cost no imbalance.
+//   * Work partition.  The list of all (request, 128-token tile) is cut into
+//     equal shares on the device, one a gang of CTAs, one CTA an SM; lengths
+//     need no host round trip and cost no imbalance.  The CTAs of a gang walk
+//     the same pages at the same time, each for its own kv head: a page whose
+//     tokens hold all heads next to each other is then read from HBM in long
+//     pieces (16 e4m3 requests of 32K-128K tokens, 4 heads of 128 bytes a
+//     token: 326 us with each head's share elsewhere in time).
 //   * Pages go through a ring of slots in shared memory (192 KB for 16-bit
 //     D = 128: six slots of 128 tokens, keys and values in turn), filled by
 //     one producer warp with 4-D tiled TMA copies, so strides and page sizes
@@ -111,7 +115,7 @@ __device__ __forceinline__ int request_len(const AttentionArgs& a, int i) {
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// Positions of one task (request, kv head, 64-row tile) in the list.
+// Positions of one task (request, a gang's kv heads, 64-row tile) in the list.
 __device__ __forceinline__ long long task_slots(int len) {
   return len > 0 ? tiles_of(len) + kSegCost : 0;
 }
@@ -127,7 +131,7 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// The consumer threads: this CTA's share of the list and the tasks at its ends.
+// The consumer threads: this gang's share of the list and the tasks at its ends.
 __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.num_reqs + kConsumers * 32 - 1) / (kConsumers * 32);
@@ -157,10 +161,11 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
     if (w < warp) before += s;
     total += s;
   }
-  // No share is empty: at most one CTA per kMinShare positions takes part.
+  // No share is empty: at most one gang per kMinShare positions takes part.
   const long long most = total / kMinShare;
-  const int G = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
-  const long long c = blockIdx.x;
+  const int gangs = gridDim.x / a.gang;
+  const int G = static_cast<int>(most < 1 ? 1 : most < gangs ? most : gangs);
+  const long long c = blockIdx.x / a.gang;
   const long long lo = c < G ? quotient(total * c, G) : 0;
   const long long hi = c < G ? quotient(total * (c + 1), G) : 0;
   if (tid == 0) {
@@ -191,9 +196,16 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
   }
 }
 
+// Which of its gang's heads a CTA works on: the CTAs of a gang are neighbours
+__device__ __forceinline__ int member_of(const AttentionArgs& a) {
+  return static_cast<int>(blockIdx.x) % a.gang;
+}
+
 // One stretch of a CTA's share: tiles [b0, b1) of a task.
 struct Segment {
-  int task, req, len;
+  int req, len;
+  int head, row0;      // this CTA's kv head, the first of its 64 rows
+  int unit;            // index of (request, kv head, 64-row tile)
   int b0, b1, nb;
   long long pos;       // the task's first position in the list
 };
@@ -206,8 +218,12 @@ struct Walker {
       : lo(m->lo), hi(m->hi), p0(m->p0), pl(m->pl), P(0), t0(m->t0), tl(m->tl), t(0), stage(0) {}
   __device__ __forceinline__ bool emit(const AttentionArgs& a, int task, long long pos,
                                        Segment& s) const {
-    s.task = task;
     s.req = task / a.tasks;
+    const int sub = task - s.req * a.tasks;
+    const int tile = sub % a.row_tiles;
+    s.head = sub / a.row_tiles * a.gang + member_of(a);
+    s.row0 = tile * 64;
+    s.unit = (s.req * a.kv_heads + s.head) * a.row_tiles + tile;
     s.len = request_len(a, s.req);
     s.nb = tiles_of(s.len);
     s.pos = pos;
@@ -240,8 +256,8 @@ struct Walker {
   }
 };
 
-// The CTA whose share holds position x.
-__device__ __forceinline__ int cta_of(long long x, long long total, int grid) {
+// The gang whose share holds position x.
+__device__ __forceinline__ int gang_of(long long x, long long total, int grid) {
   return static_cast<int>(quotient((x + 1) * grid - 1, total));
 }
 
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t wait = kv, wait_phase = 0;          // the barrier of the tile S / 2 before
       bool ok = true;
       while (ok && walk.next(a, sg)) {
-        const int head = (sg.task % a.tasks) / a.row_tiles;
+        const int head = sg.head;
         const int32_t* table = a.table + static_cast<int64_t>(sg.req) * a.table_stride;
         const int pages = (sg.len + (1 << a.page_shift) - 1) >> a.page_shift;
         auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&done[bar], phase, abort_flag);
           if (!ok) break;
           const float* from = slice + ((slot >> 1) * kConsumers + turn * TG * RT) * 16;
-          float* to = a.tile_lse + (static_cast<int64_t>(sg.task) * a.w_width + b) * (RT * 16);
+          float* to = a.tile_lse + (static_cast<int64_t>(sg.unit) * a.w_width + b) * (RT * 16);
           for (int r = lane; r < RT * 16; r += 32) {
             float x[TG], top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -604,11 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // operands; e4m3, D/4 elements from c D/4 of rows g and g + 8.
     uint32_t q[KS][4];
     auto load_queries = [&](const Segment& s) {
-      const int sub = s.task % a.tasks, head = sub / a.row_tiles;
-      const int ra = (sub % a.row_tiles) * 64 + rt * 16 + g, rb = ra + 8;
+      const int ra = s.row0 + rt * 16 + g, rb = ra + 8;
       const uint16_t* base = static_cast<const uint16_t*>(a.q) +
                              static_cast<int64_t>(s.req) * a.query_len * a.q_tok +
-                             static_cast<int64_t>(head) * a.group * a.q_head;
+                             static_cast<int64_t>(s.head) * a.group * a.q_head;
       auto row_at = [&](int r) {
         r = min(r, R - 1);
         return base + r / a.group * a.q_tok + r % a.group * a.q_head;
@@ -640,8 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = walk.next(a, sg);
     if (more) load_queries(sg);
     while (more) {
-      const int sub = sg.task % a.tasks;                   // kv head and 64-row tile
-      const int head = sub / a.row_tiles, row0 = (sub % a.row_tiles) * 64;
+      const int head = sg.head, row0 = sg.row0;
       const int rows = min(64, R - row0);                  // of this task
       const int64_t tok0 = static_cast<int64_t>(sg.req) * a.query_len;
       // Row r of the kv head is query token r / group, query head r % group.
@@ -1079,16 +1093,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Publish; the last CTA of the task joins the partial results.  (The
         // barrier orders the CTA's stores before thread 0's release.)
         const long long pb = sg.pos + kSegCost;
-        const int first_cta = cta_of(pb, misc->total, misc->grid);
-        const int parts = cta_of(pb + sg.nb - 1, misc->total, misc->grid) - first_cta + 1;
+        const int lead = gang_of(pb, misc->total, misc->grid);
+        const int parts = gang_of(pb + sg.nb - 1, misc->total, misc->grid) - lead + 1;
         if (threadIdx.x == 0)
-          misc->last = !dead && ticket(a.tickets + sg.task, parts - 1) == parts - 1;
+          misc->last = !dead && ticket(a.tickets + sg.unit, parts - 1) == parts - 1;
         consumer_sync();
         if (misc->last) {
           // A thread takes four columns of a row, the partial results in
           // order, eight loads in flight.
-          const int64_t p0 = 2 * first_cta + (sg.pos > quotient(misc->total * first_cta, misc->grid));
-          auto part_of = [&](int t) { return t == 0 ? p0 : 2 * static_cast<int64_t>(first_cta + t); };
+          const int member = member_of(a);
+          const bool second = sg.pos > quotient(misc->total * lead, misc->grid);
+          auto part_of = [&](int t) {
+            return 2 * static_cast<int64_t>((lead + t) * a.gang + member) + (t == 0 && second);
+          };
 #pragma unroll 1
           for (int unit = threadIdx.x; unit < rows * (D / 4); unit += kConsumers * 32) {
             const int r = unit / (D / 4), col = unit % (D / 4) * 4;

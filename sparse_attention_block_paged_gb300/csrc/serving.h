@@ -28,7 +28,8 @@ struct AttentionArgs {
   int32_t head_dim;
   int32_t q_type, kv_type;    // MM3IDX_TYPE_*
   int32_t row_tiles;          // 64-row tiles of a kv head's group * query_len rows
-  int32_t tasks;              // kv_heads * row_tiles, of a request
+  int32_t gang;               // kv heads that as many CTAs work on side by side (a divisor)
+  int32_t tasks;              // kv_heads / gang * row_tiles, of a request
   int32_t num_pages;
   int32_t page_shift;         // log2 of the page's tokens
   const int32_t* table;
@@ -45,11 +46,12 @@ struct AttentionArgs {
   int64_t w_stride;
   int32_t w_width;            // cdiv(max_seq_len, 128)
   // workspace
-  unsigned int* tickets;      // [num_reqs * tasks], 0 between calls
+  unsigned int* tickets;      // [num_reqs * kv_heads * row_tiles], 0 between calls
   float2* part_ml;            // [2 * grid][64]: reference and sum of a CTA's share of a task
   float* part_o;              // [2 * grid][64][head_dim]
   float* row_lse;             // with weights: [rows, q heads], base 2
-  float* tile_lse;            // with weights: [num_reqs * tasks][w_width][rows of the kernel], base 2
+  float* tile_lse;            // with weights: [num_reqs * kv_heads * row_tiles][w_width][rows of
+                              // the kernel], base 2
   int32_t* status;
 };
 
