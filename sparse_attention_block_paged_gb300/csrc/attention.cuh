@@ -74,8 +74,10 @@ constexpr float kRaise = 8.0f;
 
 // Positions that a (request, kv head) takes in the list beyond its tiles (its
 // start and its join cost time, too), and the fewest positions worth a CTA.
-constexpr int kSegCost = 2;
-constexpr int kMinShare = 4;
+// Measured over 2, 4, 6, 10: the spec-decode batch 197.7, 195.6, 194.2, 194.9
+// us; two requests of 300-700 tokens with 2, 4 positions at least: 11.0, 12.0 us.
+constexpr int kSegCost = 6;
+constexpr int kMinShare = 2;
 
 template <int KV, int D>
 struct Cfg {
@@ -100,6 +102,11 @@ struct Cfg {
   static constexpr int oMisc = oMask + kSlots * 4;
   static constexpr int kSmem = oMisc + 128 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+template <int V>
+struct Const {
+  static constexpr int value = V;
 };
 
 struct Misc {
@@ -1099,64 +1106,89 @@ __global__ void __launch_bounds__(kThreads, 1)
           misc->last = !dead && ticket(a.tickets + sg.unit, parts - 1) == parts - 1;
         consumer_sync();
         if (misc->last) {
-          // A thread takes four columns of a row, the partial results in
-          // order, eight loads in flight.
+          // A thread takes four columns of up to UB rows at a time, the partial
+          // results in order, UB x PB = 16 loads in flight.
+          constexpr int kStride = kConsumers * 32;
           const int member = member_of(a);
           const bool second = sg.pos > quotient(misc->total * lead, misc->grid);
-          auto part_of = [&](int t) {
-            return 2 * static_cast<int64_t>((lead + t) * a.gang + member) + (t == 0 && second);
-          };
+          const int units = rows * (D / 4);
+          auto join_parts = [&](auto ub, auto pb) {
+            constexpr int UB = decltype(ub)::value, PB = decltype(pb)::value;
 #pragma unroll 1
-          for (int unit = threadIdx.x; unit < rows * (D / 4); unit += kConsumers * 32) {
-            const int r = unit / (D / 4), col = unit % (D / 4) * 4;
-            float m = -INFINITY, l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-            for (int t0 = 0; t0 < parts; t0 += 8) {
-              float2 x[8];
-              float4 v[8];
+            for (int u0 = threadIdx.x; u0 < units; u0 += UB * kStride) {
+              float m[UB], l[UB];
+              float4 o[UB];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                if (t0 + k < parts) {
-                  const int64_t at = part_of(t0 + k) * 64 + r;
-                  x[k] = __ldcg(a.part_ml + at);
-                  v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
-                } else {
-                  x[k] = make_float2(-INFINITY, 0.0f);
-                  v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int u = 0; u < UB; ++u) {
+                m[u] = -INFINITY;
+                l[u] = 0.0f;
+                o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              }
+#pragma unroll 1
+              for (int t0 = 0; t0 < parts; t0 += PB) {
+                float2 x[UB][PB];
+                float4 v[UB][PB];
+#pragma unroll
+                for (int k = 0; k < PB; ++k) {
+                  const int64_t at = 2 * static_cast<int64_t>((lead + t0 + k) * a.gang + member) +
+                                     (t0 + k == 0 && second);
+#pragma unroll
+                  for (int u = 0; u < UB; ++u) {
+                    const int unit = u0 + u * kStride;
+                    x[u][k] = make_float2(-INFINITY, 0.0f);
+                    v[u][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (t0 + k < parts && unit < units) {
+                      x[u][k] = __ldcg(a.part_ml + at * 64 + unit / (D / 4));
+                      v[u][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * 64 * D) + unit);
+                    }
+                  }
+                }
+#pragma unroll
+                for (int u = 0; u < UB; ++u) {
+                  float top = m[u];
+#pragma unroll
+                  for (int k = 0; k < PB; ++k) top = fmaxf(top, x[u][k].x);
+                  if (top == -INFINITY) continue;
+                  const float f = ex2(m[u] - top);
+                  m[u] = top;
+                  l[u] *= f;
+                  o[u].x *= f; o[u].y *= f; o[u].z *= f; o[u].w *= f;
+#pragma unroll
+                  for (int k = 0; k < PB; ++k) {
+                    const float w = ex2(x[u][k].x - top);
+                    l[u] += x[u][k].y * w;
+                    o[u].x += v[u][k].x * w; o[u].y += v[u][k].y * w;
+                    o[u].z += v[u][k].z * w; o[u].w += v[u][k].w * w;
+                  }
                 }
               }
-              float top = m;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
-              if (top == -INFINITY) continue;
-              const float f = ex2(m - top);
-              m = top;
-              l *= f;
-              o.x *= f; o.y *= f; o.z *= f; o.w *= f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float w = ex2(x[k].x - top);
-                l += x[k].y * w;
-                o.x += v[k].x * w; o.y += v[k].y * w; o.z += v[k].z * w; o.w += v[k].w * w;
+              for (int u = 0; u < UB; ++u) {
+                const int unit = u0 + u * kStride;
+                if (unit >= units) break;
+                const int r = unit / (D / 4), col = unit % (D / 4) * 4;
+                const int64_t row = tok0 + (row0 + r) / a.group;
+                const int h = head * a.group + (row0 + r) % a.group;
+                const float f = l[u] == 0.0f ? 0.0f : a.v_scale / l[u];
+                uint2 w;
+                if (a.q_type == MM3IDX_TYPE_BF16)
+                  w = make_uint2(pack2<true>(o[u].x * f, o[u].y * f),
+                                 pack2<true>(o[u].z * f, o[u].w * f));
+                else
+                  w = make_uint2(pack2<false>(o[u].x * f, o[u].y * f),
+                                 pack2<false>(o[u].z * f, o[u].w * f));
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok +
+                                          h * a.o_head + col) = w;
+                if (col == 0) {
+                  const float lse2 = l[u] == 0.0f ? -INFINITY : m[u] + lg2(l[u]);
+                  if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
+                  if (weigh) a.row_lse[row * heads + h] = lse2;
+                }
               }
             }
-            const int64_t row = tok0 + (row0 + r) / a.group;
-            const int h = head * a.group + (row0 + r) % a.group;
-            const float f = l == 0.0f ? 0.0f : a.v_scale / l;
-            uint2 w;
-            if (a.q_type == MM3IDX_TYPE_BF16)
-              w = make_uint2(pack2<true>(o.x * f, o.y * f), pack2<true>(o.z * f, o.w * f));
-            else
-              w = make_uint2(pack2<false>(o.x * f, o.y * f), pack2<false>(o.z * f, o.w * f));
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
-                                      col) = w;
-            if (col == 0) {
-              const float lse2 = l == 0.0f ? -INFINITY : m + lg2(l);
-              if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
-              if (weigh) a.row_lse[row * heads + h] = lse2;
-            }
-          }
+          };
+          if (units > 2 * kStride) join_parts(Const<4>{}, Const<4>{});
+          else join_parts(Const<2>{}, Const<8>{});
         }
       }
       sg = after;
