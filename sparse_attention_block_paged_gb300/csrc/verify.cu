@@ -63,7 +63,8 @@ __device__ __forceinline__ float elem_of(const uint4& v, int e) {
 // 128 a clock and SM where a conversion to 64 bits takes the slow pipe
 // (256 requests x 131072: 131 us with it).
 struct Limbs {
-  uint32_t high, low;
+  float value;           // clamped
+  uint32_t high, low;    // images: 0x4B000000 stands for 0
 };
 __device__ __forceinline__ Limbs limbs(float p) {
   constexpr float kBase = 8388608.0f;                      // 2^23
@@ -71,9 +72,25 @@ __device__ __forceinline__ Limbs limbs(float p) {
   const float h = __fmaf_rz(p, kBase, kBase);
   const float rest = __fmaf_rn(kBase - h, 1.0f / kBase, p);  // exact: p's bits below 2^-23
   const float l = __fmaf_rn(rest, kBase * kBase, kBase);
-  return Limbs{__float_as_uint(h), __float_as_uint(l)};
+  return Limbs{p, __float_as_uint(h), __float_as_uint(l)};
 }
-constexpr uint32_t kZero = 0x4B000000u;                    // the image of 2^23
+// The weight of p, or of max(p - q, 0), added to two running sums of up to
+// 2^8 elements.
+template <bool Q>
+__device__ __forceinline__ void add_weight(float p, float q, int32_t& high, int32_t& low) {
+  constexpr uint32_t kZero = 0x4B000000u;                  // the image of 2^23
+  const Limbs a = limbs(p);
+  if constexpr (Q) {
+    const Limbs b = limbs(q);
+    if (a.value > b.value) {
+      high += static_cast<int32_t>(a.high - b.high);
+      low += static_cast<int32_t>(a.low - b.low);
+    }
+  } else {
+    high += static_cast<int32_t>(a.high - kZero);
+    low += static_cast<int32_t>(a.low - kZero);
+  }
+}
 
 // floor(u * total) for u in [0, 1) (clamped, NaN as 0).
 __device__ __forceinline__ uint64_t point_of(float u, uint64_t total) {
@@ -88,25 +105,17 @@ struct Row {
   using E = Elem<TYPE>;
   const char* p;     // token 0
   const char* q;     // null: nothing is taken off
-  int without;       // a token whose weight is dropped, -1: none
   int skew, end;     // tokens are x in [skew, end)
-  bool q_wide;       // q has its 16-byte boundaries where p has
+  bool wide;         // q (if any) has its 16-byte boundaries where p has
 
-  __device__ __forceinline__ Row(const char* p_, const char* q_, int without_, int vocab)
-      : p(p_), q(q_), without(without_) {
+  __device__ __forceinline__ Row(const char* p_, const char* q_, int vocab) : p(p_), q(q_) {
     skew = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / E::kSize;
     end = skew + vocab;
-    q_wide = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    wide = !q || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
   }
-  // kPer elements from x (a multiple of kPer), 0 outside the row.
-  __device__ __forceinline__ uint4 load(const char* row, bool wide, int x) const {
+  // kPer elements from x, 0 outside the row, one by one.
+  __device__ __forceinline__ uint4 gather(const char* row, int x) const {
     const char* at = row + static_cast<int64_t>(x - skew) * E::kSize;
-    if (wide && x >= skew && x + E::kPer <= end) {
-      uint4 v;
-      asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
-      return v;
-    }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < E::kPer; ++e) {
@@ -116,37 +125,54 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // The weight of element e of the loads at x, added to two running sums (of
-  // no more than 2^8 elements: each limb is below 2^24).
-  __device__ __forceinline__ void add(const uint4& vp, const uint4& vq, int x, int e, int32_t& high,
-                                      int32_t& low) const {
-    const float fp = elem_of<TYPE>(vp, e);
-    const Limbs lp = limbs(fp);
-    Limbs lq{kZero, kZero};
-    bool counts = x + e - skew != without;
-    if (q) {
-      const float fq = elem_of<TYPE>(vq, e);
-      lq = limbs(fq);
-      counts = lp.high > lq.high || (lp.high == lq.high && lp.low > lq.low);
-    }
-    if (counts) {
-      high += static_cast<int32_t>(lp.high - lq.high);
-      low += static_cast<int32_t>(lp.low - lq.low);
+  // One warp's elements of a step: kGroups x 32 x kPer from x0.
+  template <bool Q>
+  __device__ __forceinline__ void load(int x0, uint4 (&vp)[kGroups], uint4 (&vq)[kGroups]) const {
+    const int lane = threadIdx.x & 31;
+    if (wide && x0 >= skew && x0 + E::kStep <= end) {
+      const int64_t at = static_cast<int64_t>(x0 + lane * E::kPer - skew) * E::kSize;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        vp[k] = stream(p + at + k * 512);
+        if constexpr (Q) vq[k] = stream(q + at + k * 512);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        vp[k] = gather(p, x0 + (k * 32 + lane) * E::kPer);
+        if constexpr (Q) vq[k] = gather(q, x0 + (k * 32 + lane) * E::kPer);
+      }
     }
   }
-  // One warp's weights of a step (kGroups x 32 x kPer elements from x0).
-  __device__ __forceinline__ void load_step(int x0, uint4 (&vp)[kGroups], uint4 (&vq)[kGroups]) const {
-    const int lane = threadIdx.x & 31;
+  static __device__ __forceinline__ uint4 stream(const char* at) {
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+  }
+  // The lane's part of the weight of steps [s, end_step).
+  template <bool Q>
+  __device__ __forceinline__ uint64_t sum(int s, int end_step) const {
+    uint64_t total = 0;   // unsigned: wraps as the signed low sums need
+    for (; s < end_step; ++s) {
+      uint4 vp[kGroups], vq[kGroups];
+      load<Q>(s * E::kStep, vp, vq);
+      int32_t high = 0, low = 0;
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      const int x = x0 + (k * 32 + lane) * E::kPer;
-      vp[k] = load(p, true, x);
-      vq[k] = q ? load(q, q_wide, x) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+        for (int e = 0; e < E::kPer; ++e)
+          add_weight<Q>(elem_of<TYPE>(vp[k], e), Q ? elem_of<TYPE>(vq[k], e) : 0.0f, high, low);
+      total += static_cast<uint64_t>((static_cast<int64_t>(high) << 23) + low);
     }
+    return total;
   }
 };
 
-__device__ __forceinline__ uint64_t join(int32_t high, int32_t low) {
+template <bool Q>
+__device__ __forceinline__ uint64_t weight_of(float p, float q) {
+  int32_t high = 0, low = 0;
+  add_weight<Q>(p, q, high, low);
   return static_cast<uint64_t>((static_cast<int64_t>(high) << 23) + low);
 }
 
@@ -228,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
   const float u = __ldg(a.u + i * a.u_stride + a.drafts);
 
   for (int pass = 0;; ++pass) {
-    const Row<TYPE> r(p, pass ? nullptr : q, pass ? -1 : without, a.vocab);
+    const Row<TYPE> r(p, pass ? nullptr : q, a.vocab);
+    // The token whose weight is dropped (-1: none), as an element.
+    const int drop = pass == 0 && without >= 0 && without < a.vocab ? without + r.skew : -1;
+    const uint64_t dropped = drop >= 0 ? weight_of<false>(prob_at<TYPE>(p, without), 0.0f) : 0;
     // This CTA's part, in whole warp steps, and its chunks of whole steps.
     const int steps = (r.end + E::kStep - 1) / E::kStep;
     const int part = (steps + cluster - 1) / cluster;
@@ -236,19 +265,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
     const int per = (part + kMaxChunks - 1) / kMaxChunks;
     const int n = (s1 - s0 + per - 1) / per;
     for (int c = warp; c < n; c += kWarps) {
-      uint64_t sum = 0;   // unsigned: wraps as the signed low sums need
-      for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1); ++s) {
-        uint4 vp[kGroups], vq[kGroups];
-        r.load_step(s * E::kStep, vp, vq);
-        int32_t high = 0, low = 0;
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k)
-#pragma unroll
-          for (int e = 0; e < E::kPer; ++e)
-            r.add(vp[k], vq[k], s * E::kStep + (k * 32 + lane) * E::kPer, e, high, low);
-        sum += join(high, low);
-      }
-      sum = warp_sum(sum);
+      const int from = s0 + c * per, to = min(from + per, s1);
+      uint64_t sum = warp_sum(r.q ? r.template sum<true>(from, to) : r.template sum<false>(from, to));
+      if (drop >= from * E::kStep && drop < to * E::kStep) sum -= dropped;
       if (lane == 0) chunks[c] = sum;
     }
     __syncthreads();
@@ -294,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
       }
       for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1); ++s) {
         uint4 vp[kGroups], vq[kGroups];
-        r.load_step(s * E::kStep, vp, vq);
+        if (r.q) r.template load<true>(s * E::kStep, vp, vq);
+        else r.template load<false>(s * E::kStep, vp, vq);
         int found = -1;
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
@@ -302,9 +322,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
           uint64_t w[E::kPer], own = 0;
 #pragma unroll
           for (int e = 0; e < E::kPer; ++e) {
-            int32_t high = 0, low = 0;
-            r.add(vp[k], vq[k], x0, e, high, low);
-            own += w[e] = join(high, low);
+            const float fp = elem_of<TYPE>(vp[k], e);
+            w[e] = r.q ? weight_of<true>(fp, elem_of<TYPE>(vq[k], e)) : weight_of<false>(fp, 0.0f);
+            if (x0 + e == drop) w[e] = 0;
+            own += w[e];
           }
           const uint64_t incl = warp_scan(own);
           uint64_t at = below + incl - own;
@@ -354,11 +375,15 @@ cudaError_t launch_t(const DraftArgs& a, int cluster, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify(const DraftArgs& a, int sms, cudaStream_t s) {
-  // CTAs a request: enough to fill the card four deep, each with two steps a
+  // CTAs a request: as many as run at once (four an SM; 64 x 200000: 25.5 us
+  // with 8, 32.2 with 16, half of them in a second wave), each with a step a
   // warp at least.
+  const int step = a.type == MM3IDX_TYPE_FP32 ? Elem<MM3IDX_TYPE_FP32>::kStep
+                                              : Elem<MM3IDX_TYPE_BF16>::kStep;
+  const int most = a.vocab / (kWarps * step);
   int cluster = 1;
-  const int most = a.vocab / (4096 * 2);
-  while (cluster < kMaxCluster && cluster < most && static_cast<int64_t>(a.num_reqs) * cluster < 4 * sms)
+  while (2 * cluster <= kMaxCluster && cluster < most &&
+         static_cast<int64_t>(a.num_reqs) * 2 * cluster <= 4 * sms)
     cluster *= 2;
   if (a.type == MM3IDX_TYPE_FP32) return launch_t<MM3IDX_TYPE_FP32>(a, cluster, s);
   if (a.type == MM3IDX_TYPE_BF16) return launch_t<MM3IDX_TYPE_BF16>(a, cluster, s);
