@@ -4,9 +4,10 @@ forced init/local blocks.
 
 This module is the thin Python binding of ``libmm3idx.so`` (C ABI in
 ``include/mm3idx.h``).  It only marshals torch tensors into pointers, strides
-and the current CUDA stream; every step of the computation runs in the
-library's CUDA kernels.  Importing it fails loudly when the library has not
-been built: there is no CPU or PyTorch fallback.
+and the current CUDA stream (the operators that use the selection do so in
+``csrc/binding.cpp``); every step of the computation runs in the library's
+CUDA kernels.  Importing it fails loudly when the library has not been built:
+there is no CPU or PyTorch fallback.
 
 Entry points (names after the vLLM MiniMax-M3 ``index_topk`` page):
 
@@ -31,8 +32,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -206,26 +207,6 @@ class Drafts(ctypes.Structure):
     ]
 
 
-def _image(cls):
-    """The packer of a structure's image from its fields' values in order (a
-    call that fills a ctypes structure field by field takes several times as
-    long).  0 stands for a null pointer."""
-    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i",
-             ctypes.c_float: "f", ctypes.c_double: "d"}
-    form = "@"
-    for _, kind in cls._fields_:
-        if kind in codes:
-            form += codes[kind]
-        else:                                   # an array of structures of 8-byte fields
-            form += "".join(codes[k] for _, k in kind._type_._fields_) * kind._length_
-    packer = struct.Struct(form + "0q")
-    assert packer.size == ctypes.sizeof(cls), cls.__name__
-    return packer.pack
-
-
-_attention_image, _weights_image = _image(Attention), _image(Weights)
-_eviction_image, _drafts_image = _image(EvictionArgs), _image(Drafts)
-
 SYMBOLS = {
     "mm3idx_version": (ctypes.c_int32, []),
     "mm3idx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -284,14 +265,14 @@ SYMBOLS = {
     "mm3idx_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
-    # the structures of these go as images (bytes) or by reference
-    "mm3idx_paged_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
-                                              ctypes.c_void_p]),
+    "mm3idx_paged_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.c_void_p,
+                                              ctypes.c_size_t, ctypes.c_void_p]),
     "mm3idx_attention_workspace_bytes": (ctypes.c_int, [ctypes.c_int32] * 7 +
                                          [ctypes.POINTER(ctypes.c_size_t)]),
-    "mm3idx_accumulate_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
-    "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "mm3idx_accumulate_weights": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.c_void_p]),
+    "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.POINTER(EvictionArgs),
+                                           ctypes.c_void_p]),
+    "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Drafts), ctypes.c_void_p]),
 }
 
 
@@ -310,6 +291,21 @@ def _load():
 
 lib = _load()
 LIB_PATH = _LIB_PATH
+
+
+def _load_binding():
+    path = os.path.join(_PKG, "_lib", "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it first "
+                          "(python sparse_attention_block_paged_gb300/build.py)")
+    spec = importlib.util.spec_from_file_location("_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_error(Mm3idxError)
+    return module
+
+
+_binding = _load_binding()
 
 
 def status_string(status: int) -> str:
@@ -751,15 +747,11 @@ def decode_static(idx_q, index_cache, block_table, seq_lens, *, query_len, max_s
 
 # ------------------------------------------------ using the selection
 
-def _allocating_on(stream):
-    """Tensors that a call makes belong to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _row_stride(t):
-    """Elements between the rows of a 2-D tensor (free when it has one row)."""
-    rows, columns = t.shape
-    return t.stride(0) if rows > 1 else max(columns, 1)
+def _run_on(stream, tensor):
+    """Makes `stream` current for a call, so that it runs there and the tensors
+    it makes belong there; `stream` must belong to the inputs' GPU."""
+    _stream(tensor.device, stream)
+    return torch.cuda.stream(stream)
 
 
 def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, num_reqs: int,
@@ -800,123 +792,10 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max
     Over selected blocks: ``page_table``, ``seq_lens`` = the sparse table and
     context lengths of :func:`decode_sparse_table`, ``query_len=1`` and
     ``max_seq_len = 128 * topk``."""
-    # Each property is read once and the structure packed in one go: the call
-    # itself takes as long as a small batch's kernel.
-    dtype, dev = q.dtype, q.device
-    if not (q.ndim == 3 and (dtype is torch.bfloat16 or dtype is torch.float16)
-            and q.stride(2) == 1):
-        raise ValueError("queries must be bf16 or fp16 [tokens, heads, head_dim] with contiguous "
-                         "head_dim")
-    rows, heads, dim = q.shape
-    kv = k_cache.dtype
-    if not (k_cache.ndim == 4 and k_cache.shape == v_cache.shape and kv is v_cache.dtype
-            and (kv is dtype or kv is torch.float8_e4m3fn) and k_cache.shape[3] == dim):
-        raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] with contiguous "
-                         "head_dim, of the queries' type or float8_e4m3fn")
-    pages, size, kv_heads, _ = k_cache.shape
-    kp, kt, kh, kd = k_cache.stride()
-    vp, vt, vh, vd = v_cache.stride()
-    if kd != 1 or vd != 1:
-        raise ValueError("caches must have contiguous head_dim")
-    if not (page_table.ndim == 2 and page_table.dtype is torch.int32 and seq_lens.ndim == 1
-            and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()):
-        raise ValueError("page table and lengths must be int32 with unit stride")
-    table_rows, width = page_table.shape
-    table_stride, one = page_table.stride()
-    if one != 1 and width > 1:
-        raise ValueError("page table and lengths must be int32 with unit stride")
-    if not (q.is_cuda and k_cache.device == dev and v_cache.device == dev
-            and page_table.device == dev and seq_lens.device == dev):
-        raise ValueError("all inputs must be on the same GPU")
-    reqs = seq_lens.shape[0]
-    if rows != reqs * query_len or table_rows != reqs:
-        raise ValueError("queries must have batch * query_len rows and the page table one row per "
-                         "request")
-    if out is None:
-        with _allocating_on(stream):
-            out = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
-    elif not (out.shape == q.shape and out.dtype is dtype and out.device == dev):
-        raise ValueError("out must be like the queries")
-    qt, qh, _ = q.stride()
-    ot, oh, od = out.stride()
-    if od != 1:
-        raise ValueError("out must be like the queries")
-    if rows <= 1:                               # strides of dimensions of one are free
-        qt = ot = heads * dim
-    if heads <= 1:
-        qh = oh = dim
-    if pages <= 1:
-        kp = vp = size * kv_heads * dim
-    if kv_heads <= 1:
-        kh = vh = dim
-    lse_at = lse_stride = weights_at = weights_stride = 0
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.ndim == 2 and lse.shape[0] >= rows
-              and lse.shape[1] == heads and (lse.stride(1) == 1 or heads == 1)
-              and lse.device == dev,
-              "lse must be fp32 [>= rows, heads] with unit inner stride")
-        lse_at, lse_stride = lse.data_ptr(), _row_stride(lse)
-    if block_weights is not None:
-        _need(block_weights.dtype == torch.float32 and block_weights.ndim == 2
-              and block_weights.shape[0] >= rows
-              and block_weights.shape[1] >= _cdiv(max_seq_len, 128)
-              and (block_weights.stride(1) == 1 or block_weights.shape[1] == 1)
-              and block_weights.device == dev,
-              "block_weights must be fp32 [>= rows, >= cdiv(max_seq_len, 128)] with unit inner "
-              "stride")
-        weights_at, weights_stride = block_weights.data_ptr(), _row_stride(block_weights)
-    image = _attention_image(
-        q.data_ptr(), qt, qh, heads, kv_heads, dim, TYPES[dtype], TYPES[kv],
-        k_cache.data_ptr(), kp, kt, kh, v_cache.data_ptr(), vp, vt, vh, k_scale, v_scale,
-        pages, size, page_table.data_ptr(), table_stride if reqs > 1 else max(width, 1), width,
-        seq_lens.data_ptr(), reqs, query_len, max_seq_len, sm_scale, out.data_ptr(), ot, oh,
-        lse_at, lse_stride, weights_at, weights_stride)
-    if workspace is None:
-        with _allocating_on(stream):
-            workspace = new_attention_workspace(heads, kv_heads, dim, reqs, query_len, max_seq_len,
-                                                block_weights is not None, dev)
-    wp, wn = _ws(workspace, dev)
-    with _on(dev):
-        _check(lib.mm3idx_paged_attention(image, wp, wn, _stream(dev, stream)),
-               "mm3idx_paged_attention")
-    return out
-
-
-def _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay):
-    """The checks and the image of mm3idx_weights_t."""
-    width, dev = _cdiv(max_seq_len, 128), acc.device
-    if not (seq_lens.ndim == 1 and seq_lens.dtype is torch.int32 and seq_lens.is_contiguous()):
-        raise ValueError("lengths must be contiguous int32")
-    reqs = seq_lens.shape[0]
-    if not (acc.dtype is torch.float32 and acc.ndim == 2 and acc.shape[0] == reqs
-            and acc.shape[1] >= width and (acc.stride(1) == 1 or acc.shape[1] == 1)):
-        raise ValueError("weights must be fp32 [num_reqs, >= cdiv(max_seq_len, 128)] with unit "
-                         "inner stride")
-    if not (acc.is_cuda and seq_lens.device == dev):
-        raise ValueError("all inputs must be on the same GPU")
-    w_at = w_stride = ids_at = ids_stride = topk = 0
-    if block_weights is not None:
-        rows, columns = block_weights.shape
-        if not (block_weights.dtype is torch.float32 and rows >= reqs * query_len
-                and (columns == 1 or block_weights.stride(1) == 1)
-                and block_weights.device == dev
-                and columns >= (width if ids is None else ids.shape[-1])):
-            raise ValueError("block_weights must be fp32 [>= num_reqs * query_len, a column per "
-                             "block or id] with unit inner stride")
-        w_at, w_stride = block_weights.data_ptr(), _row_stride(block_weights)
-    if ids is not None:
-        if ids.ndim == 3:                       # the ids of one index head, as decode returns them
-            _need(ids.shape[0] == 1, "ids must be those of one index head")
-            ids = ids[0]
-        rows, topk = ids.shape
-        if not (block_weights is not None and ids.dtype is torch.int32
-                and rows >= reqs * query_len and (topk == 1 or ids.stride(1) == 1)
-                and ids.device == dev):
-            raise ValueError("ids must be int32 [>= num_reqs * query_len, topk] with unit inner "
-                             "stride, with their block_weights")
-        ids_at, ids_stride = ids.data_ptr(), _row_stride(ids)
-    return _weights_image(acc.data_ptr(), _row_stride(acc), w_at, w_stride, ids_at, ids_stride,
-                          topk, seq_lens.data_ptr(), reqs, query_len, max_seq_len, decay)
+    with _HERE if stream is None else _run_on(stream, q):
+        return _binding.paged_attention(q, k_cache, v_cache, page_table, seq_lens, query_len,
+                                        max_seq_len, sm_scale, k_scale, v_scale, out, lse,
+                                        block_weights, workspace)
 
 
 def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, ids=None,
@@ -925,10 +804,9 @@ def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, 
     ``block_weights`` (of :func:`paged_attention`) summed over the request's
     ``query_len`` rows, in place: column b is block b, or with ``ids`` (int32
     [rows, topk] or [1, rows, topk], -1: none) column k is block ids[row, k]."""
-    w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
-    with _on(acc.device):
-        _check(lib.mm3idx_accumulate_weights(w, _stream(acc.device, stream)),
-               "mm3idx_accumulate_weights")
+    with _HERE if stream is None else _run_on(stream, acc):
+        _binding.accumulate_weights(acc, block_weights, seq_lens, ids, query_len, max_seq_len,
+                                    decay)
     return acc
 
 
@@ -957,62 +835,10 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
     inputs are left as they are, or with ``in_place`` overwritten by them
     (their columns from ``budget`` on stay as they were).  ``out``: an
     Eviction of the same shapes to write into."""
-    w = _weights(acc, seq_lens, block_weights, ids, query_len, max_seq_len, decay)
-    dev, reqs, width = acc.device, seq_lens.shape[0], _cdiv(max_seq_len, 128)
-    second = attention_block_table
-    for t in (block_table,) if second is None else (block_table, second):
-        if not (t.dtype is torch.int32 and t.ndim == 2 and t.shape[0] == reqs
-                and t.shape[1] >= width and (t.shape[1] == 1 or t.stride(1) == 1)
-                and t.device == dev):
-            raise ValueError("block tables must be int32 [num_reqs, >= cdiv(max_seq_len, 128)] "
-                             "with unit inner stride, on the weights' GPU")
-        if in_place and t.shape[1] < budget:
-            raise ValueError("in-place tables must have at least budget columns")
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
-    gone = max(1, width - budget)
-    if out is None:
-        with _allocating_on(stream):
-            i32 = {"dtype": torch.int32, "device": dev}
-            ids, freed = torch.empty((reqs, budget), **i32), torch.empty((reqs, gone), **i32)
-            table, table2, freed2 = block_table, second, None
-            new_lens, new_acc = seq_lens, acc
-            if second is not None:
-                freed2 = torch.empty((reqs, gone), **i32)
-            if not in_place:
-                table = torch.empty((reqs, budget), **i32)
-                if second is not None:
-                    table2 = torch.empty((reqs, budget), **i32)
-                new_lens = torch.empty((reqs,), **i32)
-                new_acc = torch.empty((reqs, width), dtype=torch.float32, device=dev)
-            out = Eviction(ids, new_lens, new_acc, table, freed, table2, freed2)
-    else:
-        _need(not in_place, "out and in_place exclude each other")
-        _need((out.attention_block_table is None) == (out.attention_freed is None)
-              == (second is None)
-              and out.weights.dtype == torch.float32 and out.weights.shape[1] >= width
-              and out.seq_lens.dtype == torch.int32 and out.seq_lens.shape == seq_lens.shape
-              and out.seq_lens.is_contiguous()
-              and all(t is None or (t.device == dev and t.shape[0] == reqs and
-                                    (t.ndim == 1 or t.stride(1) == 1 or t.shape[1] == 1))
-                      for t in out)
-              and all(t is None or (t.dtype == torch.int32 and t.shape[1] >= n) for t, n in (
-                  (out.ids, budget), (out.block_table, budget), (out.freed, gone),
-                  (out.attention_block_table, budget), (out.attention_freed, gone))),
-              "out must be an Eviction of these shapes")
-
-    ids, new_lens, new_acc, table, freed, table2, freed2 = out
-    e = _eviction_image(
-        budget, init_blocks, local_blocks, block_table.data_ptr(), _row_stride(block_table),
-        table.data_ptr(), _row_stride(table), freed.data_ptr(), _row_stride(freed),
-        *((0,) * 6 if second is None else
-          (second.data_ptr(), _row_stride(second), table2.data_ptr(), _row_stride(table2),
-           freed2.data_ptr(), _row_stride(freed2))),
-        ids.data_ptr(), _row_stride(ids), new_acc.data_ptr(), _row_stride(new_acc),
-        new_lens.data_ptr())
-    with _on(dev):
-        _check(lib.mm3idx_evict_blocks(w, e, _stream(dev, stream)), "mm3idx_evict_blocks")
-    return out
+    with _HERE if stream is None else _run_on(stream, acc):
+        return Eviction._make(_binding.evict_blocks(
+            acc, seq_lens, block_table, attention_block_table, block_weights, ids, budget,
+            init_blocks, local_blocks, max_seq_len, query_len, decay, in_place, out))
 
 
 def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, draft_lens=None,
@@ -1028,58 +854,9 @@ def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, dra
     [num_reqs, drafts + 1]; draft_lens int32 [num_reqs] when requests have
     fewer.  Returns (tokens int32 [num_reqs, drafts + 1]: the accepted drafts,
     the drawn token, then -1; the number accepted, int32 [num_reqs])."""
-    dtype, dev = target_probs.dtype, target_probs.device
-    if not (target_probs.ndim == 3 and (dtype is torch.float32 or dtype is torch.bfloat16
-                                        or dtype is torch.float16)):
-        raise ValueError("target_probs must be fp32, bf16 or fp16 [num_reqs, drafts + 1, vocab]")
-    reqs, rows, vocab = target_probs.shape
-    tr, tt, one = target_probs.stride()
-    if (one != 1 and vocab != 1) or rows < 1:
-        raise ValueError("target_probs must have drafts + 1 rows of contiguous vocab")
-    k = rows - 1
-    if not (draft_tokens.dtype is torch.int32 and draft_tokens.shape == (reqs, k)
-            and (k <= 1 or draft_tokens.stride(1) == 1)):
-        raise ValueError("draft_tokens must be int32 [num_reqs, drafts] with unit inner stride")
-    if not (uniforms.dtype is torch.float32 and uniforms.shape == (reqs, rows)
-            and (k == 0 or uniforms.stride(1) == 1)):
-        raise ValueError("uniforms must be fp32 [num_reqs, drafts + 1] with unit inner stride")
-    draft_at = dr = dt = 0
-    if draft_probs is not None:
-        if not (draft_probs.dtype is dtype and draft_probs.shape == (reqs, k, vocab)):
-            raise ValueError("draft_probs must be [num_reqs, drafts, vocab] of target_probs' type")
-        dr, dt, one = draft_probs.stride()
-        if one != 1 and vocab != 1:
-            raise ValueError("draft_probs must have contiguous vocab")
-        draft_at = draft_probs.data_ptr()
-    lens_at = 0
-    if draft_lens is not None:
-        if not (draft_lens.dtype is torch.int32 and draft_lens.is_contiguous()
-                and draft_lens.shape == (reqs,)):
-            raise ValueError("draft_lens must be contiguous int32 [num_reqs]")
-        lens_at = draft_lens.data_ptr()
-    if not (target_probs.is_cuda and draft_tokens.device == dev and uniforms.device == dev
-            and (draft_probs is None or draft_probs.device == dev)
-            and (draft_lens is None or draft_lens.device == dev)):
-        raise ValueError("all inputs must be on the same GPU")
-    if out is None or accepted is None:
-        with _allocating_on(stream):
-            if out is None:
-                out = torch.empty((reqs, rows), dtype=torch.int32, device=dev)
-            if accepted is None:
-                accepted = torch.empty((reqs,), dtype=torch.int32, device=dev)
-    if not (out.dtype is torch.int32 and out.shape == (reqs, rows) and out.device == dev
-            and (k == 0 or out.stride(1) == 1) and accepted.dtype is torch.int32
-            and accepted.shape == (reqs,) and accepted.is_contiguous()
-            and accepted.device == dev):
-        raise ValueError("out must be int32 [num_reqs, drafts + 1] with unit inner stride, "
-                         "accepted int32 [num_reqs]")
-    image = _drafts_image(
-        target_probs.data_ptr(), tr, tt, draft_at, dr, dt, TYPES[dtype], draft_tokens.data_ptr(),
-        _row_stride(draft_tokens), lens_at, uniforms.data_ptr(), _row_stride(uniforms), reqs, k,
-        vocab, out.data_ptr(), _row_stride(out), accepted.data_ptr())
-    with _on(dev):
-        _check(lib.mm3idx_verify_drafts(image, _stream(dev, stream)), "mm3idx_verify_drafts")
-    return out, accepted
+    with _HERE if stream is None else _run_on(stream, target_probs):
+        return _binding.verify_drafts(target_probs, draft_tokens, uniforms, draft_probs,
+                                      draft_lens, out, accepted)
 
 
 def _stream_device(stream):

@@ -1202,16 +1202,18 @@ template <int KV, int D, int RT>
 cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                       int grid, cudaStream_t s) {
   using C = Cfg<KV, D>;
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<KV, D, RT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  // The register split waits for what the launch does not have: never launch
-  // a build that got fewer.
-  static const int regs = [] {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    // The register split waits for what the launch does not have: never
+    // launch a build that got fewer.
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, attention_kernel<KV, D, RT>) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+    const cudaError_t err = cudaFuncGetAttributes(&at, attention_kernel<KV, D, RT>);
+    if (err != cudaSuccess) return err;
+    if (at.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(attention_kernel<KV, D, RT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);

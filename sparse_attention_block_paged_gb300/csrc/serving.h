@@ -3,6 +3,7 @@
 // verification), shared by their C ABI (api_serving.cu) and kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -110,6 +111,19 @@ struct DraftArgs {
   int32_t* accepted;
   int32_t* status;
 };
+
+// Runs f, which sets a kernel's attributes, once for each device (`done`: a
+// bit a device, one word a kernel); the attributes stay with the device.
+template <class F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F f) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if ((e = f()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 cudaError_t launch_attention(const CUtensorMap& kmap, const CUtensorMap& vmap,
                              const AttentionArgs& a, int grid, cudaStream_t s);

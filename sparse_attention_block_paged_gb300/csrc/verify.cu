@@ -353,8 +353,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
 
 template <int TYPE>
 cudaError_t launch_t(const DraftArgs& a, int cluster, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(verify_kernel<TYPE>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(verify_kernel<TYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_reqs) * cluster);
