@@ -201,6 +201,7 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   a.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
   a.table = p->page_table;
   a.table_stride = p->table_stride;
+  a.table_width = p->table_width;
   a.seq_lens = p->seq_lens;
   a.num_reqs = p->num_reqs;
   a.query_len = p->query_len;

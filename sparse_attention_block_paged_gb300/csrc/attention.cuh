@@ -61,7 +61,8 @@ namespace attn {
 constexpr int kConsumers = 8;                    // warps
 constexpr int kProducer = kConsumers;            // warp of the keys' copies; the next: the values'
 constexpr int kWeigher = kConsumers + 2;         // warp that writes the tiles' weights
-constexpr int kThreads = (kConsumers + 4) * 32;  // three warpgroups, the last one half empty
+constexpr int kSpare = kConsumers + 3;           // warp that sees to empty requests
+constexpr int kThreads = (kConsumers + 4) * 32;  // three warpgroups
 // Registers a thread: the launch's, and the split of them (setmaxnreg) between
 // the consumers' two warpgroups and the third, whose sum is the launch's.
 constexpr int kRegsLaunch = 168, kRegsConsumer = 216, kRegsOther = 72;
@@ -109,9 +110,15 @@ struct Const {
   static constexpr int value = V;
 };
 
-struct Misc {
+// A gang's share [lo, hi) of the list of `total` positions that `grid` gangs
+// share, its first and last task and their first positions.
+struct Share {
   long long lo, hi, total, p0, pl;
   int t0, tl, grid;
+};
+
+struct Misc {
+  Share share;
   int abort, last;
   long long scan[kConsumers];
 };
@@ -138,8 +145,56 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// The consumer threads: this gang's share of the list and the tasks at its ends.
-__device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
+__device__ __forceinline__ int length_bits(const AttentionArgs& a, int raw) {
+  return (raw > a.max_seq_len ? MM3IDX_DEV_SEQ_TOO_LONG : 0) |
+         (raw != 0 && raw < a.query_len ? MM3IDX_DEV_SEQ_TOO_SHORT : 0);
+}
+
+// This gang's bounds in a list of `total` positions.  No share is empty: at
+// most one gang per kMinShare positions takes part.
+__device__ __forceinline__ void bounds(const AttentionArgs& a, long long total, Share& s) {
+  const long long most = total / kMinShare;
+  const int gangs = static_cast<int>(gridDim.x) / a.gang;
+  s.grid = static_cast<int>(most < 1 ? 1 : most < gangs ? most : gangs);
+  const long long c = blockIdx.x / a.gang;
+  s.total = total;
+  s.lo = c < s.grid ? quotient(total * c, s.grid) : 0;
+  s.hi = c < s.grid ? quotient(total * (c + 1), s.grid) : 0;
+}
+
+// Up to 32 requests, one a lane: every warp finds the share by itself, without
+// a barrier.
+__device__ __forceinline__ Share share_of_few(const AttentionArgs& a, bool report) {
+  const int lane = threadIdx.x & 31;
+  const int raw = lane < a.num_reqs ? __ldg(a.seq_lens + lane) : 0;
+  const long long one = task_slots(min(max(raw, 0), a.max_seq_len)), mine = one * a.tasks;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (report) {
+    const int bits = lane < a.num_reqs ? length_bits(a, raw) : 0;
+    if (bits) atomicOr(a.status, bits);
+  }
+  Share s;
+  bounds(a, __shfl_sync(0xffffffffu, incl, 31), s);
+  auto find = [&](long long x, int& task, long long& pos) {
+    const long long before = incl - mine;
+    const unsigned here = __ballot_sync(0xffffffffu, before <= x && x < incl);
+    const int h = here >> lane & 1u ? static_cast<int>(quotient(x - before, one)) : 0;
+    const int src = here ? __ffs(here) - 1 : 0;
+    task = __shfl_sync(0xffffffffu, lane * a.tasks + h, src);
+    pos = __shfl_sync(0xffffffffu, before + h * one, src);
+  };
+  find(s.lo, s.t0, s.p0);
+  find(s.hi - 1, s.tl, s.pl);
+  return s;
+}
+
+// Any number of requests, by the consumer threads, into shared memory.
+__device__ __forceinline__ void share_of_many(const AttentionArgs& a, Misc* m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.num_reqs + kConsumers * 32 - 1) / (kConsumers * 32);
   const int first = min(tid * per, a.num_reqs), end = min(first + per, a.num_reqs);
@@ -147,8 +202,7 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
   int bits = 0;
   for (int i = first; i < end; ++i) {
     const int raw = __ldg(a.seq_lens + i);
-    if (raw > a.max_seq_len) bits |= MM3IDX_DEV_SEQ_TOO_LONG;
-    if (raw != 0 && raw < a.query_len) bits |= MM3IDX_DEV_SEQ_TOO_SHORT;
+    bits |= length_bits(a, raw);
     mine += task_slots(min(max(raw, 0), a.max_seq_len));
   }
   if (bits && blockIdx.x == 0) atomicOr(a.status, bits);
@@ -168,39 +222,49 @@ __device__ __forceinline__ void partition(const AttentionArgs& a, Misc* m) {
     if (w < warp) before += s;
     total += s;
   }
-  // No share is empty: at most one gang per kMinShare positions takes part.
-  const long long most = total / kMinShare;
-  const int gangs = gridDim.x / a.gang;
-  const int G = static_cast<int>(most < 1 ? 1 : most < gangs ? most : gangs);
-  const long long c = blockIdx.x / a.gang;
-  const long long lo = c < G ? quotient(total * c, G) : 0;
-  const long long hi = c < G ? quotient(total * (c + 1), G) : 0;
+  Share s;
+  bounds(a, total, s);
   if (tid == 0) {
-    m->lo = lo;
-    m->hi = hi;
-    m->total = total;
-    m->grid = G;
+    m->share.lo = s.lo;
+    m->share.hi = s.hi;
+    m->share.total = s.total;
+    m->share.grid = s.grid;
   }
-  if (hi <= lo || mine == 0) return;
-  const bool has_lo = before <= lo && lo < before + mine;
-  const bool has_hi = before <= hi - 1 && hi - 1 < before + mine;
+  if (s.hi <= s.lo || mine == 0) return;
+  const bool has_lo = before <= s.lo && s.lo < before + mine;
+  const bool has_hi = before <= s.hi - 1 && s.hi - 1 < before + mine;
   if (!has_lo && !has_hi) return;
   long long P = before;
   for (int i = first; i < end; ++i) {
     const long long one = task_slots(request_len(a, i));
     const long long all = one * a.tasks;
-    if (has_lo && P <= lo && lo < P + all) {
-      const int h = static_cast<int>(quotient(lo - P, one));
-      m->t0 = i * a.tasks + h;
-      m->p0 = P + h * one;
+    if (has_lo && P <= s.lo && s.lo < P + all) {
+      const int h = static_cast<int>(quotient(s.lo - P, one));
+      m->share.t0 = i * a.tasks + h;
+      m->share.p0 = P + h * one;
     }
-    if (has_hi && P <= hi - 1 && hi - 1 < P + all) {
-      const int h = static_cast<int>(quotient(hi - 1 - P, one));
-      m->tl = i * a.tasks + h;
-      m->pl = P + h * one;
+    if (has_hi && P <= s.hi - 1 && s.hi - 1 < P + all) {
+      const int h = static_cast<int>(quotient(s.hi - 1 - P, one));
+      m->share.tl = i * a.tasks + h;
+      m->share.pl = P + h * one;
     }
     P += all;
   }
+}
+
+// Lines of the lengths, the page table and the queries on their way to L2
+// (one a lane of one warp in every CTA) while the kernel before this one ends:
+// they are read again, as they then are, after it.
+__device__ __forceinline__ void prefetch_inputs(const AttentionArgs& a) {
+  const int64_t line = (static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31)) * 128;
+  auto pull = [&](const void* p, int64_t bytes) {
+    if (line < bytes)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + line));
+  };
+  pull(a.seq_lens, 4 * static_cast<int64_t>(a.num_reqs));
+  pull(a.table, 4 * ((a.num_reqs - 1) * a.table_stride + a.table_width));
+  if (a.q_tok > 0 && a.q_head <= a.q_tok)
+    pull(a.q, 2 * ((static_cast<int64_t>(a.num_reqs) * a.query_len - 1) * a.q_tok + a.head_dim));
 }
 
 // Which of its gang's heads a CTA works on: the CTAs of a gang are neighbours
@@ -221,8 +285,8 @@ struct Segment {
 struct Walker {
   long long lo, hi, p0, pl, P;
   int t0, tl, t, stage;
-  __device__ explicit Walker(const Misc* m)
-      : lo(m->lo), hi(m->hi), p0(m->p0), pl(m->pl), P(0), t0(m->t0), tl(m->tl), t(0), stage(0) {}
+  __device__ explicit Walker(const Share& s)
+      : lo(s.lo), hi(s.hi), p0(s.p0), pl(s.pl), P(0), t0(s.t0), tl(s.tl), t(0), stage(0) {}
   __device__ __forceinline__ bool emit(const AttentionArgs& a, int task, long long pos,
                                        Segment& s) const {
     s.req = task / a.tasks;
@@ -464,13 +528,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
+  if (warp == kSpare) prefetch_inputs(a);
+  __syncthreads();
   // A programmatic dependent launch: what the kernel before it wrote is read
   // (and the workspace it used is written) only after this.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp < kConsumers) partition(a, misc);
-  __syncthreads();
-  Walker walk(misc);
+  Share share;
+  if (a.num_reqs <= 32) {
+    share = share_of_few(a, blockIdx.x == 0 && warp == 0);
+    if (threadIdx.x == 0) misc->share = share;    // for the joins, behind their barriers
+  } else {
+    if (warp < kConsumers) share_of_many(a, misc);
+    __syncthreads();
+    share = misc->share;
+  }
+  Walker walk(share);
   Segment sg;
 
   if (warp >= kConsumers) {
@@ -576,6 +649,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    } else if (warp == kSpare) {
+      // ------------------------------------------- rows of empty requests
+      const int heads = a.kv_heads * a.group;
+      for (int i = blockIdx.x; i < a.num_reqs; i += gridDim.x) {
+        if (request_len(a, i) > 0) continue;
+        const int per_row = heads * (D / 8);
+        for (int e = lane; e < a.query_len * per_row; e += 32) {
+          const int64_t row = static_cast<int64_t>(i) * a.query_len + e / per_row;
+          const int h = e % per_row / (D / 8), d = e % (D / 8) * 8;
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head + d;
+          *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+          if (d == 0) {
+            if (a.lse) a.lse[row * a.lse_tok + h] = -INFINITY;
+            if (weigh) a.row_lse[row * heads + h] = -INFINITY;
+          }
+        }
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
@@ -601,25 +691,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       koff = twisted((first + g) * C::kRow + c * (D / 4));
       voff0 = twisted((first + 2 * c) * C::kRow + g * 4);
       voff1 = twisted((first + 2 * c + 1) * C::kRow + g * 4);
-    }
-
-    // Rows of empty requests.
-    {
-      const int heads = a.kv_heads * a.group;
-      for (int i = blockIdx.x * kConsumers + warp; i < a.num_reqs; i += gridDim.x * kConsumers) {
-        if (request_len(a, i) > 0) continue;
-        const int per_row = heads * (D / 8);
-        for (int e = lane; e < a.query_len * per_row; e += 32) {
-          const int64_t row = static_cast<int64_t>(i) * a.query_len + e / per_row;
-          const int h = e % per_row / (D / 8), d = e % (D / 8) * 8;
-          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head + d;
-          *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
-          if (d == 0) {
-            if (a.lse) a.lse[row * a.lse_tok + h] = -INFINITY;
-            if (weigh) a.row_lse[row * heads + h] = -INFINITY;
-          }
-        }
-      }
     }
 
     const int R = a.group * a.query_len;
@@ -1100,95 +1171,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Publish; the last CTA of the task joins the partial results.  (The
         // barrier orders the CTA's stores before thread 0's release.)
         const long long pb = sg.pos + kSegCost;
-        const int lead = gang_of(pb, misc->total, misc->grid);
-        const int parts = gang_of(pb + sg.nb - 1, misc->total, misc->grid) - lead + 1;
+        const int lead = gang_of(pb, misc->share.total, misc->share.grid);
+        const int parts = gang_of(pb + sg.nb - 1, misc->share.total, misc->share.grid) - lead + 1;
         if (threadIdx.x == 0)
           misc->last = !dead && ticket(a.tickets + sg.unit, parts - 1) == parts - 1;
         consumer_sync();
         if (misc->last) {
-          // A thread takes four columns of up to UB rows at a time, the partial
-          // results in order, UB x PB = 16 loads in flight.
+          // Four columns of a row are a unit.  A thread takes up to UB units, their
+          // partial results in order, UB x PB = 16 loads in flight.
           constexpr int kStride = kConsumers * 32;
           const int member = member_of(a);
-          const bool second = sg.pos > quotient(misc->total * lead, misc->grid);
+          const bool second = sg.pos > quotient(misc->share.total * lead, misc->share.grid);
           const int units = rows * (D / 4);
-          auto join_parts = [&](auto ub, auto pb) {
+          auto gather = [&](auto ub, auto pb, int u0, int t_first, int t_step, float* m, float* l,
+                            float4* o) {
             constexpr int UB = decltype(ub)::value, PB = decltype(pb)::value;
+#pragma unroll
+            for (int u = 0; u < UB; ++u) {
+              m[u] = -INFINITY;
+              l[u] = 0.0f;
+              o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
 #pragma unroll 1
-            for (int u0 = threadIdx.x; u0 < units; u0 += UB * kStride) {
-              float m[UB], l[UB];
-              float4 o[UB];
+            for (int t0 = t_first; t0 < parts; t0 += t_step) {
+              float2 x[UB][PB];
+              float4 v[UB][PB];
 #pragma unroll
-              for (int u = 0; u < UB; ++u) {
-                m[u] = -INFINITY;
-                l[u] = 0.0f;
-                o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              }
-#pragma unroll 1
-              for (int t0 = 0; t0 < parts; t0 += PB) {
-                float2 x[UB][PB];
-                float4 v[UB][PB];
-#pragma unroll
-                for (int k = 0; k < PB; ++k) {
-                  const int64_t at = 2 * static_cast<int64_t>((lead + t0 + k) * a.gang + member) +
-                                     (t0 + k == 0 && second);
-#pragma unroll
-                  for (int u = 0; u < UB; ++u) {
-                    const int unit = u0 + u * kStride;
-                    x[u][k] = make_float2(-INFINITY, 0.0f);
-                    v[u][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (t0 + k < parts && unit < units) {
-                      x[u][k] = __ldcg(a.part_ml + at * 64 + unit / (D / 4));
-                      v[u][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * 64 * D) + unit);
-                    }
-                  }
-                }
+              for (int k = 0; k < PB; ++k) {
+                const int64_t at = 2 * static_cast<int64_t>((lead + t0 + k) * a.gang + member) +
+                                   (t0 + k == 0 && second);
 #pragma unroll
                 for (int u = 0; u < UB; ++u) {
-                  float top = m[u];
-#pragma unroll
-                  for (int k = 0; k < PB; ++k) top = fmaxf(top, x[u][k].x);
-                  if (top == -INFINITY) continue;
-                  const float f = ex2(m[u] - top);
-                  m[u] = top;
-                  l[u] *= f;
-                  o[u].x *= f; o[u].y *= f; o[u].z *= f; o[u].w *= f;
-#pragma unroll
-                  for (int k = 0; k < PB; ++k) {
-                    const float w = ex2(x[u][k].x - top);
-                    l[u] += x[u][k].y * w;
-                    o[u].x += v[u][k].x * w; o[u].y += v[u][k].y * w;
-                    o[u].z += v[u][k].z * w; o[u].w += v[u][k].w * w;
+                  const int unit = u0 + u * kStride;
+                  x[u][k] = make_float2(-INFINITY, 0.0f);
+                  v[u][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  if (t0 + k < parts && unit < units) {
+                    x[u][k] = __ldcg(a.part_ml + at * 64 + unit / (D / 4));
+                    v[u][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * 64 * D) + unit);
                   }
                 }
               }
 #pragma unroll
               for (int u = 0; u < UB; ++u) {
-                const int unit = u0 + u * kStride;
-                if (unit >= units) break;
-                const int r = unit / (D / 4), col = unit % (D / 4) * 4;
-                const int64_t row = tok0 + (row0 + r) / a.group;
-                const int h = head * a.group + (row0 + r) % a.group;
-                const float f = l[u] == 0.0f ? 0.0f : a.v_scale / l[u];
-                uint2 w;
-                if (a.q_type == MM3IDX_TYPE_BF16)
-                  w = make_uint2(pack2<true>(o[u].x * f, o[u].y * f),
-                                 pack2<true>(o[u].z * f, o[u].w * f));
-                else
-                  w = make_uint2(pack2<false>(o[u].x * f, o[u].y * f),
-                                 pack2<false>(o[u].z * f, o[u].w * f));
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok +
-                                          h * a.o_head + col) = w;
-                if (col == 0) {
-                  const float lse2 = l[u] == 0.0f ? -INFINITY : m[u] + lg2(l[u]);
-                  if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
-                  if (weigh) a.row_lse[row * heads + h] = lse2;
+                float top = m[u];
+#pragma unroll
+                for (int k = 0; k < PB; ++k) top = fmaxf(top, x[u][k].x);
+                if (top == -INFINITY) continue;
+                const float f = ex2(m[u] - top);
+                m[u] = top;
+                l[u] *= f;
+                o[u].x *= f; o[u].y *= f; o[u].z *= f; o[u].w *= f;
+#pragma unroll
+                for (int k = 0; k < PB; ++k) {
+                  const float w = ex2(x[u][k].x - top);
+                  l[u] += x[u][k].y * w;
+                  o[u].x += v[u][k].x * w; o[u].y += v[u][k].y * w;
+                  o[u].z += v[u][k].z * w; o[u].w += v[u][k].w * w;
                 }
               }
             }
           };
-          if (units > 2 * kStride) join_parts(Const<4>{}, Const<4>{});
-          else join_parts(Const<2>{}, Const<8>{});
+          auto finish = [&](int unit, float m, float l, float4 o) {
+            const int r = unit / (D / 4), col = unit % (D / 4) * 4;
+            const int64_t row = tok0 + (row0 + r) / a.group;
+            const int h = head * a.group + (row0 + r) % a.group;
+            const float f = l == 0.0f ? 0.0f : a.v_scale / l;
+            uint2 w;
+            if (a.q_type == MM3IDX_TYPE_BF16)
+              w = make_uint2(pack2<true>(o.x * f, o.y * f), pack2<true>(o.z * f, o.w * f));
+            else
+              w = make_uint2(pack2<false>(o.x * f, o.y * f), pack2<false>(o.z * f, o.w * f));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
+                                      col) = w;
+            if (col == 0) {
+              const float lse2 = l == 0.0f ? -INFINITY : m + lg2(l);
+              if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
+              if (weigh) a.row_lse[row * heads + h] = lse2;
+            }
+          };
+          if (units > kStride) {
+            constexpr int UB = 4;
+#pragma unroll 1
+            for (int u0 = threadIdx.x; u0 < units; u0 += UB * kStride) {
+              float m[UB], l[UB];
+              float4 o[UB];
+              gather(Const<UB>{}, Const<4>{}, u0, 0, 4, m, l, o);
+#pragma unroll
+              for (int u = 0; u < UB; ++u)
+                if (u0 + u * kStride < units) finish(u0 + u * kStride, m[u], l[u], o[u]);
+            }
+          } else {
+            // Few columns: with many parts `turns` threads a unit, every
+            // turns-th eight parts each, joined through shared memory in order.
+            const int turns = parts <= 8 || units > kStride / 2 ? 1 : units > kStride / 4 ? 2 : 4;
+            const int each = kStride / turns, unit = threadIdx.x % each, turn = threadIdx.x / each;
+            float m, l;
+            float4 o;
+            gather(Const<1>{}, Const<8>{}, unit, turn * 8, turns * 8, &m, &l, &o);
+            if (turns > 1) {
+              float* mine = red + threadIdx.x * 6;
+              mine[0] = m; mine[1] = l; mine[2] = o.x; mine[3] = o.y; mine[4] = o.z; mine[5] = o.w;
+              consumer_sync();
+              for (int t = 1; t < turns && turn == 0; ++t) {
+                const float* from = red + (t * each + unit) * 6;
+                const float top = fmaxf(m, from[0]);
+                if (top == -INFINITY) continue;
+                const float f = ex2(m - top), w = ex2(from[0] - top);
+                m = top;
+                l = l * f + from[1] * w;
+                o.x = o.x * f + from[2] * w; o.y = o.y * f + from[3] * w;
+                o.z = o.z * f + from[4] * w; o.w = o.w * f + from[5] * w;
+              }
+              consumer_sync();      // `red` is free again
+            }
+            if (turn == 0 && unit < units) finish(unit, m, l, o);
+          }
         }
       }
       sg = after;

@@ -35,6 +35,7 @@ struct AttentionArgs {
   int32_t page_shift;         // log2 of the page's tokens
   const int32_t* table;
   int64_t table_stride;
+  int32_t table_width;
   const int32_t* seq_lens;
   int32_t num_reqs, query_len, max_seq_len;
   float scale;                // sm_scale * k_scale
