@@ -7,6 +7,7 @@ namespace mm3idx {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kAhead = 8;
 
 // block_weights[row, b] = sum over the heads of 2^(tile - row), the base-2
 // log-sum-exps of the row's scores in the block and in all: one thread per
@@ -20,14 +21,24 @@ __global__ void __launch_bounds__(kThreads) block_weight_kernel(const AttentionA
   const int len = min(max(__ldg(a.seq_lens + i), 0), a.max_seq_len);
   float sum = 0.0f;
   if (b * kBlock < len - a.query_len + j + 1) {
+    const int first = j * a.group;                 // rows of the kv head, 64 a task
     for (int h = 0; h < a.kv_heads; ++h) {
       const float* lse = a.row_lse + (row * a.kv_heads + h) * a.group;
-      for (int k = 0; k < a.group; ++k) {
-        const int r = j * a.group + k;             // row of the kv head: 64 a task
-        const int64_t task = (static_cast<int64_t>(i) * a.kv_heads + h) * a.row_tiles + r / 64;
-        const float all = lse[k];
-        if (all == -INFINITY) continue;
-        sum += exp2f(a.tile_lse[(task * a.w_width + b) * pitch + r % 64] - all);
+      const float* tile = a.tile_lse +
+                          ((static_cast<int64_t>(i) * a.kv_heads + h) * a.row_tiles * a.w_width + b) * pitch;
+      const int64_t next = static_cast<int64_t>(a.w_width) * pitch;
+      for (int k0 = 0; k0 < a.group; k0 += kAhead) {
+        float x[kAhead], all[kAhead];              // in flight together
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = first + k0 + k;
+          const bool in = k0 + k < a.group;
+          all[k] = in ? __ldcg(lse + k0 + k) : -INFINITY;
+          x[k] = in ? __ldcg(tile + (r >> 6) * next + (r & 63)) : -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (all[k] != -INFINITY) sum += exp2f(x[k] - all[k]);
       }
     }
   }
