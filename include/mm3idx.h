@@ -467,18 +467,21 @@ typedef struct mm3idx_attention {
  *
  * workspace: >= mm3idx_attention_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use and kept by the caller for the
- * next call, under the rules of mm3idx_decode.  One workspace serves every
- * batch that its bounds cover.  Device status: MM3IDX_DEV_BAD_PAGE,
+ * next call, under the rules of mm3idx_decode (launches that share one must
+ * not overlap; zero it again after MM3IDX_DEV_TIMEOUT).  One workspace, given
+ * with the same size each time, serves every batch of a model whose num_reqs,
+ * query_len, max_seq_len and block weights stay within those it was sized for.
+ * Outputs must not overlap inputs or each other.  Device status: MM3IDX_DEV_BAD_PAGE,
  * _SEQ_TOO_LONG, _SEQ_TOO_SHORT (0 < seq_len < query_len), _TIMEOUT.
  */
 int mm3idx_paged_attention(const mm3idx_attention_t *a, void *workspace, size_t workspace_bytes,
                            void *stream);
 
 /*
- * mm3idx_attention_workspace_bytes -- workspace of mm3idx_paged_attention: a
- * ticket per (request, kv head), the partial results of those that are split
- * across CTAs, and with block_weights != 0 one fp32 per (row, query head,
- * block).  Reads the current device's SM count; no allocation.
+ * mm3idx_attention_workspace_bytes -- workspace of mm3idx_paged_attention: the
+ * partial results of requests that are split across CTAs, with block_weights
+ * != 0 one fp32 per (row, query head, block), and a ticket per (request, kv
+ * head).  Reads the current device's SM count; no allocation.
  */
 int mm3idx_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                      int32_t num_reqs, int32_t query_len, int32_t max_seq_len,
@@ -585,6 +588,7 @@ typedef struct mm3idx_drafts {
  * clamped to 0..1, NaN counts as 0, and every fp32 value from 2^-23 on is
  * exact), which makes the token independent of the order of the sum.  A row
  * without any weight gives token vocab - 1.  A row must sum to less than 2^17.
+ * Outputs must not overlap inputs.
  */
 int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
 

@@ -168,6 +168,69 @@ def test_strided_queries_and_wide_bounds(mm):
     check(got, R.attention_ref(t))
 
 
+def test_one_workspace_for_batches_of_many_sizes(mm):
+    """Small and large batches, with and without weights, take turns on a workspace made for the
+    largest: what one leaves behind does not disturb the next."""
+    lens = [[9000], [700 + 13 * i for i in range(400)], [5000, 20, 0, 3000], [64] * 300, [20000, 1]]
+    ws = mm.new_attention_workspace(8, 2, 128, 400, 1, 20000, block_weights=True)
+    made = [R.make_attention(n, group=4, kvh=2, page=64, seed=40 + k) for k, n in enumerate(lens)]
+    want = [call(mm, s, weights=k % 2 == 0) for k, s in enumerate(made)]
+    for _ in range(2):
+        for k, s in enumerate(made):
+            got = call(mm, s, weights=k % 2 == 0, workspace=ws)
+            assert torch.equal(got[0], want[k][0])
+            assert k % 2 or torch.equal(got[2], want[k][2])
+    check(want[4], R.attention_ref(made[4]))
+    assert mm.get_device_error() == 0
+
+
+def test_two_calls_at_once(mm):
+    """Calls on two streams, each with its own workspace, side by side."""
+    made = [R.make_attention([3000, 17, 9000], ql=2, group=8, kvh=2, page=32, seed=60),
+            R.make_attention([800] * 40, group=2, kvh=2, page=16, seed=61, kv=E4M3)]
+    want = [call(mm, s, weights=False)[0] for s in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    wss = [mm.new_attention_workspace(s["q"].shape[1], 2, 128, s["lens"].shape[0], s["ql"], 9000)
+           for s in made]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for s, stream, ws in zip(made, streams, wss):
+            outs.append(mm.paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"],
+                                           query_len=s["ql"], max_seq_len=s["max_seq_len"],
+                                           sm_scale=s["sm_scale"], workspace=ws, stream=stream))
+    torch.cuda.synchronize()
+    for k, out in enumerate(outs):
+        assert torch.equal(out, want[k % 2])
+
+
+def test_refusals_with_real_tensors(mm):
+    s = R.make_attention([300], group=4, kvh=2, page=64, seed=62)
+    ws = mm.new_attention_workspace(8, 2, 128, 1, 1, 300)
+
+    def go(**kw):
+        names = ("q", "k", "v", "table", "lens")
+        a = {k: kw.pop(k, s[k]) for k in names}
+        return mm.paged_attention(a["q"], a["k"], a["v"], a["table"], a["lens"],
+                                  **{**dict(query_len=1, max_seq_len=300, sm_scale=1.0), **kw})
+
+    for kw, status in [(dict(workspace=ws[:ws.numel() - 256]), -9), (dict(workspace=ws[8:]), -9),
+                       (dict(max_seq_len=400), -4), (dict(sm_scale=0.0), -1),
+                       (dict(q=s["q"][:, :7]), -13), (dict(max_seq_len=0), -6),
+                       (dict(out=torch.empty((1, 8, 132), dtype=BF16, device="cuda")[:, :, :128]),
+                        -14)]:
+        with pytest.raises(mm.Mm3idxError) as e:
+            go(**kw)
+        assert e.value.status == status
+    for kw in (dict(workspace=ws.cpu()), dict(lens=s["lens"].cpu()),
+               dict(out=torch.empty_like(s["q"]).half()), dict(query_len=2),
+               dict(lse=torch.empty((1, 7), device="cuda")),
+               dict(block_weights=torch.empty((1, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            go(**kw)
+    assert torch.isfinite(go(workspace=ws)).all()
+
+
 def test_far_pages(mm):
     """Pages that lie more than 2^32 bytes into the cache."""
     pages, page = 2 ** 18 + 5, 128

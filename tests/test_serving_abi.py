@@ -67,7 +67,8 @@ def test_attention_accepts_an_empty_batch_and_null():
     assert size(7, 2, 128, 1, 1, 100, 0, ctypes.byref(n)) == -13
     assert size(8, 2, 100, 1, 1, 100, 0, ctypes.byref(n)) == -13
     assert size(8, 2, 128, -1, 1, 100, 0, ctypes.byref(n)) == -1
-    assert size(8, 2, 128, 1, 0, 100, 0, ctypes.byref(n)) == -1
+    assert size(8, 2, 128, 1, 0, 100, 0, ctypes.byref(n)) == -6
+    assert size(8, 2, 128, 1, 1, 0, 0, ctypes.byref(n)) == -6
     assert size(8, 2, 128, 1, 1, 100, 0, None) == -1
 
 
