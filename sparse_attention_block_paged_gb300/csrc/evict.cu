@@ -39,6 +39,10 @@ constexpr int kFastWidth = kMaxItems * kFastThreads;   // blocks: a million toke
 __device__ __forceinline__ uint32_t rank_bits(float w) {
   return w != w ? 0xFFFFFFFFu : ordered_bits(w);
 }
+// The weight of a place (NaN for all NaNs; -0 comes back as 0).
+__device__ __forceinline__ float weight_at(uint32_t r) {
+  return __uint_as_float((r & 0x80000000u) ? r ^ 0x80000000u : ~r);
+}
 
 // high + low, a sum in about twice fp32's digits.
 struct Sum {
@@ -212,21 +216,22 @@ __device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at
   for (int k = 0; k < ITEMS; ++k) at[k] += counts[k * warps + warp];
 }
 
-// The threshold and the places at it: `picks` of the keys for which `each`
-// calls back stay, those above `cut` and the first `ties` at it.  `each(f)`
-// applies f to this thread's keys (no more than 31); called by all threads.
-template <class Each>
-__device__ __forceinline__ void threshold(int picks, Exchange& ex, int& turn, Each each,
-                                          uint32_t& cut, int& ties) {
+// The threshold among this CTA's keys (0: none, which no weight has): `picks`
+// of them stay, those above `cut` and the first `ties` at it.
+template <int ITEMS>
+__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int picks, Exchange& ex,
+                                          int& turn, uint32_t& cut, int& ties) {
+  static_assert(32 * ITEMS < 1024, "packed counts of a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   cut = 0xFFFFFFFFu;
   ties = 0;
   if (picks == 0) return;
   uint32_t top = 0, bottom = 0xFFFFFFFFu;
-  each([&](uint32_t r) {
-    top = max(top, r);
-    bottom = min(bottom, r);
-  });
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    top = max(top, key[k]);
+    if (key[k]) bottom = min(bottom, key[k]);
+  }
   top = __reduce_max_sync(0xffffffffu, top);
   bottom = __reduce_min_sync(0xffffffffu, bottom);
   if (lane == 0) {
@@ -244,9 +249,9 @@ __device__ __forceinline__ void threshold(int picks, Exchange& ex, int& turn, Ea
   for (; shift >= 0; shift -= 2) {
     const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
     uint32_t c = 0;
-    each([&](uint32_t r) {
-      c += (r >= t1 ? 1u : 0u) + (r >= t2 ? 1u << 10 : 0u) + (r >= t3 ? 1u << 20 : 0u);
-    });
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      c += (key[k] >= t1 ? 1u : 0u) + (key[k] >= t2 ? 1u << 10 : 0u) + (key[k] >= t3 ? 1u << 20 : 0u);
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) ex.word[turn & 1][warp] = c;
     __syncthreads();
@@ -255,7 +260,7 @@ __device__ __forceinline__ void threshold(int picks, Exchange& ex, int& turn, Ea
     const int c1 = __reduce_add_sync(0xffffffffu, c & 1023u);
     const int c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
     const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
-    int here;
+    int here = 0;
     if (c3 >= picks) {
       cut = t3;
       here = c3;
@@ -268,7 +273,6 @@ __device__ __forceinline__ void threshold(int picks, Exchange& ex, int& turn, Ea
       here = c1;
       above = c2;
     } else {
-      here = 0;
       above = c1;
     }
     if (here == picks) {       // exactly the keys from cut on
@@ -369,28 +373,21 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     }
   }
   const int kept = min(n, e.budget), f_lo = e.init_blocks, l_lo = n - e.local_blocks;
-  uint32_t cut = 0;
+  uint32_t place[ITEMS], key[ITEMS], cut = 0, stays = 0, tied = 0;
   int ties = 0, turn = 0;
   const bool full = n > e.budget;
-  if (full)
-    threshold(kept - (n - max(0, l_lo - f_lo)), ex, turn,
-              [&](auto f) {
-#pragma unroll
-                for (int k = 0; k < ITEMS; ++k) {
-                  const int b = k * T + threadIdx.x;
-                  if (b >= f_lo && b < l_lo) f(rank_bits(w[k]));
-                }
-              },
-              cut, ties);
-  // Which blocks stay, and the columns they move to.
-  uint32_t stays = 0, tied = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const int b = k * T + threadIdx.x;
-    const bool open = full && b >= f_lo && b < l_lo;
-    const uint32_t r = rank_bits(w[k]);
-    if (b < n && (!open || r > cut)) stays |= 1u << k;
-    if (open && r == cut) tied |= 1u << k;
+    place[k] = rank_bits(w[k]);
+    key[k] = full && b >= f_lo && b < l_lo ? place[k] : 0u;
+  }
+  if (full) threshold<ITEMS>(key, kept - (n - max(0, l_lo - f_lo)), ex, turn, cut, ties);
+  // Which blocks stay, and the columns they move to.
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (k * T + threadIdx.x < n && (!key[k] || key[k] > cut)) stays |= 1u << k;
+    if (full && key[k] == cut) tied |= 1u << k;
   }
   int at[ITEMS];
   if (ties > 0) {
@@ -408,7 +405,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     const bool stay = (stays >> k) & 1u;
     if (stay) {
       if (e.ids) e.ids[i * e.ids_stride + at[k]] = b;
-      e.acc_out[i * e.acc_out_stride + at[k]] = w[k];
+      e.acc_out[i * e.acc_out_stride + at[k]] = weight_at(place[k]);
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
