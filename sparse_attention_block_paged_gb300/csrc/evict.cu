@@ -31,6 +31,7 @@ namespace {
 constexpr int kEntries = MM3IDX_MAX_WEIGHT_ENTRIES;
 constexpr int kWideThreads = 1024;
 constexpr int kSumThreads = 256;
+constexpr int kFew = 1024;
 constexpr int kMaxItems = 8;
 constexpr int kFastThreads = 1024;
 constexpr int kFastWidth = kMaxItems * kFastThreads;   // blocks: a million tokens
@@ -156,6 +157,8 @@ __global__ void __launch_bounds__(kSumThreads)
 struct Exchange {
   uint32_t word[2][32];
   uint32_t top[32], bottom[32];
+  uint32_t list[kFew];         // the keys left in a search
+  int few;
 };
 
 // Exclusive sum of x over the threads before this one, and the total.
@@ -216,12 +219,61 @@ __device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at
   for (int k = 0; k < ITEMS; ++k) at[k] += counts[k * warps + warp];
 }
 
+// Where the search for the threshold stands: it lies in the 2^(shift + 2)
+// places from `cut` on; `from` keys are at or above cut, `above` of them above
+// that interval.
+struct Search {
+  uint32_t cut;
+  int shift, from, above;
+};
+
+// Two bits a round, until the interval is one key, its keys number at most
+// `few`, or a count meets `picks` exactly (returns true: the keys from cut on).
+template <int ITEMS>
+__device__ __forceinline__ bool narrow(const uint32_t (&key)[ITEMS], int picks, int few, Search& s,
+                                       Exchange& ex, int& turn) {
+  static_assert(32 * ITEMS < 1024, "packed counts of a warp");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  while (s.shift >= 0 && s.from - s.above > few) {
+    const uint32_t t1 = s.cut | (1u << s.shift), t2 = s.cut | (2u << s.shift),
+                   t3 = s.cut | (3u << s.shift);
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      c += (key[k] >= t1 ? 1u : 0u) + (key[k] >= t2 ? 1u << 10 : 0u) + (key[k] >= t3 ? 1u << 20 : 0u);
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) ex.word[turn & 1][warp] = c;
+    __syncthreads();
+    c = lane < warps ? ex.word[turn & 1][lane] : 0u;
+    ++turn;
+    const int c1 = __reduce_add_sync(0xffffffffu, c & 1023u);
+    const int c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
+    const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
+    s.shift -= 2;
+    if (c3 >= picks) {
+      s.cut = t3;
+      s.from = c3;
+    } else if (c2 >= picks) {
+      s.cut = t2;
+      s.from = c2;
+      s.above = c3;
+    } else if (c1 >= picks) {
+      s.cut = t1;
+      s.from = c1;
+      s.above = c2;
+    } else {
+      s.above = c1;
+    }
+    if (s.from == picks) return true;
+  }
+  return false;
+}
+
 // The threshold among this CTA's keys (0: none, which no weight has): `picks`
 // of them stay, those above `cut` and the first `ties` at it.
 template <int ITEMS>
-__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int picks, Exchange& ex,
-                                          int& turn, uint32_t& cut, int& ties) {
-  static_assert(32 * ITEMS < 1024, "packed counts of a warp");
+__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int total, int picks,
+                                          Exchange& ex, int& turn, uint32_t& cut, int& ties) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   cut = 0xFFFFFFFFu;
   ties = 0;
@@ -238,50 +290,41 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int pick
     ex.top[warp] = top;
     ex.bottom[warp] = bottom;
   }
+  if (threadIdx.x == 0) ex.few = 0;
   __syncthreads();
   top = __reduce_max_sync(0xffffffffu, lane < warps ? ex.top[lane] : 0u);
   bottom = __reduce_min_sync(0xffffffffu, lane < warps ? ex.bottom[lane] : 0xFFFFFFFFu);
   cut = top;
   ties = picks;
   if (top == bottom) return;
-  int shift = (31 - __clz(top ^ bottom)) & ~1, above = 0;
-  cut = shift == 30 ? 0u : top & ~((4u << shift) - 1u);
-  for (; shift >= 0; shift -= 2) {
-    const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
-    uint32_t c = 0;
+  Search s;
+  s.shift = (31 - __clz(top ^ bottom)) & ~1;
+  s.cut = s.shift == 30 ? 0u : top & ~((4u << s.shift) - 1u);
+  s.from = total;
+  s.above = 0;
+  bool exact = false;
+  if (ITEMS > 1) {
+    // With few keys left in the interval, one a thread: a round over eight
+    // keys a thread costs 0.8 us with 1024 threads, over one 0.3.
+    exact = narrow<ITEMS>(key, picks, min(static_cast<int>(blockDim.x), kFew), s, ex, turn);
+    if (!exact && s.shift >= 0) {
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-      c += (key[k] >= t1 ? 1u : 0u) + (key[k] >= t2 ? 1u << 10 : 0u) + (key[k] >= t3 ? 1u << 20 : 0u);
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) ex.word[turn & 1][warp] = c;
-    __syncthreads();
-    c = lane < warps ? ex.word[turn & 1][lane] : 0u;
-    ++turn;
-    const int c1 = __reduce_add_sync(0xffffffffu, c & 1023u);
-    const int c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
-    const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
-    int here = 0;
-    if (c3 >= picks) {
-      cut = t3;
-      here = c3;
-    } else if (c2 >= picks) {
-      cut = t2;
-      here = c2;
-      above = c3;
-    } else if (c1 >= picks) {
-      cut = t1;
-      here = c1;
-      above = c2;
-    } else {
-      above = c1;
+      for (int k = 0; k < ITEMS; ++k)
+        if (key[k] && (static_cast<uint64_t>(key[k] ^ s.cut) >> (s.shift + 2)) == 0)
+          ex.list[atomicAdd(&ex.few, 1)] = key[k];   // their order does not count
+      __syncthreads();
+      const int left = s.from - s.above, gone = s.above;
+      const uint32_t mine[1] = {static_cast<int>(threadIdx.x) < left ? ex.list[threadIdx.x] : 0u};
+      s.from = left;
+      s.above = 0;
+      exact = narrow<1>(mine, picks - gone, 0, s, ex, turn);
+      s.above += gone;
     }
-    if (here == picks) {       // exactly the keys from cut on
-      --cut;
-      ties = 0;
-      return;
-    }
+  } else {
+    exact = narrow<ITEMS>(key, picks, 0, s, ex, turn);
   }
-  ties = picks - above;
+  cut = exact ? s.cut - 1 : s.cut;
+  ties = exact ? 0 : picks - s.above;
 }
 
 // ---------------------------------------------------------------- eviction
@@ -382,7 +425,8 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     place[k] = rank_bits(w[k]);
     key[k] = full && b >= f_lo && b < l_lo ? place[k] : 0u;
   }
-  if (full) threshold<ITEMS>(key, kept - (n - max(0, l_lo - f_lo)), ex, turn, cut, ties);
+  const int open = max(0, l_lo - f_lo);
+  if (full) threshold<ITEMS>(key, open, kept - (n - open), ex, turn, cut, ties);
   // Which blocks stay, and the columns they move to.
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {

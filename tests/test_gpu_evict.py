@@ -141,6 +141,26 @@ def test_without_new_weights_and_with_nan(mm):
     assert r.attention_block_table is None
 
 
+@pytest.mark.parametrize("n,budget", [(3000, 1500), (3000, 2990), (8000, 5), (1500, 700), (700, 350)])
+@pytest.mark.parametrize("kind", ["equal", "two", "signs", "narrow", "steps"])
+def test_thresholds_of_all_kinds(mm, n, budget, kind):
+    """Weights that are all equal, of two values, of both signs, a few units apart or on a coarse
+    grid: the search ends at every depth, with and without ties."""
+    g = torch.Generator().manual_seed(n + budget)
+    x = {"equal": torch.full((1, n), 0.37),
+         "two": torch.randint(0, 2, (1, n), generator=g).float() * 3 + 1,
+         "signs": torch.randn((1, n), generator=g) * 1e10 ** torch.rand((1, n), generator=g),
+         "narrow": 1.0 + torch.randint(0, 900, (1, n), generator=g).float() * 2.0 ** -23,
+         "steps": torch.exp2(torch.randint(-60, 60, (1, n), generator=g).float())}[kind]
+    lens = [n * 128]
+    new, kept, _ = R.evict_ref(x, lens, [], budget=budget, init=1, local=2, max_seq_len=n * 128)
+    table = torch.arange(n, dtype=torch.int32)[None].cuda()
+    r = mm.evict_blocks(x.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table,
+                        budget=budget, init_blocks=1, local_blocks=2, max_seq_len=n * 128)
+    assert r.ids[0].tolist() == kept[0]
+    assert torch.equal(r.weights[0, :budget].cpu(), x[0, kept[0]])
+
+
 def test_ids_given_twice_and_outside(mm):
     acc = torch.ones((1, 4)).cuda()
     lens = torch.tensor([400], dtype=torch.int32).cuda()
