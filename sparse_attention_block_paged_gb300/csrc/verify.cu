@@ -215,7 +215,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, int cluster) {
   using E = Elem<TYPE>;
   __shared__ uint64_t chunks[kMaxChunks];
-  __shared__ uint64_t totals[2];
+  __shared__ uint64_t totals[2], groups[kGroups];
   __shared__ int s_count;
   const int rank = cluster_rank(), i = blockIdx.x / cluster;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
       if (lane <= a.drafts && lane != count) out[lane] = lane < count ? __ldg(tokens + lane) : -1;
       if (lane == 0 && total == 0) out[count] = a.vocab - 1;
     }
-    if (warp == 0 && x >= before && x < before + mine) {
+    if (x >= before && x < before + mine) {    // one CTA of the cluster, all of it
       // The first chunk whose sum, with all before it, is above the point.
       int c = 0;
       uint64_t below = before;
@@ -311,38 +311,45 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const DraftArgs a, 
           break;
         }
       }
-      for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1); ++s) {
-        uint4 vp[kGroups], vq[kGroups];
-        if (r.q) r.template load<true>(s * E::kStep, vp, vq);
-        else r.template load<false>(s * E::kStep, vp, vq);
-        int found = -1;
+      // Warp k takes group k of each of its steps.
+      bool found = false;
+      for (int s = s0 + c * per; s < min(s0 + (c + 1) * per, s1) && !found; ++s) {
+        const int x0 = s * E::kStep + threadIdx.x * E::kPer;
+        uint64_t own = 0, upto = 0;
+        uint4 vp = {}, vq = {};
+        auto weight = [&](int e) {
+          if (x0 + e == drop) return static_cast<uint64_t>(0);
+          const float fp = elem_of<TYPE>(vp, e);
+          return r.q ? weight_of<true>(fp, elem_of<TYPE>(vq, e)) : weight_of<false>(fp, 0.0f);
+        };
+        if (warp < kGroups) {
+          vp = r.gather(p, x0);
+          if (r.q) vq = r.gather(r.q, x0);
+#pragma unroll
+          for (int e = 0; e < E::kPer; ++e) own += weight(e);
+          upto = warp_scan(own);
+          if (lane == 31) groups[warp] = upto;
+        }
+        __syncthreads();
+        uint64_t at = below;
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
-          const int x0 = s * E::kStep + (k * 32 + lane) * E::kPer;
-          uint64_t w[E::kPer], own = 0;
-#pragma unroll
-          for (int e = 0; e < E::kPer; ++e) {
-            const float fp = elem_of<TYPE>(vp[k], e);
-            w[e] = r.q ? weight_of<true>(fp, elem_of<TYPE>(vq[k], e)) : weight_of<false>(fp, 0.0f);
-            if (x0 + e == drop) w[e] = 0;
-            own += w[e];
-          }
-          const uint64_t incl = warp_scan(own);
-          uint64_t at = below + incl - own;
-          const unsigned hit = __ballot_sync(0xffffffffu, found < 0 && below + incl > x);
-          if (hit && lane == __ffs(hit) - 1) {
-            int e = 0;
-#pragma unroll
-            for (int y = 0; y < E::kPer; ++y) {
-              at += w[y];
-              if (at <= x) e = y + 1;
-            }
-            out[count] = x0 + e - r.skew;
-          }
-          if (hit) found = 0;
-          below += __shfl_sync(0xffffffffu, incl, 31);
+          if (k < warp) at += groups[k];
+          below += groups[k];
         }
-        if (found >= 0) break;
+        found = below > x;
+        const unsigned hit = __ballot_sync(0xffffffffu, at + upto > x);
+        if (warp < kGroups && at <= x && hit && lane == __ffs(hit) - 1) {
+          at += upto - own;
+          int e = 0;
+#pragma unroll
+          for (int y = 0; y < E::kPer; ++y) {
+            at += weight(y);
+            if (at <= x) e = y + 1;
+          }
+          out[count] = x0 + e - r.skew;
+        }
+        __syncthreads();
       }
     }
     break;
