@@ -26,26 +26,40 @@
 //     pieces (16 e4m3 requests of 32K-128K tokens, 4 heads of 128 bytes a
 //     token: 326 us with each head's share elsewhere in time).
 //   * Pages go through a ring of slots in shared memory (192 KB for 16-bit
-//     D = 128: six slots of 128 tokens, keys and values in turn), filled by
-//     one producer warp with 4-D tiled TMA copies, so strides and page sizes
-//     cost nothing and about three tiles are in flight.
+//     D = 128: six slots of 128 tokens, keys and values in turn), filled with
+//     4-D tiled TMA copies, so strides and page sizes cost nothing and about
+//     three tiles are in flight.  Keys and values have a producer warp each:
+//     a copy takes one about 50 ns to issue, and pages of 16 tokens are 16 of
+//     them a tile (one request of 128K tokens, head_dim 64: 70 us with one
+//     producer, 48 with two).
 //   * Eight warps consume it.  The query rows of one kv head (group x
-//     query_len) are rows of 16-row matrix products (mma.sync m16n8k16: with
-//     this few rows the kernel needs a tenth of even that rate, and a warp
-//     that owns its scores needs no exchange with others inside the loop).
-//     A warp owns one of RT 16-row tiles and one part of the tokens: of every
-//     tile, or with few rows of every second one, so that it has at least two
-//     16-token slices to overlap.
-//   * The reference m moves only when a score passes it by 8 (a factor of 256
-//     in the weights, which fp32 sums and 16-bit weights hold without loss),
-//     so the accumulators are rarely rescaled.
+//     query_len) are rows of 16-row matrix products (mma.sync m16n8k16: up to
+//     32 rows need less than that rate's half, and a warp that owns its scores
+//     needs no exchange with others inside the loop).  A warp owns one of RT
+//     16-row tiles and one part of the tokens: of every tile, or with few rows
+//     of every second or fourth one, so that it has two or four 16-token
+//     slices whose products interleave (one slice a warp: 1058 ns a tile from
+//     L2 against 787).  Registers go from the other warps to these
+//     (setmaxnreg).
+//   * The reference m moves only when a score passes the largest so far by 8
+//     (fp16 weights: 4), a factor that fp32 sums and 16-bit weights hold
+//     without loss, so the accumulators are rarely rescaled.
 //   * Weights for the second product are held as the sum of two 16-bit numbers
 //     (one would cost an error as large as the output's own rounding; the
-//     second product's extra MMAs hide behind the copies).  Over e4m3 values
-//     one fp16 number is enough: its step is 1/8 of the output's in bf16.
+//     extra products hide behind the copies up to 32 rows).  Over e4m3 values
+//     and for bf16 output one fp16 number is enough: its step is 1/8 of the
+//     output's.
 //   * e4m3 pages are widened to fp16 (exact) in registers.  The query is then
 //     fp16 as well, scaled by a power of two so that its largest element is
 //     in [1, 2): what this loses is below 2^-25 of that element.
+//
+// What it measured (GB300, tables and caches dealt at random; K and V bytes
+// over the measured copy rate in brackets): 64 requests x 4 rows over 4K-32K
+// tokens, 8 heads a kv head, bf16: 194 us (92 %); 16 x 32K-128K e4m3: 237 us
+// (84 %); one request of 128K tokens, head_dim 64, pages of 16: 50 us (80 %);
+// 8 x 128K: 315 us (100 %).  From L2 (no HBM) a 64 KB tile takes 0.79 us with
+// up to 16 rows, 1.39 with 32 and 2.3 with 64, against 1.47 us at the HBM rate:
+// 64 rows are bound by the products.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -71,7 +85,6 @@ constexpr int kTile = kBlock;                    // tokens of a tile
 constexpr int kRedStride = 40;                   // floats of a 32-column row in the join buffer
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.0f;
 
 // Positions that a (request, kv head) takes in the list beyond its tiles (its
 // start and its join cost time, too), and the fewest positions worth a CTA.
@@ -490,6 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int S = C::kSlots, NB = C::kBars;       // data slots; barriers (a multiple of them)
   constexpr bool kByte = C::kByte;
   constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
+  // The reference lies kHead (base 2) below the largest score at its last move
+  // and moves again when a score is kRaise above that one: fp16 weights then
+  // reach 2^15 and those down to 2^-36 of the largest still count.
+  constexpr float kHead = kBf ? 0.0f : 11.0f, kRaise = kBf ? 8.0f : 4.0f;
   constexpr int TJ = kConsumers / RT;               // warps that share a row tile
   // A warp takes every ALT-th tile, so that it has 32 tokens of a tile with
   // 16-bit D = 128 and 64 where a tile is half the bytes (or RT = 4).
@@ -615,40 +632,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == kWeigher) {
-    // ------------------------------------- log-sum-exp of each tile's rows
-    if (weigh) {
-      uint32_t slot = 1, bar = 1, phase = 0, turn = 0;
-      bool ok = true;
-      while (ok && walk.next(a, sg)) {
-        for (int b = sg.b0; b < sg.b1 && ok; ++b, turn = (turn + 1) % ALT) {
-          ok = warp_wait(&done[bar], phase, abort_flag);
-          if (!ok) break;
-          const float* from = slice + ((slot >> 1) * kConsumers + turn * TG * RT) * 16;
-          float* to = a.tile_lse + (static_cast<int64_t>(sg.unit) * a.w_width + b) * (RT * 16);
-          for (int r = lane; r < RT * 16; r += 32) {
-            float x[TG], top = -INFINITY, sum = 0.0f;
+      // ------------------------------------- log-sum-exp of each tile's rows
+      if (weigh) {
+        uint32_t slot = 1, bar = 1, phase = 0, turn = 0;
+        bool ok = true;
+        while (ok && walk.next(a, sg)) {
+          for (int b = sg.b0; b < sg.b1 && ok; ++b, turn = (turn + 1) % ALT) {
+            ok = warp_wait(&done[bar], phase, abort_flag);
+            if (!ok) break;
+            const float* from = slice + ((slot >> 1) * kConsumers + turn * TG * RT) * 16;
+            float* to = a.tile_lse + (static_cast<int64_t>(sg.unit) * a.w_width + b) * (RT * 16);
+            for (int r = lane; r < RT * 16; r += 32) {
+              float x[TG], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int t = 0; t < TG; ++t) {
-              x[t] = from[(t * RT + (r >> 4)) * 16 + (r & 15)];
-              top = fmaxf(top, x[t]);
+              for (int t = 0; t < TG; ++t) {
+                x[t] = from[(t * RT + (r >> 4)) * 16 + (r & 15)];
+                top = fmaxf(top, x[t]);
+              }
+              const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+              for (int t = 0; t < TG; ++t) sum += ex2(x[t] - ref);
+              to[r] = ref + lg2(sum);
             }
-            const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int t = 0; t < TG; ++t) sum += ex2(x[t] - ref);
-            to[r] = ref + lg2(sum);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[bar]);
-          slot += 2;
-          if (slot > S) slot = 1;
-          bar += 2;
-          if (bar > NB) {
-            bar = 1;
-            phase ^= 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[bar]);
+            slot += 2;
+            if (slot > S) slot = 1;
+            bar += 2;
+            if (bar > NB) {
+              bar = 1;
+              phase ^= 1;
+            }
           }
         }
       }
-    }
     } else if (warp == kSpare) {
       // ------------------------------------------- rows of empty requests
       const int heads = a.kv_heads * a.group;
@@ -891,13 +908,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         top_a *= sc_a;
         top_b *= sc_b;
-        if (__any_sync(0xffffffffu, top_a > st.m0 + kRaise || top_b > st.m1 + kRaise)) {
+        if (__any_sync(0xffffffffu, top_a > st.m0 + kHead + kRaise || top_b > st.m1 + kHead + kRaise)) {
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
             top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, o));
             top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, o));
           }
-          const float na = fmaxf(st.m0, top_a), nb = fmaxf(st.m1, top_b);
+          const float na = fmaxf(st.m0, top_a - kHead), nb = fmaxf(st.m1, top_b - kHead);
           const float fa = na == -INFINITY ? 0.0f : ex2(st.m0 - na);
           const float fb = nb == -INFINITY ? 0.0f : ex2(st.m1 - nb);
           st.m0 = na;

@@ -69,7 +69,9 @@ def attention_ref(s, k_scale=1.0, v_scale=1.0, drop=()):
     tokens do not count.  The bounds count the roundings: half a step of the output; the weights'
     (WEIGHT); scores as fp32 sums of d exact products in any order, each off by at most 2^-23 of the
     sum of their magnitudes (e4m3 keys: the query scaled into fp16 first, off by 2^-24 of its
-    largest); sums over n tokens of which no more than n / 16 are added one after another."""
+    largest); sums over n tokens of which no more than n / 16 are added one after another; fp16
+    weights (fp16 and e4m3 caches) of which the largest is at least 2^11 (2^15 at most): each is off
+    by half of the smallest step, 2^-25, so by 2^-36 of the sum."""
     q, k, v, table, lens, ql = (s[x] for x in ("q", "k", "v", "table", "lens", "ql"))
     rows, qh, d = q.shape
     page, kvh = k.shape[1], k.shape[2]
@@ -82,6 +84,7 @@ def attention_ref(s, k_scale=1.0, v_scale=1.0, drop=()):
     ltol = torch.zeros_like(lse)
     mass = torch.zeros((rows, width), dtype=F64, device=dev)
     scale = s["sm_scale"] * k_scale
+    tiny = 0.0 if v.dtype == torch.bfloat16 else 2.0 ** -36
     raw = torch.uint8 if k.dtype.itemsize == 1 else torch.int16
     for i, n in enumerate(lens.tolist()):
         n = min(max(n, 0), s["max_seq_len"])
@@ -119,7 +122,7 @@ def attention_ref(s, k_scale=1.0, v_scale=1.0, drop=()):
                 size = p @ vh.abs() * abs(v_scale)
                 tol[r, hs] = (HALF[q.dtype] * out[r, hs].abs()
                               + (2 * WEIGHT[v.dtype] + 2 * dev_s[:, None] + 2 * sums) * size
-                              + 2.0 ** -24)
+                              + tiny * m * vh.abs().max() * abs(v_scale) + 2.0 ** -24)
                 ltol[r, hs] = dev_s + sums + 2.0 ** -22 * (lse[r, hs].abs() + 16)
                 mass[r].index_add_(0, see // BLOCK, p.sum(0))
     return out, lse, mass, tol, ltol

@@ -130,6 +130,28 @@ def test_extreme_scores(mm):
         check(call(mm, t), R.attention_ref(t))
 
 
+@pytest.mark.parametrize("kv", [BF16, FP16, E4M3])
+@pytest.mark.parametrize("where", [0, 1, -1])
+def test_many_small_weights_next_to_a_large_one(mm, kv, where):
+    """One token takes nearly all the weight and has values of 0: what is left is the sum of 4000
+    weights of 2^-22 to 2^-26 each, the large one seen first, among them or last.  304 requests of
+    the same tokens, so that a warp sees many of them after the large one."""
+    n, reqs = 4000, 304
+    s = R.make_attention([n], group=4, kvh=1, page=64, seed=12, dtype=FP16 if kv is FP16 else BF16,
+                         kv=kv)
+    k, v = torch.zeros(s["k"].shape, device="cuda"), torch.ones(s["v"].shape, device="cuda")
+    t = {0: 0, 1: n // 3, -1: n - 1}[where]
+    at = int(s["table"][0, t // 64])
+    k[at, t % 64, :, 0] = 64.0
+    v[at, t % 64] = 0.0
+    q = torch.zeros(s["q"].shape, device="cuda")
+    q[0, :, 0] = torch.tensor([15.25, 16.0, 17.0, 18.0]) * 128 ** 0.5 / 64.0
+    s = {**s, "q": q.to(s["q"].dtype), "k": k.to(kv), "v": v.to(kv)}
+    ref = R.attention_ref(s)
+    many = {**s, **{x: s[x].repeat(reqs, *[1] * (s[x].dim() - 1)) for x in ("q", "table", "lens")}}
+    check(call(mm, many), [x.repeat(reqs, *[1] * (x.dim() - 1)) for x in ref])
+
+
 @pytest.mark.parametrize("page", [16, 128])
 @pytest.mark.parametrize("bad", [-1, 10 ** 6])
 def test_pages_outside_the_cache_hold_nothing(mm, page, bad):
