@@ -243,6 +243,12 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   const int64_t most = static_cast<int64_t>(p->num_reqs) * a.tasks * (cdiv(p->max_seq_len, kBlock) + 2);
   const int gangs = static_cast<int>(most < sms / a.gang ? most : sms / a.gang);
   const int grid = gangs * a.gang;
+  const int32_t deal = (a.num_reqs + gangs - 1) / gangs;
+  a.deal = Divisor(deal);
+  a.deal_full = a.num_reqs / deal;
+  a.deal_rest = a.num_reqs % deal;
+  a.by_tasks = Divisor(a.tasks);
+  a.by_row_tiles = Divisor(a.row_tiles);
   return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
 }
 

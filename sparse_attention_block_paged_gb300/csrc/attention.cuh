@@ -24,7 +24,12 @@
 //     the same pages at the same time, each for its own kv head: a page whose
 //     tokens hold all heads next to each other is then read from HBM in long
 //     pieces (16 e4m3 requests of 32K-128K tokens, 4 heads of 128 bytes a
-//     token: 326 us with each head's share elsewhere in time).
+//     token: 326 us with each head's share elsewhere in time).  Where a gang
+//     gets several requests, the list holds them dealt out in turns, so that
+//     neighbours (rows of one request over their sparse tables, requests with a
+//     common beginning) are read at about the same time and their common pages
+//     once (64 requests x 4 rows, 64 heads, 16 selected blocks a row: 149 us,
+//     165 in their own order; 4 rows that select the same: 129 and 162).
 //   * Pages go through a ring of slots in shared memory (192 KB for 16-bit
 //     D = 128: six slots of 128 tokens, keys and values in turn), filled with
 //     4-D tiled TMA copies, so strides and page sizes cost nothing and about
@@ -56,7 +61,7 @@
 // What it measured (GB300, tables and caches dealt at random; K and V bytes
 // over the measured copy rate in brackets): 64 requests x 4 rows over 4K-32K
 // tokens, 8 heads a kv head, bf16: 194 us (92 %); 16 x 32K-128K e4m3: 237 us
-// (84 %); one request of 128K tokens, head_dim 64, pages of 16: 50 us (80 %);
+// (84 %); one request of 128K tokens, head_dim 64, pages of 16: 48 us (82 %);
 // 8 x 128K: 315 us (100 %).  From L2 (no HBM) a 64 KB tile takes 0.79 us with
 // up to 16 rows, 1.39 with 32 and 2.3 with 64, against 1.47 us at the HBM rate:
 // 64 rows are bound by the products.
@@ -140,6 +145,12 @@ __device__ __forceinline__ int request_len(const AttentionArgs& a, int i) {
   return min(max(__ldg(a.seq_lens + i), 0), a.max_seq_len);
 }
 
+// The request at place k of the list (see the work partition above).
+__device__ __forceinline__ int dealt(const AttentionArgs& a, int k) {
+  const int round = a.deal.quotient(k), turn = k - round * static_cast<int>(a.deal.d);
+  return turn * a.deal_full + min(turn, a.deal_rest) + round;
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 // Positions of one task (request, a gang's kv heads, 64-row tile) in the list.
@@ -179,7 +190,7 @@ __device__ __forceinline__ void bounds(const AttentionArgs& a, long long total, 
 // a barrier.
 __device__ __forceinline__ Share share_of_few(const AttentionArgs& a, bool report) {
   const int lane = threadIdx.x & 31;
-  const int raw = lane < a.num_reqs ? __ldg(a.seq_lens + lane) : 0;
+  const int raw = lane < a.num_reqs ? __ldg(a.seq_lens + dealt(a, lane)) : 0;
   const long long one = task_slots(min(max(raw, 0), a.max_seq_len)), mine = one * a.tasks;
   long long incl = mine;
 #pragma unroll
@@ -214,7 +225,7 @@ __device__ __forceinline__ void share_of_many(const AttentionArgs& a, Misc* m) {
   long long mine = 0;
   int bits = 0;
   for (int i = first; i < end; ++i) {
-    const int raw = __ldg(a.seq_lens + i);
+    const int raw = __ldg(a.seq_lens + dealt(a, i));
     bits |= length_bits(a, raw);
     mine += task_slots(min(max(raw, 0), a.max_seq_len));
   }
@@ -249,7 +260,7 @@ __device__ __forceinline__ void share_of_many(const AttentionArgs& a, Misc* m) {
   if (!has_lo && !has_hi) return;
   long long P = before;
   for (int i = first; i < end; ++i) {
-    const long long one = task_slots(request_len(a, i));
+    const long long one = task_slots(request_len(a, dealt(a, i)));
     const long long all = one * a.tasks;
     if (has_lo && P <= s.lo && s.lo < P + all) {
       const int h = static_cast<int>(quotient(s.lo - P, one));
@@ -294,49 +305,43 @@ struct Segment {
   long long pos;       // the task's first position in the list
 };
 
-// The stretches of the share, the two that other CTAs may share first.
+// The stretches of the share, the two that other CTAs may share first.  (One
+// copy of the code a role: four of them, inlined, took 168.5 us where this
+// takes 164.5 over 256 rows of 16 selected blocks, and spilled registers.)
 struct Walker {
   long long lo, hi, p0, pl, P;
   int t0, tl, t, stage;
   __device__ explicit Walker(const Share& s)
       : lo(s.lo), hi(s.hi), p0(s.p0), pl(s.pl), P(0), t0(s.t0), tl(s.tl), t(0), stage(0) {}
-  __device__ __forceinline__ bool emit(const AttentionArgs& a, int task, long long pos,
-                                       Segment& s) const {
-    s.req = task / a.tasks;
-    const int sub = task - s.req * a.tasks;
-    const int tile = sub % a.row_tiles;
-    s.head = sub / a.row_tiles * a.gang + member_of(a);
-    s.row0 = tile * 64;
-    s.unit = (s.req * a.kv_heads + s.head) * a.row_tiles + tile;
-    s.len = request_len(a, s.req);
-    s.nb = tiles_of(s.len);
-    s.pos = pos;
-    const long long pb = pos + kSegCost;
-    const long long from = pb > lo ? pb : lo, to = pb + s.nb < hi ? pb + s.nb : hi;
-    if (s.nb == 0 || to <= from) return false;
-    s.b0 = static_cast<int>(from - pb);
-    s.b1 = static_cast<int>(to - pb);
-    return true;
-  }
   __device__ bool next(const AttentionArgs& a, Segment& s) {
     if (lo >= hi) return false;
-    if (stage == 0) {
-      stage = 1;
-      if (emit(a, t0, p0, s)) return true;
+    for (;;) {
+      const int step = stage;
+      if (step < 2) stage = step + 1;
+      else if (t >= tl) return false;
+      if (step == 1 && tl == t0) continue;
+      const int task = step == 0 ? t0 : step == 1 ? tl : t;
+      const long long pos = step == 0 ? p0 : step == 1 ? pl : P;
+      const int place = a.by_tasks.quotient(task), sub = task - place * a.tasks;
+      const int head = a.by_row_tiles.quotient(sub), tile = sub - head * a.row_tiles;
+      s.req = dealt(a, place);
+      s.head = head * a.gang + member_of(a);
+      s.row0 = tile * 64;
+      s.unit = (s.req * a.kv_heads + s.head) * a.row_tiles + tile;
+      s.len = request_len(a, s.req);
+      s.nb = tiles_of(s.len);
+      s.pos = pos;
+      if (step != 1) {
+        t = task + 1;
+        P = pos + task_slots(s.len);
+      }
+      const long long pb = pos + kSegCost;
+      const long long from = pb > lo ? pb : lo, to = pb + s.nb < hi ? pb + s.nb : hi;
+      if (s.nb == 0 || to <= from) continue;
+      s.b0 = static_cast<int>(from - pb);
+      s.b1 = static_cast<int>(to - pb);
+      return true;
     }
-    if (stage == 1) {
-      stage = 2;
-      t = t0 + 1;
-      P = p0 + task_slots(request_len(a, t0 / a.tasks));
-      if (tl != t0 && emit(a, tl, pl, s)) return true;
-    }
-    while (t < tl) {
-      const int task = t++;
-      const long long pos = P;
-      P += task_slots(request_len(a, task / a.tasks));
-      if (emit(a, task, pos, s)) return true;
-    }
-    return false;
   }
 };
 

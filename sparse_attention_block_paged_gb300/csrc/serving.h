@@ -21,6 +21,23 @@ using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32
                                      CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TensorMapEncode tensor_map_encoder();
 
+// Division by a number that the host knows: a product and a correction (with
+// divisions in the kernel 4096 requests of up to 400 tokens took 318 us instead
+// of 304, and 16 long ones 242 instead of 237).
+struct Divisor {
+  uint32_t d, m;
+  Divisor() = default;
+  explicit Divisor(int32_t x) : d(static_cast<uint32_t>(x)), m(0xFFFFFFFFu / d) {}
+#ifdef __CUDACC__
+  // n / d for 0 <= n < 2^31.  n m / 2^32 is short of it by less than n / 2^32,
+  // so its whole part by 1 at most.
+  __device__ __forceinline__ int quotient(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n), q = __umulhi(u, m);
+    return static_cast<int>(q + (u - q * d >= d));
+  }
+#endif
+};
+
 struct AttentionArgs {
   const void* q;
   int64_t q_tok, q_head;      // element strides
@@ -38,6 +55,9 @@ struct AttentionArgs {
   int32_t table_width;
   const int32_t* seq_lens;
   int32_t num_reqs, query_len, max_seq_len;
+  Divisor deal;               // places of the list that a gang gets: requests are dealt in so many turns
+  int32_t deal_full, deal_rest;  // num_reqs / deal, num_reqs % deal
+  Divisor by_tasks, by_row_tiles;
   float scale;                // sm_scale * k_scale
   float v_scale;
   void* out;

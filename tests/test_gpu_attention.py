@@ -152,6 +152,17 @@ def test_many_small_weights_next_to_a_large_one(mm, kv, where):
     check(call(mm, many), [x.repeat(reqs, *[1] * (x.dim() - 1)) for x in ref])
 
 
+@pytest.mark.parametrize("reqs,kvh", [(31, 8), (38, 4), (39, 4), (153, 1), (305, 1), (77, 4),
+                                      (1000, 2)])
+def test_more_requests_than_multiprocessors(mm, reqs, kvh):
+    """Requests are dealt out to CTAs in turns; every count of full turns and of the rest."""
+    g = torch.Generator().manual_seed(reqs)
+    lens = torch.randint(0, 300, (reqs,), generator=g).tolist()
+    lens[reqs // 2] = 5000
+    s = R.make_attention(lens, group=2, kvh=kvh, page=16, d=64, seed=reqs)
+    check(call(mm, s), R.attention_ref(s))
+
+
 @pytest.mark.parametrize("page", [16, 128])
 @pytest.mark.parametrize("bad", [-1, 10 ** 6])
 def test_pages_outside_the_cache_hold_nothing(mm, page, bad):
