@@ -52,7 +52,8 @@ cudaError_t launch_attention(const CUtensorMap& kmap, const CUtensorMap& vmap,
   cudaError_t e;
   if (a.kv_type == MM3IDX_TYPE_BF16) e = launch_attention_bf16(kmap, vmap, a, grid, s);
   else if (a.kv_type == MM3IDX_TYPE_FP16) e = launch_attention_fp16(kmap, vmap, a, grid, s);
-  else e = launch_attention_e4m3(kmap, vmap, a, grid, s);
+  else if (a.q_type == MM3IDX_TYPE_BF16) e = launch_attention_bf16_e4m3(kmap, vmap, a, grid, s);
+  else e = launch_attention_fp16_e4m3(kmap, vmap, a, grid, s);
   if (e != cudaSuccess || !a.weights) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_reqs) * a.query_len,

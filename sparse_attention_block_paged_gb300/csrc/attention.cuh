@@ -1,7 +1,7 @@
 // attention.cuh -- attention of a few new tokens a request over the paged
 // key-value cache (include/mm3idx.h, mm3idx_paged_attention), one kernel per
-// element type, head size and row count; the type's instances are compiled in
-// attention_<type>.cu.
+// pair of types, head size and row count; the types' instances are compiled in
+// attention_<types>.cu.
 //
 // Mathematics.  For a query row and the tokens it sees, taken in any order and
 // any grouping, three numbers are enough: the reference m, the sum
@@ -302,26 +302,27 @@ struct Segment {
   int head, row0;      // this CTA's kv head, the first of its 64 rows
   int unit;            // index of (request, kv head, 64-row tile)
   int b0, b1, nb;
-  long long pos;       // the task's first position in the list
+  int pos;             // the task's first position, from the share's start
 };
 
 // The stretches of the share, the two that other CTAs may share first.  (One
 // copy of the code a role: four of them, inlined, took 168.5 us where this
 // takes 164.5 over 256 rows of 16 selected blocks, and spilled registers.)
 struct Walker {
-  long long lo, hi, p0, pl, P;
-  int t0, tl, t, stage;
+  int size, p0, pl, P;         // positions from the share's start (2^31 tiles would take one CTA
+  int t0, tl, t, stage;        // half an hour)
   __device__ explicit Walker(const Share& s)
-      : lo(s.lo), hi(s.hi), p0(s.p0), pl(s.pl), P(0), t0(s.t0), tl(s.tl), t(0), stage(0) {}
+      : size(static_cast<int>(s.hi - s.lo)), p0(static_cast<int>(s.p0 - s.lo)),
+        pl(static_cast<int>(s.pl - s.lo)), P(0), t0(s.t0), tl(s.tl), t(0), stage(0) {}
   __device__ bool next(const AttentionArgs& a, Segment& s) {
-    if (lo >= hi) return false;
+    if (size <= 0) return false;
     for (;;) {
       const int step = stage;
       if (step < 2) stage = step + 1;
       else if (t >= tl) return false;
       if (step == 1 && tl == t0) continue;
       const int task = step == 0 ? t0 : step == 1 ? tl : t;
-      const long long pos = step == 0 ? p0 : step == 1 ? pl : P;
+      const int pos = step == 0 ? p0 : step == 1 ? pl : P;
       const int place = a.by_tasks.quotient(task), sub = task - place * a.tasks;
       const int head = a.by_row_tiles.quotient(sub), tile = sub - head * a.row_tiles;
       s.req = dealt(a, place);
@@ -333,13 +334,12 @@ struct Walker {
       s.pos = pos;
       if (step != 1) {
         t = task + 1;
-        P = pos + task_slots(s.len);
+        P = pos + static_cast<int>(task_slots(s.len));
       }
-      const long long pb = pos + kSegCost;
-      const long long from = pb > lo ? pb : lo, to = pb + s.nb < hi ? pb + s.nb : hi;
+      const int pb = pos + kSegCost, from = max(pb, 0), to = min(pb + s.nb, size);
       if (s.nb == 0 || to <= from) continue;
-      s.b0 = static_cast<int>(from - pb);
-      s.b1 = static_cast<int>(to - pb);
+      s.b0 = from - pb;
+      s.b1 = to - pb;
       return true;
     }
   }
@@ -500,7 +500,8 @@ struct State {
   float m0, m1, l0, l1;
 };
 
-template <int KV, int D, int RT>
+// Q: type of the queries and the output.  KV: of the cache, Q or e4m3.
+template <int Q, int KV, int D, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const AttentionArgs a) {
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int S = C::kSlots, NB = C::kBars;       // data slots; barriers (a multiple of them)
   constexpr bool kByte = C::kByte;
   constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
+  constexpr bool kOutBf = Q == MM3IDX_TYPE_BF16;
   // The reference lies kHead (base 2) below the largest score at its last move
   // and moves again when a score is kRaise above that one: fp16 weights then
   // reach 2^15 and those down to 2^-36 of the largest still count.
@@ -698,7 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     State<KV, D> st;
     uint32_t slot = 0, bar = 0, phase = 0, turn = 0;
     bool dead = false;       // a wait gave up: go through the motions to the end
-    const bool rest = !kByte || a.q_type == MM3IDX_TYPE_FP16;   // weights as pairs
+    // Weights as pairs.  (Known to the compiler: the second numbers' registers and
+    // instructions, unused, cost the e4m3 batch above 236 us instead of 223.)
+    constexpr bool rest = !kByte || Q == MM3IDX_TYPE_FP16;
 
     // Offsets of this lane in a slot for slice 0 of its tokens.  A 16-byte
     // piece p of a row lies at p xor (row mod 8) (swizzled copies); slices and
@@ -774,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // largest element into [1, 2) (not at all where that is 0)
         float top[2] = {0.0f, 0.0f}, down[2];
         auto floats = [&](uint32_t w) {
-          if (a.q_type == MM3IDX_TYPE_BF16)
+          if constexpr (kOutBf)
             return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
           return __half22float2(*reinterpret_cast<const __half2*>(&w));
         };
@@ -1107,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float fa = ma == -INFINITY ? 0.0f : ex2(st.m0 - ma);
       const float fb = mb == -INFINITY ? 0.0f : ex2(st.m1 - mb);
-      const int64_t part = 2 * blockIdx.x + (sg.pos > walk.lo ? 1 : 0);
+      const int64_t part = 2 * blockIdx.x + (sg.pos > 0 ? 1 : 0);
       const int heads = a.kv_heads * a.group;
       if (threadIdx.x < RT * 16) {
         const int r = threadIdx.x;
@@ -1181,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (whole) {
             const float f = fin[r].x;
             *reinterpret_cast<uint32_t*>(out_at[q2] + ch * 32) =
-                a.q_type == MM3IDX_TYPE_BF16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
+                pack2<kOutBf>(x * f, y * f);
           } else {
             __stcg(reinterpret_cast<float2*>(a.part_o + (part * 64 + r) * D + ch * 32 + col),
                    make_float2(x, y));
@@ -1192,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) {
         // Publish; the last CTA of the task joins the partial results.  (The
         // barrier orders the CTA's stores before thread 0's release.)
-        const long long pb = sg.pos + kSegCost;
+        const long long pos = misc->share.lo + sg.pos, pb = pos + kSegCost;
         const int lead = gang_of(pb, misc->share.total, misc->share.grid);
         const int parts = gang_of(pb + sg.nb - 1, misc->share.total, misc->share.grid) - lead + 1;
         if (threadIdx.x == 0)
@@ -1203,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // partial results in order, UB x PB = 16 loads in flight.
           constexpr int kStride = kConsumers * 32;
           const int member = member_of(a);
-          const bool second = sg.pos > quotient(misc->share.total * lead, misc->share.grid);
+          const bool second = pos > quotient(misc->share.total * lead, misc->share.grid);
           const int units = rows * (D / 4);
           auto gather = [&](auto ub, auto pb, int u0, int t_first, int t_step, float* m, float* l,
                             float4* o) {
@@ -1258,11 +1262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row = tok0 + (row0 + r) / a.group;
             const int h = head * a.group + (row0 + r) % a.group;
             const float f = l == 0.0f ? 0.0f : a.v_scale / l;
-            uint2 w;
-            if (a.q_type == MM3IDX_TYPE_BF16)
-              w = make_uint2(pack2<true>(o.x * f, o.y * f), pack2<true>(o.z * f, o.w * f));
-            else
-              w = make_uint2(pack2<false>(o.x * f, o.y * f), pack2<false>(o.z * f, o.w * f));
+            const uint2 w =
+                make_uint2(pack2<kOutBf>(o.x * f, o.y * f), pack2<kOutBf>(o.z * f, o.w * f));
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head +
                                       col) = w;
             if (col == 0) {
@@ -1317,7 +1318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && misc->abort) atomicOr(a.status, MM3IDX_DEV_TIMEOUT);
 }
 
-template <int KV, int D, int RT>
+template <int Q, int KV, int D, int RT>
 cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                       int grid, cudaStream_t s) {
   using C = Cfg<KV, D>;
@@ -1326,10 +1327,10 @@ cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const At
     // The register split waits for what the launch does not have: never
     // launch a build that got fewer.
     cudaFuncAttributes at;
-    const cudaError_t err = cudaFuncGetAttributes(&at, attention_kernel<KV, D, RT>);
+    const cudaError_t err = cudaFuncGetAttributes(&at, attention_kernel<Q, KV, D, RT>);
     if (err != cudaSuccess) return err;
     if (at.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(attention_kernel<KV, D, RT>,
+    return cudaFuncSetAttribute(attention_kernel<Q, KV, D, RT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
@@ -1343,23 +1344,23 @@ cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const At
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel<KV, D, RT>, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, attention_kernel<Q, KV, D, RT>, kmap, vmap, a);
 }
 
-template <int KV, int D>
+template <int Q, int KV, int D>
 cudaError_t launch_d(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                      int grid, cudaStream_t s) {
   const int tiles = attention_row_tiles16(a.group * a.query_len);
-  if (tiles == 1) return launch_rt<KV, D, 1>(kmap, vmap, a, grid, s);
-  if (tiles == 2) return launch_rt<KV, D, 2>(kmap, vmap, a, grid, s);
-  return launch_rt<KV, D, 4>(kmap, vmap, a, grid, s);
+  if (tiles == 1) return launch_rt<Q, KV, D, 1>(kmap, vmap, a, grid, s);
+  if (tiles == 2) return launch_rt<Q, KV, D, 2>(kmap, vmap, a, grid, s);
+  return launch_rt<Q, KV, D, 4>(kmap, vmap, a, grid, s);
 }
 
-template <int KV>
+template <int Q, int KV>
 cudaError_t launch_kv(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                       int grid, cudaStream_t s) {
-  return a.head_dim == 128 ? launch_d<KV, 128>(kmap, vmap, a, grid, s)
-                           : launch_d<KV, 64>(kmap, vmap, a, grid, s);
+  return a.head_dim == 128 ? launch_d<Q, KV, 128>(kmap, vmap, a, grid, s)
+                           : launch_d<Q, KV, 64>(kmap, vmap, a, grid, s);
 }
 
 }  // namespace attn

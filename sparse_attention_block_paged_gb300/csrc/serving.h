@@ -152,8 +152,10 @@ cudaError_t launch_attention_bf16(const CUtensorMap& kmap, const CUtensorMap& vm
                                   const AttentionArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_attention_fp16(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const AttentionArgs& a, int grid, cudaStream_t s);
-cudaError_t launch_attention_e4m3(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                  const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_bf16_e4m3(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                       const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_fp16_e4m3(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                       const AttentionArgs& a, int grid, cudaStream_t s);
 // dst may be a.acc itself.
 cudaError_t launch_accumulate(const WeightArgs& a, float* dst, int64_t dst_stride, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
