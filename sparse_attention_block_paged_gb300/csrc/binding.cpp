@@ -97,6 +97,39 @@ void same_gpu(const at::Tensor& ref, std::initializer_list<const at::Tensor*> ot
 at::Tensor make(const at::Tensor& like, at::ScalarType type, std::initializer_list<int64_t> sizes) {
   return at::empty(at::IntArrayRef(sizes.begin(), sizes.size()), like.options().dtype(type));
 }
+// Several outputs of a call in one allocation, 256 bytes apart: an allocation
+// costs the host 0.6 us, a tensor on a part of one a tenth of that.
+template <int N>
+class Outputs {
+ public:
+  void add(int k, at::ScalarType type, std::initializer_list<int64_t> sizes) {
+    int64_t count = 1;
+    for (const int64_t x : sizes) count *= x;
+    parts_[k] = Part{type, at::DimVector(sizes.begin(), sizes.end()), bytes_};
+    bytes_ += (count * static_cast<int64_t>(c10::elementSize(type)) + 255) & ~int64_t{255};
+  }
+  void allocate(const at::Tensor& like, at::Tensor* out) {
+    const at::Tensor base = at::empty({bytes_}, like.options().dtype(at::kByte));
+    for (int k = 0; k < N; ++k) {
+      const Part& p = parts_[k];
+      if (p.offset < 0) continue;
+      out[k] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                        c10::scalarTypeToTypeMeta(p.type));
+      c10::TensorImpl* t = out[k].unsafeGetTensorImpl();
+      t->set_sizes_contiguous(p.sizes);
+      t->set_storage_offset(p.offset / static_cast<int64_t>(c10::elementSize(p.type)));
+    }
+  }
+
+ private:
+  struct Part {
+    at::ScalarType type = at::kByte;
+    at::DimVector sizes;
+    int64_t offset = -1;
+  };
+  Part parts_[N];
+  int64_t bytes_ = 0;
+};
 void* stream_of(const at::Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
 }
@@ -290,13 +323,15 @@ PyObject* evict_blocks(PyObject* const* args) {
            "out must be an Eviction of these shapes");
     }
   } else {
+    Outputs<7> made;
     for (int k = 0; k < 7; ++k) {
       if (k >= 5 && !second) continue;
       if (in_place && (k == 1 || k == 2 || k == 3 || k == 5))
         out[k] = k == 1 ? lens : k == 2 ? acc : k == 3 ? table : *second;
-      else if (k == 1) out[k] = make(acc, at::kInt, {reqs});
-      else out[k] = make(acc, k == 2 ? at::kFloat : at::kInt, {reqs, columns[k]});
+      else if (k == 1) made.add(k, at::kInt, {reqs});
+      else made.add(k, k == 2 ? at::kFloat : at::kInt, {reqs, columns[k]});
     }
+    made.allocate(acc, out);
   }
   mm3idx_eviction_t e{};
   e.budget = budget;
@@ -352,8 +387,14 @@ PyObject* verify_drafts(PyObject* const* args) {
        "draft_lens must be contiguous int32 [num_reqs]");
   same_gpu(target, {&tokens, &u, draft, lens, out_given, acc_given});
   const c10::cuda::CUDAGuard guard(target.device());
-  at::Tensor out = out_given ? *out_given : make(target, at::kInt, {reqs, rows});
-  at::Tensor accepted = acc_given ? *acc_given : make(target, at::kInt, {reqs});
+  at::Tensor results[2];
+  Outputs<2> made;
+  if (out_given) results[0] = *out_given;
+  else made.add(0, at::kInt, {reqs, rows});
+  if (acc_given) results[1] = *acc_given;
+  else made.add(1, at::kInt, {reqs});
+  if (!out_given || !acc_given) made.allocate(target, results);
+  at::Tensor &out = results[0], &accepted = results[1];
   need(is(out, at::kInt, 2) && shaped(out, {reqs, rows}) && unit_inner(out) &&
            is(accepted, at::kInt, 1) && accepted.size(0) == reqs && accepted.is_contiguous(),
        "out must be int32 [num_reqs, drafts + 1] with unit inner stride, accepted int32 [num_reqs]");
