@@ -249,6 +249,10 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
   a.deal_rest = a.num_reqs % deal;
   a.by_tasks = Divisor(a.tasks);
   a.by_row_tiles = Divisor(a.row_tiles);
+  a.by_group = Divisor(a.group);
+  const int64_t list = static_cast<int64_t>(p->num_reqs) * a.tasks *
+                       (cdiv(p->max_seq_len, kBlock) + kTaskCost);
+  a.few = p->num_reqs <= 32 && list <= UINT32_MAX / gangs;
   return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
 }
 

@@ -91,13 +91,6 @@ constexpr int kRedStride = 40;                   // floats of a 32-column row in
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Positions that a (request, kv head) takes in the list beyond its tiles (its
-// start and its join cost time, too), and the fewest positions worth a CTA.
-// Measured over 2, 4, 6, 10: the spec-decode batch 197.7, 195.6, 194.2, 194.9
-// us; two requests of 300-700 tokens with 2, 4 positions at least: 11.0, 12.0 us.
-constexpr int kSegCost = 6;
-constexpr int kMinShare = 2;
-
 template <int KV, int D>
 struct Cfg {
   static constexpr bool kByte = KV == MM3IDX_TYPE_E4M3;
@@ -145,6 +138,12 @@ __device__ __forceinline__ int request_len(const AttentionArgs& a, int i) {
   return min(max(__ldg(a.seq_lens + i), 0), a.max_seq_len);
 }
 
+// The CTAs of a gang are neighbours: x is the kv head that one works on, of the
+// gang's, y the gang.
+__device__ __forceinline__ int cta() {
+  return static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);
+}
+
 // The request at place k of the list (see the work partition above).
 __device__ __forceinline__ int dealt(const AttentionArgs& a, int k) {
   const int round = a.deal.quotient(k), turn = k - round * static_cast<int>(a.deal.d);
@@ -155,7 +154,7 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 
 // Positions of one task (request, a gang's kv heads, 64-row tile) in the list.
 __device__ __forceinline__ long long task_slots(int len) {
-  return len > 0 ? tiles_of(len) + kSegCost : 0;
+  return len > 0 ? tiles_of(len) + kTaskCost : 0;
 }
 
 // a / b of non-negative numbers, in 32 bits where they allow it (a 64-bit
@@ -178,42 +177,48 @@ __device__ __forceinline__ int length_bits(const AttentionArgs& a, int raw) {
 // most one gang per kMinShare positions takes part.
 __device__ __forceinline__ void bounds(const AttentionArgs& a, long long total, Share& s) {
   const long long most = total / kMinShare;
-  const int gangs = static_cast<int>(gridDim.x) / a.gang;
+  const int gangs = static_cast<int>(gridDim.y);
   s.grid = static_cast<int>(most < 1 ? 1 : most < gangs ? most : gangs);
-  const long long c = blockIdx.x / a.gang;
+  const long long c = blockIdx.y;
   s.total = total;
   s.lo = c < s.grid ? quotient(total * c, s.grid) : 0;
   s.hi = c < s.grid ? quotient(total * (c + 1), s.grid) : 0;
 }
 
-// Up to 32 requests, one a lane: every warp finds the share by itself, without
-// a barrier.
+// Up to 32 requests, one a lane, in a list that times the grid stays below
+// 2^32: every warp finds the share by itself, without a barrier.
 __device__ __forceinline__ Share share_of_few(const AttentionArgs& a, bool report) {
   const int lane = threadIdx.x & 31;
   const int raw = lane < a.num_reqs ? __ldg(a.seq_lens + dealt(a, lane)) : 0;
-  const long long one = task_slots(min(max(raw, 0), a.max_seq_len)), mine = one * a.tasks;
-  long long incl = mine;
+  const uint32_t one = static_cast<uint32_t>(task_slots(min(max(raw, 0), a.max_seq_len)));
+  const uint32_t mine = one * static_cast<uint32_t>(a.tasks);
+  uint32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (report) {
     const int bits = lane < a.num_reqs ? length_bits(a, raw) : 0;
     if (bits) atomicOr(a.status, bits);
   }
+  const uint32_t total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+  const uint32_t grid = max(min(total / kMinShare, gridDim.y), 1u), c = blockIdx.y;
+  const uint32_t lo = c < grid ? total * c / grid : 0, hi = c < grid ? total * (c + 1) / grid : 0;
   Share s;
-  bounds(a, __shfl_sync(0xffffffffu, incl, 31), s);
-  auto find = [&](long long x, int& task, long long& pos) {
-    const long long before = incl - mine;
+  s.lo = lo;
+  s.hi = hi;
+  s.total = total;
+  s.grid = static_cast<int>(grid);
+  auto find = [&](uint32_t x, int& task, long long& pos) {
     const unsigned here = __ballot_sync(0xffffffffu, before <= x && x < incl);
-    const int h = here >> lane & 1u ? static_cast<int>(quotient(x - before, one)) : 0;
+    const uint32_t h = here >> lane & 1u ? (x - before) / one : 0;
     const int src = here ? __ffs(here) - 1 : 0;
-    task = __shfl_sync(0xffffffffu, lane * a.tasks + h, src);
+    task = __shfl_sync(0xffffffffu, lane * a.tasks + static_cast<int>(h), src);
     pos = __shfl_sync(0xffffffffu, before + h * one, src);
   };
-  find(s.lo, s.t0, s.p0);
-  find(s.hi - 1, s.tl, s.pl);
+  find(lo, s.t0, s.p0);
+  find(hi - 1, s.tl, s.pl);
   return s;
 }
 
@@ -229,7 +234,7 @@ __device__ __forceinline__ void share_of_many(const AttentionArgs& a, Misc* m) {
     bits |= length_bits(a, raw);
     mine += task_slots(min(max(raw, 0), a.max_seq_len));
   }
-  if (bits && blockIdx.x == 0) atomicOr(a.status, bits);
+  if (bits && cta() == 0) atomicOr(a.status, bits);
   mine *= a.tasks;
   long long incl = mine;
 #pragma unroll
@@ -280,7 +285,7 @@ __device__ __forceinline__ void share_of_many(const AttentionArgs& a, Misc* m) {
 // (one a lane of one warp in every CTA) while the kernel before this one ends:
 // they are read again, as they then are, after it.
 __device__ __forceinline__ void prefetch_inputs(const AttentionArgs& a) {
-  const int64_t line = (static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31)) * 128;
+  const int64_t line = (static_cast<int64_t>(cta()) * 32 + (threadIdx.x & 31)) * 128;
   auto pull = [&](const void* p, int64_t bytes) {
     if (line < bytes)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + line));
@@ -289,11 +294,6 @@ __device__ __forceinline__ void prefetch_inputs(const AttentionArgs& a) {
   pull(a.table, 4 * ((a.num_reqs - 1) * a.table_stride + a.table_width));
   if (a.q_tok > 0 && a.q_head <= a.q_tok)
     pull(a.q, 2 * ((static_cast<int64_t>(a.num_reqs) * a.query_len - 1) * a.q_tok + a.head_dim));
-}
-
-// Which of its gang's heads a CTA works on: the CTAs of a gang are neighbours
-__device__ __forceinline__ int member_of(const AttentionArgs& a) {
-  return static_cast<int>(blockIdx.x) % a.gang;
 }
 
 // One stretch of a CTA's share: tiles [b0, b1) of a task.
@@ -326,7 +326,7 @@ struct Walker {
       const int place = a.by_tasks.quotient(task), sub = task - place * a.tasks;
       const int head = a.by_row_tiles.quotient(sub), tile = sub - head * a.row_tiles;
       s.req = dealt(a, place);
-      s.head = head * a.gang + member_of(a);
+      s.head = head * a.gang + static_cast<int>(blockIdx.x);
       s.row0 = tile * 64;
       s.unit = (s.req * a.kv_heads + s.head) * a.row_tiles + tile;
       s.len = request_len(a, s.req);
@@ -336,7 +336,7 @@ struct Walker {
         t = task + 1;
         P = pos + static_cast<int>(task_slots(s.len));
       }
-      const int pb = pos + kSegCost, from = max(pb, 0), to = min(pb + s.nb, size);
+      const int pb = pos + kTaskCost, from = max(pb, 0), to = min(pb + s.nb, size);
       if (s.nb == 0 || to <= from) continue;
       s.b0 = from - pb;
       s.b1 = to - pb;
@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Share share;
-  if (a.num_reqs <= 32) {
-    share = share_of_few(a, blockIdx.x == 0 && warp == 0);
+  if (a.few) {
+    share = share_of_few(a, cta() == 0 && warp == 0);
     if (threadIdx.x == 0) misc->share = share;    // for the joins, behind their barriers
   } else {
     if (warp < kConsumers) share_of_many(a, misc);
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kv = warp - kProducer;
       const CUtensorMap* map = kv ? &vmap : &kmap;
       const int per = kTile >> a.page_shift;       // pages of a tile
-      const int batch = 32 / per;                  // tiles whose page ids one register holds
+      const int batch = 32 * (1 << a.page_shift) / kTile;                  // tiles whose page ids one register holds
       const int box = C::kRow << a.page_shift;
       uint32_t slot = kv, bar = kv, items = 0;
       uint32_t wait = kv, wait_phase = 0;          // the barrier of the tile S / 2 before
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kSpare) {
       // ------------------------------------------- rows of empty requests
       const int heads = a.kv_heads * a.group;
-      for (int i = blockIdx.x; i < a.num_reqs; i += gridDim.x) {
+      for (int i = cta(); i < a.num_reqs; i += gridDim.x * gridDim.y) {
         if (request_len(a, i) > 0) continue;
         const int per_row = heads * (D / 8);
         for (int e = lane; e < a.query_len * per_row; e += 32) {
@@ -730,7 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                              static_cast<int64_t>(s.head) * a.group * a.q_head;
       auto row_at = [&](int r) {
         r = min(r, R - 1);
-        return base + r / a.group * a.q_tok + r % a.group * a.q_head;
+        const int j = a.by_group.quotient(r);
+        return base + j * a.q_tok + (r - j * a.group) * a.q_head;
       };
       const uint16_t* qa = row_at(ra);
       const uint16_t* qb = row_at(rb);
@@ -764,10 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t tok0 = static_cast<int64_t>(sg.req) * a.query_len;
       // Row r of the kv head is query token r / group, query head r % group.
       const int ra = row0 + rt * 16 + g, rb = ra + 8;
-      const int ja = min(ra, R - 1) / a.group, jb = min(rb, R - 1) / a.group;
+      const int ja = a.by_group.quotient(min(ra, R - 1)), jb = a.by_group.quotient(min(rb, R - 1));
       const int shift = sg.len - a.query_len + 1;          // query token j sees [0, shift + j)
-      const int j_lo = min(row0 + rt * 16, R - 1) / a.group;
-      const int j_hi = min(row0 + rt * 16 + 15, R - 1) / a.group;
+      const int j_lo = a.by_group.quotient(min(row0 + rt * 16, R - 1));
+      const int j_hi = a.by_group.quotient(min(row0 + rt * 16 + 15, R - 1));
       const int lim_a = shift + ja, lim_b = shift + jb;
       const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
       const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
@@ -1111,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float fa = ma == -INFINITY ? 0.0f : ex2(st.m0 - ma);
       const float fb = mb == -INFINITY ? 0.0f : ex2(st.m1 - mb);
-      const int64_t part = 2 * blockIdx.x + (sg.pos > 0 ? 1 : 0);
+      const int64_t part = 2 * cta() + (sg.pos > 0 ? 1 : 0);
       const int heads = a.kv_heads * a.group;
       if (threadIdx.x < RT * 16) {
         const int r = threadIdx.x;
@@ -1125,8 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (r < rows) {
           if (whole) {
-            const int64_t row = tok0 + (row0 + r) / a.group;
-            const int h = head * a.group + (row0 + r) % a.group;
+            const int j = a.by_group.quotient(row0 + r);
+            const int64_t row = tok0 + j;
+            const int h = head * a.group + row0 + r - j * a.group;
             const float lse2 = sum == 0.0f ? -INFINITY : top + lg2(sum);
             if (a.lse) a.lse[row * a.lse_tok + h] = lse2 * kLn2;
             if (weigh) a.row_lse[row * heads + h] = lse2;
@@ -1141,8 +1143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int q2 = 0; q2 < RT; ++q2) {
         const int r = min(q2 * 16 + static_cast<int>(threadIdx.x >> 4), rows - 1);
-        out_at[q2] = static_cast<uint16_t*>(a.out) + (tok0 + (row0 + r) / a.group) * a.o_tok +
-                     (head * a.group + (row0 + r) % a.group) * a.o_head + (threadIdx.x & 15) * 2;
+        const int j = a.by_group.quotient(row0 + r);
+        out_at[q2] = static_cast<uint16_t*>(a.out) + (tok0 + j) * a.o_tok +
+                     (head * a.group + row0 + r - j * a.group) * a.o_head + (threadIdx.x & 15) * 2;
       }
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -1196,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) {
         // Publish; the last CTA of the task joins the partial results.  (The
         // barrier orders the CTA's stores before thread 0's release.)
-        const long long pos = misc->share.lo + sg.pos, pb = pos + kSegCost;
+        const long long pos = misc->share.lo + sg.pos, pb = pos + kTaskCost;
         const int lead = gang_of(pb, misc->share.total, misc->share.grid);
         const int parts = gang_of(pb + sg.nb - 1, misc->share.total, misc->share.grid) - lead + 1;
         if (threadIdx.x == 0)
@@ -1206,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Four columns of a row are a unit.  A thread takes up to UB units, their
           // partial results in order, UB x PB = 16 loads in flight.
           constexpr int kStride = kConsumers * 32;
-          const int member = member_of(a);
+          const int member = static_cast<int>(blockIdx.x);
           const bool second = pos > quotient(misc->share.total * lead, misc->share.grid);
           const int units = rows * (D / 4);
           auto gather = [&](auto ub, auto pb, int u0, int t_first, int t_step, float* m, float* l,
@@ -1259,8 +1262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           auto finish = [&](int unit, float m, float l, float4 o) {
             const int r = unit / (D / 4), col = unit % (D / 4) * 4;
-            const int64_t row = tok0 + (row0 + r) / a.group;
-            const int h = head * a.group + (row0 + r) % a.group;
+            const int j = a.by_group.quotient(row0 + r);
+            const int64_t row = tok0 + j;
+            const int h = head * a.group + row0 + r - j * a.group;
             const float f = l == 0.0f ? 0.0f : a.v_scale / l;
             const uint2 w =
                 make_uint2(pack2<kOutBf>(o.x * f, o.y * f), pack2<kOutBf>(o.z * f, o.w * f));
@@ -1286,8 +1290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // Few columns: with many parts `turns` threads a unit, every
             // turns-th eight parts each, joined through shared memory in order.
-            const int turns = parts <= 8 || units > kStride / 2 ? 1 : units > kStride / 4 ? 2 : 4;
-            const int each = kStride / turns, unit = threadIdx.x % each, turn = threadIdx.x / each;
+            const int split = parts <= 8 || units > kStride / 2 ? 0 : units > kStride / 4 ? 1 : 2;
+            const int turns = 1 << split, each = kStride >> split;
+            const int unit = threadIdx.x & (each - 1), turn = threadIdx.x * turns / kStride;
             float m, l;
             float4 o;
             gather(Const<1>{}, Const<8>{}, unit, turn * 8, turns * 8, &m, &l, &o);
@@ -1335,7 +1340,7 @@ cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const At
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(a.gang, grid / a.gang);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;

@@ -21,6 +21,13 @@ using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32
                                      CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TensorMapEncode tensor_map_encoder();
 
+// Positions that a (request, kv head) takes in the list beyond its tiles (its
+// start and its join cost time, too), and the fewest positions worth a CTA.
+// Measured over 2, 4, 6, 10: the spec-decode batch 197.7, 195.6, 194.2, 194.9
+// us; two requests of 300-700 tokens with 2, 4 positions at least: 11.0, 12.0 us.
+constexpr int kTaskCost = 6;
+constexpr int kMinShare = 2;
+
 // Division by a number that the host knows: a product and a correction (with
 // divisions in the kernel 4096 requests of up to 400 tokens took 318 us instead
 // of 304, and 16 long ones 242 instead of 237).
@@ -57,7 +64,8 @@ struct AttentionArgs {
   int32_t num_reqs, query_len, max_seq_len;
   Divisor deal;               // places of the list that a gang gets: requests are dealt in so many turns
   int32_t deal_full, deal_rest;  // num_reqs / deal, num_reqs % deal
-  Divisor by_tasks, by_row_tiles;
+  Divisor by_tasks, by_row_tiles, by_group;
+  bool few;                   // at most 32 requests, and a list whose positions times gangs fit 32 bits
   float scale;                // sm_scale * k_scale
   float v_scale;
   void* out;
