@@ -29,7 +29,7 @@
 //     neighbours (rows of one request over their sparse tables, requests with a
 //     common beginning) are read at about the same time and their common pages
 //     once (64 requests x 4 rows, 64 heads, 16 selected blocks a row: 149 us,
-//     165 in their own order; 4 rows that select the same: 129 and 162).
+//     165 in their own order; with 4 rows that select the same 129 and 162).
 //   * Pages go through a ring of slots in shared memory (192 KB for 16-bit
 //     D = 128: six slots of 128 tokens, keys and values in turn), filled with
 //     4-D tiled TMA copies, so strides and page sizes cost nothing and about
@@ -60,11 +60,12 @@
 //
 // What it measured (GB300, tables and caches dealt at random; K and V bytes
 // over the measured copy rate in brackets): 64 requests x 4 rows over 4K-32K
-// tokens, 8 heads a kv head, bf16: 194 us (92 %); 16 x 32K-128K e4m3: 237 us
-// (84 %); one request of 128K tokens, head_dim 64, pages of 16: 48 us (82 %);
-// 8 x 128K: 315 us (100 %).  From L2 (no HBM) a 64 KB tile takes 0.79 us with
-// up to 16 rows, 1.39 with 32 and 2.3 with 64, against 1.47 us at the HBM rate:
-// 64 rows are bound by the products.
+// tokens, 8 heads a kv head, bf16: 191 us (94 %); 16 x 32K-128K e4m3: 214 us
+// (93 %); 64 x 4 rows of 16 selected blocks: 146 us; one request of 128K
+// tokens, head_dim 64, pages of 16: 48 us (82 %; 9 us of it start and join);
+// 8 x 128K: 310 us (100 %).  From L2 (no HBM) a 64 KB tile takes 0.80 us with
+// up to 16 rows, 1.41 with 32 and 2.26 with 64, against 1.47 us at the HBM
+// rate: 64 rows are bound by the products.
 #pragma once
 
 #include <cuda_bf16.h>
