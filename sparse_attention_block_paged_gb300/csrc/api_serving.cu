@@ -43,6 +43,11 @@ int check_attention(const mm3idx_attention_t* a) {
     return MM3IDX_ERR_ATTENTION_SHAPE;
   if (static_cast<int64_t>(a->q_heads) * a->num_reqs * a->query_len >= INT_MAX)
     return MM3IDX_ERR_INVALID_ARGUMENT;
+  // A CTA counts its share of the work list in 32 bits: 2^37 / SMs < 2^30.
+  const int64_t group = a->q_heads / a->kv_heads;
+  if (static_cast<int64_t>(a->num_reqs) * a->kv_heads * cdiv(group * a->query_len, 64) >
+      (int64_t{1} << 37) / (cdiv(a->max_seq_len, kBlock) + kTaskCost))
+    return MM3IDX_ERR_INVALID_ARGUMENT;
   if (a->num_reqs == 0) return MM3IDX_OK;
   if (!a->q || !a->k_cache || !a->v_cache || !a->page_table || !a->seq_lens || !a->out)
     return MM3IDX_ERR_INVALID_ARGUMENT;

@@ -237,6 +237,19 @@ def test_two_calls_at_once(mm):
         assert torch.equal(out, want[k % 2])
 
 
+def test_many_row_tiles_and_a_bound_far_above_the_lengths(mm):
+    """130 64-row tiles a kv head, and a bound of 65533 blocks: a few requests whose work list the
+    32-bit form cannot hold."""
+    lens = [130, 400, 0, 150]
+    s = R.make_attention(lens, ql=130, group=64, kvh=1, d=64, page=128, seed=33)
+    want = R.attention_ref(s)
+    check(call(mm, s), want)
+    most = 65533 * 128
+    table = torch.nn.functional.pad(s["table"], (0, 65533 - s["table"].shape[1]), value=2 ** 30)
+    check(call(mm, {**s, "table": table, "max_seq_len": most}, weights=False), want)
+    assert mm.get_device_error() == 0
+
+
 def test_refusals_with_real_tensors(mm):
     s = R.make_attention([300], group=4, kvh=2, page=64, seed=62)
     ws = mm.new_attention_workspace(8, 2, 128, 1, 1, 300)

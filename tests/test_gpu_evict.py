@@ -180,3 +180,31 @@ def test_lengths_out_of_bounds_are_clamped(mm):
     assert mm.get_device_error() == mm.DEV_SEQ_TOO_LONG | mm.DEV_SEQ_TOO_SHORT
     assert r.ids.tolist() == [[2, 3], [-1, -1]] and r.seq_lens.tolist() == [256, 0]
     assert r.freed.tolist() == [[0, 1], [-1, -1]]
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_outputs_are_ordinary_tensors(mm, mode):
+    """Parts of one allocation: contiguous, apart from each other, alive on their own, of use to
+    every other operation."""
+    with mode():
+        acc = torch.arange(24.0).view(3, 8).cuda()
+        lens = torch.tensor([1024, 300, 900], dtype=torch.int32).cuda()
+        table = torch.arange(24, dtype=torch.int32).view(3, 8).cuda()
+        args = dict(budget=3, init_blocks=1, local_blocks=1, max_seq_len=1024,
+                    attention_block_table=table + 100)
+        r = mm.evict_blocks(acc, lens, table, **args)
+        want = [x.clone() for x in r]
+        spans = sorted((x.data_ptr(), x.data_ptr() + x.nbytes) for x in r)
+        assert all(x.is_contiguous() and x.data_ptr() % 256 == 0 for x in r)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        ids = r.ids
+        del r
+        other = mm.evict_blocks(acc, lens, table, **args)
+        assert torch.equal(ids, want[0]) and ids.data_ptr() != other.ids.data_ptr()
+        other.weights.zero_()
+        other.ids.add_(1)
+        assert torch.equal(other.ids, want[0] + 1)
+        assert all(torch.equal(x, y) for x, y in zip(other[3:], want[3:]))
+        none = mm.evict_blocks(acc[:0], lens[:0], table[:0], budget=3, init_blocks=1,
+                               local_blocks=1, max_seq_len=1024)
+        assert none.ids.shape == (0, 3) and none.freed.shape == (0, 5)

@@ -36,7 +36,7 @@ def attend(ws=FAKE, n=1 << 40, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(num_reqs=-1), -1), (dict(query_len=0), -6), (dict(max_seq_len=0), -6),
     (dict(query_len=4, max_seq_len=3), -6), (dict(num_reqs=1 << 30, query_len=2), -1),
-    (dict(max_seq_len=0xFFFF * 128), -5),
+    (dict(max_seq_len=0xFFFF * 128), -5), (dict(num_reqs=1 << 27, max_seq_len=1 << 20), -1),
     (dict(sm_scale=0.0), -1), (dict(sm_scale=float("nan")), -1), (dict(k_scale=0.0), -1),
     (dict(sm_scale=1e-30, k_scale=1e-10), -1), (dict(sm_scale=1e30, k_scale=1e30), -1),
     (dict(k_scale=float("inf")), -1), (dict(v_scale=float("nan")), -1),
