@@ -473,7 +473,7 @@ typedef struct mm3idx_attention {
  * query_len, max_seq_len and block weights stay within those it was sized for.
  * Outputs must not overlap inputs or each other.  A work list that could pass
  * 2^37 places (num_reqs * kv_heads * cdiv(group * query_len, 64) *
- * (cdiv(max_seq_len, 128) + 6)) is MM3IDX_ERR_INVALID_ARGUMENT.
+ * (cdiv(max_seq_len, 128) + 4)) is MM3IDX_ERR_INVALID_ARGUMENT.
  * Device status: MM3IDX_DEV_BAD_PAGE, _SEQ_TOO_LONG, _SEQ_TOO_SHORT
  * (0 < seq_len < query_len), _TIMEOUT.
  */

@@ -23,9 +23,10 @@ TensorMapEncode tensor_map_encoder();
 
 // Positions that a (request, kv head) takes in the list beyond its tiles (its
 // start and its join cost time, too), and the fewest positions worth a CTA.
-// Measured over 2, 4, 6, 10: the spec-decode batch 197.7, 195.6, 194.2, 194.9
-// us; two requests of 300-700 tokens with 2, 4 positions at least: 11.0, 12.0 us.
-constexpr int kTaskCost = 6;
+// Measured over 3, 4, 5, 6: 64 x 4 rows of 4K-32K tokens 189.0, 189.4, 190.3,
+// 191.5 us; 300 rows of 16 selected blocks 189.6, 189.2, 188.9, 188.2; two
+// requests of 300-700 tokens with 2, 3, 4 positions at least 9.8, 10.2, 10.6.
+constexpr int kTaskCost = 4;
 constexpr int kMinShare = 2;
 
 // Division by a number that the host knows: a product and a correction (with
