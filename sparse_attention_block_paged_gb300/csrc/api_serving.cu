@@ -160,7 +160,8 @@ WeightArgs weight_args(const mm3idx_weights_t* w, int32_t* status) {
   a.num_reqs = w->num_reqs;
   a.query_len = w->query_len;
   a.max_seq_len = w->max_seq_len;
-  a.decay = w->decay;
+  a.decay = static_cast<float>(w->decay);
+  a.decay_low = static_cast<float>(w->decay - static_cast<double>(a.decay));
   a.status = status;
   return a;
 }

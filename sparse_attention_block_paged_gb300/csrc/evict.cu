@@ -33,7 +33,8 @@ namespace {
 constexpr int kEntries = MM3IDX_MAX_WEIGHT_ENTRIES;
 constexpr int kWideThreads = 1024;
 constexpr int kSumThreads = 256;
-constexpr int kFew = 1024;
+constexpr int kFew = 256;      // keys that are compared with each other
+constexpr int kBins = 256;
 constexpr int kMaxItems = 8;
 constexpr int kFastThreads = 1024;
 constexpr int kFastWidth = kMaxItems * kFastThreads;   // blocks: a million tokens
@@ -66,12 +67,6 @@ struct Sum {
   }
 };
 
-struct Decay {
-  float high, low;
-  __device__ __forceinline__ explicit Decay(double d)
-      : high(static_cast<float>(d)), low(static_cast<float>(d - static_cast<double>(high))) {}
-};
-
 // The step's entries (query row, place) of a request, in shared memory.
 struct Entries {
   int32_t id[kEntries];
@@ -79,7 +74,7 @@ struct Entries {
 };
 
 __device__ __forceinline__ int load_entries(const WeightArgs& a, int i, Entries& en) {
-  const int count = a.w ? a.query_len * a.topk : 0, padded = (count + 3) & ~3;
+  const int count = a.w ? a.query_len * a.topk : 0, padded = (count + 31) & ~31;
   const int64_t row0 = static_cast<int64_t>(i) * a.query_len;
   for (int e = threadIdx.x; e < padded; e += blockDim.x) {
     const int64_t row = row0 + e / a.topk;
@@ -94,18 +89,21 @@ __device__ __forceinline__ int load_entries(const WeightArgs& a, int i, Entries&
 // earlier entry has that block (which then is its to sum).
 __device__ __forceinline__ bool sum_block(const Entries& en, int count, int e, Sum& s) {
   const int b = en.id[e];
-  bool first = true;
-  for (int x = 0; x < count; x += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(en.id + x);
-    const int ids[4] = {v.x, v.y, v.z, v.w};
+  for (int x = 0; x < count; x += 32) {
+    uint32_t same = 0;               // the entries of this block among 32, without a branch each
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (ids[k] != b) continue;
-      if (x + k < e) first = false;
-      else s.add(en.w[x + k]);
+    for (int k = 0; k < 8; ++k) {
+      const int4 v = *reinterpret_cast<const int4*>(en.id + x + 4 * k);
+      same |= (v.x == b ? 1u : 0u) << (4 * k) | (v.y == b ? 2u : 0u) << (4 * k) |
+              (v.z == b ? 4u : 0u) << (4 * k) | (v.w == b ? 8u : 0u) << (4 * k);
     }
+    if (x <= e) {
+      const uint32_t before = e - x < 32 ? (1u << (e - x)) - 1u : 0xFFFFFFFFu;
+      if (same & before) return false;
+    }
+    for (; same; same &= same - 1) s.add(en.w[x + __ffs(same) - 1]);
   }
-  return first;
+  return true;
 }
 
 __device__ __forceinline__ int request_len(const WeightArgs& a, int i, bool report) {
@@ -127,11 +125,10 @@ __global__ void __launch_bounds__(kSumThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = blocks_of(request_len(a, i, threadIdx.x == 0 && b0 == 0));
   if (b0 >= n) return;
-  const Decay d(a.decay);
   const float* acc = a.acc + i * a.acc_stride;
   float* out = dst + i * dst_stride;
   const float old = b < n ? acc[b] : 0.0f;
-  Sum s(old, d.high, d.low);
+  Sum s(old, a.decay, a.decay_low);
   if (a.ids && a.w) {
     const int count = load_entries(a, i, en);
     touched[threadIdx.x] = 0;
@@ -139,7 +136,7 @@ __global__ void __launch_bounds__(kSumThreads)
     for (int e = threadIdx.x; e < count; e += kSumThreads) {
       const int at = en.id[e];
       if (at < b0 || at >= min(n, b0 + kSumThreads)) continue;
-      Sum t(acc[at], d.high, d.low);
+      Sum t(acc[at], a.decay, a.decay_low);
       if (!sum_block(en, count, e, t)) continue;
       touched[at - b0] = 1;
       out[at] = t.value();
@@ -155,12 +152,16 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // ------------------------------------------------------------ block-wide sums
 
-// Packed sums over the warps; buffers alternate, so one barrier a call.
+// Sums over the warps (buffers alternate, so one barrier a call) and the
+// search for the threshold.
 struct Exchange {
   uint32_t word[2][32];
   uint32_t top[32], bottom[32];
-  uint32_t list[kFew];         // the keys left in a search
+  int bins[kBins];
+  __align__(16) uint32_t list[kFew + 4];   // the keys left in the search
   int few;
+  uint32_t found;
+  int over, from;
 };
 
 // Exclusive sum of x over the threads before this one, and the total.
@@ -221,112 +222,128 @@ __device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at
   for (int k = 0; k < ITEMS; ++k) at[k] += counts[k * warps + warp];
 }
 
-// Where the search for the threshold stands: it lies in the 2^(shift + 2)
-// places from `cut` on; `from` keys are at or above cut, `above` of them above
-// that interval.
-struct Search {
-  uint32_t cut;
-  int shift, from, above;
-};
-
-// Two bits a round, until the interval is one key, its keys number at most
-// `few`, or a count meets `picks` exactly (returns true: the keys from cut on).
-template <int ITEMS>
-__device__ __forceinline__ bool narrow(const uint32_t (&key)[ITEMS], int picks, int few, Search& s,
-                                       Exchange& ex, int& turn) {
-  static_assert(32 * ITEMS < 1024, "packed counts of a warp");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  while (s.shift >= 0 && s.from - s.above > few) {
-    const uint32_t t1 = s.cut | (1u << s.shift), t2 = s.cut | (2u << s.shift),
-                   t3 = s.cut | (3u << s.shift);
-    uint32_t c = 0;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-      c += (key[k] >= t1 ? 1u : 0u) + (key[k] >= t2 ? 1u << 10 : 0u) + (key[k] >= t3 ? 1u << 20 : 0u);
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) ex.word[turn & 1][warp] = c;
-    __syncthreads();
-    c = lane < warps ? ex.word[turn & 1][lane] : 0u;
-    ++turn;
-    const int c1 = __reduce_add_sync(0xffffffffu, c & 1023u);
-    const int c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
-    const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
-    s.shift -= 2;
-    if (c3 >= picks) {
-      s.cut = t3;
-      s.from = c3;
-    } else if (c2 >= picks) {
-      s.cut = t2;
-      s.from = c2;
-      s.above = c3;
-    } else if (c1 >= picks) {
-      s.cut = t1;
-      s.from = c1;
-      s.above = c2;
-    } else {
-      s.above = c1;
-    }
-    if (s.from == picks) return true;
-  }
-  return false;
-}
-
 // The threshold among this CTA's keys (0: none, which no weight has): `picks`
 // of them stay, those above `cut` and the first `ties` at it.
 template <int ITEMS>
-__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int total, int picks,
-                                          Exchange& ex, int& turn, uint32_t& cut, int& ties) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int picks, Exchange& ex,
+                                          uint32_t& cut, int& ties) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = blockDim.x, warps = T >> 5;
   cut = 0xFFFFFFFFu;
   ties = 0;
   if (picks == 0) return;
-  uint32_t top = 0, bottom = 0xFFFFFFFFu;
-#pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    top = max(top, key[k]);
-    if (key[k]) bottom = min(bottom, key[k]);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  bottom = __reduce_min_sync(0xffffffffu, bottom);
-  if (lane == 0) {
-    ex.top[warp] = top;
-    ex.bottom[warp] = bottom;
-  }
-  if (threadIdx.x == 0) ex.few = 0;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, lane < warps ? ex.top[lane] : 0u);
-  bottom = __reduce_min_sync(0xffffffffu, lane < warps ? ex.bottom[lane] : 0xFFFFFFFFu);
-  cut = top;
-  ties = picks;
-  if (top == bottom) return;
-  Search s;
-  s.shift = (31 - __clz(top ^ bottom)) & ~1;
-  s.cut = s.shift == 30 ? 0u : top & ~((4u << s.shift) - 1u);
-  s.from = total;
-  s.above = 0;
-  bool exact = false;
-  if (ITEMS > 1) {
-    // With few keys left in the interval, one a thread: a round over eight
-    // keys a thread costs 0.8 us with 1024 threads, over one 0.3.
-    exact = narrow<ITEMS>(key, picks, min(static_cast<int>(blockDim.x), kFew), s, ex, turn);
-    if (!exact && s.shift >= 0) {
-#pragma unroll
-      for (int k = 0; k < ITEMS; ++k)
-        if (key[k] && (static_cast<uint64_t>(key[k] ^ s.cut) >> (s.shift + 2)) == 0)
-          ex.list[atomicAdd(&ex.few, 1)] = key[k];   // their order does not count
-      __syncthreads();
-      const int left = s.from - s.above, gone = s.above;
-      const uint32_t mine[1] = {static_cast<int>(threadIdx.x) < left ? ex.list[threadIdx.x] : 0u};
-      s.from = left;
-      s.above = 0;
-      exact = narrow<1>(mine, picks - gone, 0, s, ex, turn);
-      s.above += gone;
-    }
+  int left = T;                          // keys in the list, and how many of them stay
+  if (ITEMS == 1 && T <= kFew) {
+    ex.list[threadIdx.x] = key[0];
   } else {
-    exact = narrow<ITEMS>(key, picks, 0, s, ex, turn);
+    uint32_t top = 0, bottom = 0xFFFFFFFFu;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      top = max(top, key[k]);
+      if (key[k]) bottom = min(bottom, key[k]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bottom = __reduce_min_sync(0xffffffffu, bottom);
+    if (lane == 0) {
+      ex.top[warp] = top;
+      ex.bottom[warp] = bottom;
+    }
+    for (int x = threadIdx.x; x < kBins; x += T) ex.bins[x] = 0;
+    if (threadIdx.x == 0) ex.few = 0;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, lane < warps ? ex.top[lane] : 0u);
+    bottom = __reduce_min_sync(0xffffffffu, lane < warps ? ex.bottom[lane] : 0xFFFFFFFFu);
+    cut = top;
+    ties = picks;
+    if (top == bottom) return;
+    // The threshold lies in [base, base + 2^size): how many keys in each 256th of it?
+    int size = 32 - __clz(top ^ bottom);
+    uint32_t base = size == 32 ? 0u : top >> size << size;
+    for (;;) {
+      const int shift = max(size - 8, 0);
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        const uint32_t d = key[k] - base;
+        const bool in = key[k] >= base && key[k] && (size == 32 || (d >> size) == 0);
+        const uint32_t bin = in ? d >> shift : 0xFFFFFFFFu;
+        // (a warp's keys in one bin are one addition: equal weights are common)
+        const uint32_t one = __shfl_sync(0xffffffffu, bin, 0);
+        if (__all_sync(0xffffffffu, bin == one)) {
+          if (in && lane == 0) atomicAdd(&ex.bins[bin], 32);
+        } else if (in) {
+          atomicAdd(&ex.bins[bin], 1);
+        }
+      }
+      __syncthreads();
+      // Every warp: from the top, eight bins a lane (lane 0 has the highest).
+      int c[8], sum = 0;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        c[x] = ex.bins[kBins - 1 - 8 * lane - x];
+        sum += c[x];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int above = incl - sum, bin = 0, n = 0;
+      bool here = false;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        if (!here) {
+          n = c[x];
+          bin = kBins - 1 - 8 * lane - x;
+          here = above < picks && picks <= above + n;
+          if (!here) above += n;
+        }
+      }
+      const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      picks -= __shfl_sync(0xffffffffu, above, src);
+      left = __shfl_sync(0xffffffffu, n, src);
+      base += static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src)) << shift;
+      size = shift;
+      if (left == picks) {               // all of them stay
+        cut = base - 1;
+        ties = 0;
+        return;
+      }
+      if (size == 0) {                   // they are equal
+        cut = base;
+        ties = picks;
+        return;
+      }
+      if (left <= kFew) break;
+      __syncthreads();                   // (the bins have been read)
+      for (int x = threadIdx.x; x < kBins; x += T) ex.bins[x] = 0;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (key[k] >= base && ((key[k] - base) >> size) == 0)
+        ex.list[atomicAdd(&ex.few, 1)] = key[k];     // their order does not count
+    if (threadIdx.x < 4) ex.list[left + threadIdx.x] = 0;
   }
-  cut = exact ? s.cut - 1 : s.cut;
-  ties = exact ? 0 : picks - s.above;
+  __syncthreads();
+  // Every key of the list against all of them.
+  if (static_cast<int>(threadIdx.x) < left) {
+    const uint32_t mine = ex.list[threadIdx.x];
+    int over = 0, from = 0;
+    for (int x = 0; x < left; x += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(ex.list + x);
+      over += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+      from += (v.x >= mine) + (v.y >= mine) + (v.z >= mine) + (v.w >= mine);
+    }
+    if (mine && over < picks && picks <= from) {     // (equal keys write the same)
+      ex.found = mine;
+      ex.over = over;
+      ex.from = from;
+    }
+  }
+  __syncthreads();
+  const bool all = ex.from == picks;                 // all equal ones stay
+  cut = ex.found - (all ? 1u : 0u);
+  ties = all ? 0 : picks - ex.over;
 }
 
 // ---------------------------------------------------------------- eviction
@@ -377,7 +394,6 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     for (int t = 0; t < 2; ++t)
       entry[t][k] = in && e.t[t].in ? __ldcg(e.t[t].in + i * e.t[t].in_stride + b) : 0;
   }
-  const Decay d(a.decay);
   if (a.w && a.ids) {
     const int count = load_entries(a, i, en);
     for (int k = threadIdx.x; k < (e.width + 31) / 32; k += T) touched[k] = 0;
@@ -388,7 +404,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     for (int x = threadIdx.x; x < count; x += T) {
       const int b = en.id[x];
       if (b < 0 || b >= n) continue;
-      Sum s(staged[b], d.high, d.low);
+      Sum s(staged[b], a.decay, a.decay_low);
       if (!sum_block(en, count, x, s)) continue;
       staged[b] = s.value();       // no other thread has this block
       atomicOr(&touched[b >> 5], 1u << (b & 31));
@@ -399,7 +415,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
       const int b = k * T + threadIdx.x;
       if (b >= e.width) continue;
       const bool fresh = (touched[b >> 5] >> (b & 31)) & 1u;
-      w[k] = fresh ? staged[b] : Sum(w[k], d.high, d.low).value();
+      w[k] = fresh ? staged[b] : Sum(w[k], a.decay, a.decay_low).value();
     }
   } else {
     float x0[ITEMS];                             // the first row's, all in flight at once
@@ -409,7 +425,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
       x0[k] = a.w && k * T + threadIdx.x < e.width ? __ldg(x + k * T) : 0.0f;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-      Sum s(w[k], d.high, d.low);
+      Sum s(w[k], a.decay, a.decay_low);
       if (a.w && k * T + threadIdx.x < e.width) {
         s.add(x0[k]);
         for (int j = 1; j < a.query_len; ++j) s.add(__ldg(x + j * a.w_stride + k * T));
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
   }
   const int kept = min(n, e.budget), f_lo = e.init_blocks, l_lo = n - e.local_blocks;
   uint32_t place[ITEMS], key[ITEMS], cut = 0, stays = 0, tied = 0;
-  int ties = 0, turn = 0;
+  int ties = 0;
   const bool full = n > e.budget;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     key[k] = full && b >= f_lo && b < l_lo ? place[k] : 0u;
   }
   const int open = max(0, l_lo - f_lo);
-  if (full) threshold<ITEMS>(key, open, kept - (n - open), ex, turn, cut, ties);
+  if (full) threshold<ITEMS>(key, kept - (n - open), ex, cut, ties);
   // Which blocks stay, and the columns they move to.
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
@@ -444,20 +460,26 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
   }
   // (its barriers also part the loads of every thread from the stores below)
   block_rank<ITEMS>(stays, counts, at);
+  int32_t* ids = e.ids ? e.ids + i * e.ids_stride : nullptr;
+  float* acc_out = e.acc_out + i * e.acc_out_stride;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    const int b = k * T + threadIdx.x;
-    if (b >= n) continue;
-    const bool stay = (stays >> k) & 1u;
-    if (stay) {
-      if (e.ids) e.ids[i * e.ids_stride + at[k]] = b;
-      e.acc_out[i * e.acc_out_stride + at[k]] = weight_at(place[k]);
+    if ((stays >> k) & 1u) {
+      if (ids) ids[at[k]] = k * T + threadIdx.x;
+      acc_out[at[k]] = weight_at(place[k]);
     }
+  }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (!e.t[t].in) continue;
-      if (stay) e.t[t].out[i * e.t[t].out_stride + at[k]] = entry[t][k];
-      else if (e.t[t].freed) e.t[t].freed[i * e.t[t].freed_stride + b - at[k]] = entry[t][k];
+  for (int t = 0; t < 2; ++t) {
+    if (!e.t[t].in) continue;
+    int32_t* out = e.t[t].out + i * e.t[t].out_stride;
+    int32_t* freed = e.t[t].freed ? e.t[t].freed + i * e.t[t].freed_stride : nullptr;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int b = k * T + threadIdx.x;
+      const bool stay = (stays >> k) & 1u;
+      int32_t* to = stay ? out + at[k] : freed + (b - at[k]);
+      if (b < n && (stay || freed)) *to = entry[t][k];
     }
   }
   finish(e, i, seq, n, kept);

@@ -99,7 +99,7 @@ struct WeightArgs {
   int32_t topk;
   const int32_t* seq_lens;
   int32_t num_reqs, query_len, max_seq_len;
-  double decay;
+  float decay, decay_low;     // the decay as a sum
   int32_t* status;
 };
 
