@@ -160,8 +160,8 @@ struct Exchange {
   int bins[kBins];
   __align__(16) uint32_t list[kFew + 4];   // the keys left in the search
   int few;
-  uint32_t found;
-  int over, from;
+  uint32_t low[kFew / 32];                 // of the list's warps
+  int most[kFew / 32], count[kFew / 32];
 };
 
 // Exclusive sum of x over the threads before this one, and the total.
@@ -222,16 +222,16 @@ __device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at
   for (int k = 0; k < ITEMS; ++k) at[k] += counts[k * warps + warp];
 }
 
-// The threshold among this CTA's keys (0: none, which no weight has): `picks`
+// The threshold among this CTA's n keys (0: none, which no weight has): `picks`
 // of them stay, those above `cut` and the first `ties` at it.
 template <int ITEMS>
-__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int picks, Exchange& ex,
+__device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, int picks, Exchange& ex,
                                           uint32_t& cut, int& ties) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = blockDim.x, warps = T >> 5;
   cut = 0xFFFFFFFFu;
   ties = 0;
   if (picks == 0) return;
-  int left = T;                          // keys in the list, and how many of them stay
+  int left = min(T, (n + 3) & ~3);       // keys in the list, `picks` of which stay
   if (ITEMS == 1 && T <= kFew) {
     ex.list[threadIdx.x] = key[0];
   } else {
@@ -325,25 +325,32 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int pick
     if (threadIdx.x < 4) ex.list[left + threadIdx.x] = 0;
   }
   __syncthreads();
-  // Every key of the list against all of them.
-  if (static_cast<int>(threadIdx.x) < left) {
-    const uint32_t mine = ex.list[threadIdx.x];
-    int over = 0, from = 0;
+  // Every key of the list against all of them.  Those with fewer than `picks`
+  // above them stay, at least in part: the lowest of them is the threshold.
+  const uint32_t mine = static_cast<int>(threadIdx.x) < left ? ex.list[threadIdx.x] : 0u;
+  int over = 0;
+  if (warp * 32 < left) {
     for (int x = 0; x < left; x += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(ex.list + x);
       over += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
-      from += (v.x >= mine) + (v.y >= mine) + (v.z >= mine) + (v.w >= mine);
     }
-    if (mine && over < picks && picks <= from) {     // (equal keys write the same)
-      ex.found = mine;
-      ex.over = over;
-      ex.from = from;
+    const bool in = mine && over < picks;
+    const unsigned all = __ballot_sync(0xffffffffu, in);
+    const uint32_t low = __reduce_min_sync(0xffffffffu, in ? mine : 0xFFFFFFFFu);
+    const int most = __reduce_max_sync(0xffffffffu, in ? over : -1);
+    if (lane == 0) {
+      ex.low[warp] = low;
+      ex.most[warp] = most;
+      ex.count[warp] = __popc(all);
     }
   }
   __syncthreads();
-  const bool all = ex.from == picks;                 // all equal ones stay
-  cut = ex.found - (all ? 1u : 0u);
-  ties = all ? 0 : picks - ex.over;
+  const bool part = lane * 32 < left;              // (a warp's results a lane)
+  const uint32_t found = __reduce_min_sync(0xffffffffu, part ? ex.low[lane] : 0xFFFFFFFFu);
+  const int from = __reduce_add_sync(0xffffffffu, part ? ex.count[lane] : 0);
+  over = __reduce_max_sync(0xffffffffu, part ? ex.most[lane] : -1);
+  cut = from == picks ? found - 1 : found;         // all equal ones stay
+  ties = from == picks ? 0 : picks - over;
 }
 
 // ---------------------------------------------------------------- eviction
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     key[k] = full && b >= f_lo && b < l_lo ? place[k] : 0u;
   }
   const int open = max(0, l_lo - f_lo);
-  if (full) threshold<ITEMS>(key, kept - (n - open), ex, cut, ties);
+  if (full) threshold<ITEMS>(key, n, kept - (n - open), ex, cut, ties);
   // Which blocks stay, and the columns they move to.
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
