@@ -837,7 +837,7 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
     (their columns from ``budget`` on stay as they were).  ``out``: an
     Eviction of the same shapes to write into."""
     with _HERE if stream is None else _run_on(stream, acc):
-        return Eviction._make(_binding.evict_blocks(
+        return tuple.__new__(Eviction, _binding.evict_blocks(
             acc, seq_lens, block_table, attention_block_table, block_weights, ids, budget,
             init_blocks, local_blocks, max_seq_len, query_len, decay, in_place, out))
 

@@ -7,22 +7,26 @@
 // exact to about 2^-46, then rounded once to fp32: the order of the terms does
 // not show.  (fp64 instructions would do the same at a sixtieth of the rate:
 // 128 requests of 8192 blocks took 52 us with them, most of it there.)  The
-// weights are ordered by the unsigned image of their bits (ordered_bits), and
-// the weight of the last block that stays is found from the top, two bits a
-// round: how many blocks are at or above each of three trial values.  Rounds
-// start at the highest bit in which any two weights differ and stop when a
-// count meets the number of places; of blocks at the threshold the lowest ids
-// stay.  Whole numbers throughout: the result depends on the weights alone.
+// weights are ordered by the unsigned image of their bits (ordered_bits).  The
+// weight of the last block that stays is found in two steps: the keys between
+// the lowest and the highest are counted in 256 bins (again within the bin that
+// holds it while more than 256 keys are left), then the keys of that bin are
+// compared with each other: the threshold is the lowest with fewer above it
+// than have to stay.  Of blocks at the threshold the lowest ids stay.  Whole
+// numbers throughout: the result depends on the weights alone.  (Two bits a
+// round over all keys took 18.4 us where this takes 14.0.)
 //
-// What bounds it.  A few bytes a block: latency, of one round of loads and of
-// the rounds of counts.  One CTA takes a request; every load is issued before
-// the first is used, and a thread keeps its blocks' weights and table entries
-// in registers (blocks kThreads apart, so that a warp's accesses are one line:
-// 16 neighbouring blocks a thread took 39 us for 128 x 8192 blocks), so a round
-// is a few compares, one warp reduction and one barrier.  Wider tables than the
-// registers hold (kFastWidth) go through global memory.  It measured 18.4 us
-// for 128 requests of 1K to 8K blocks and 7.2 us for 64 of 32 to 256 blocks with
-// the entries of a step of 4 rows x 16 blocks.
+// What bounds it.  A few bytes a block: latency, of one round of loads, of the
+// counts and of a dozen barriers.  One CTA takes a request; every load is issued
+// before the first is used, and a thread keeps its blocks' weights and table
+// entries in registers (blocks blockDim.x apart, so that a warp's accesses are
+// one line: 16 neighbouring blocks a thread took 39 us for 128 x 8192 blocks).
+// With many blocks a thread the issue of instructions bounds it.  Wider tables
+// than the registers hold (kFastWidth) go through global memory.  It measured
+// 14.0 us for 128 requests of 1K to 8K blocks (sums 3.4, counts 3.8, columns
+// 1.2, stores 2.7) and 4.6 us for 64 of 32 to 256 blocks with the entries of a
+// step of 4 rows x 16 blocks (7.2 with a branch an entry in sum_block and rounds
+// of counts).
 #include "../../include/mm3idx.h"
 #include "ptx.cuh"
 #include "serving.h"
@@ -157,8 +161,9 @@ __global__ void __launch_bounds__(kSumThreads)
 struct Exchange {
   uint32_t word[2][32];
   uint32_t top[32], bottom[32];
-  int bins[kBins];
-  __align__(16) uint32_t list[kFew + 4];   // the keys left in the search
+  __align__(16) int bins[kBins];           // the highest first
+  int bin, above, left;                    // the threshold's
+  __align__(16) uint32_t list[kFew + 32];   // the keys left in the search
   int few;
   uint32_t low[kFew / 32];                 // of the list's warps
   int most[kFew / 32], count[kFew / 32];
@@ -223,16 +228,17 @@ __device__ __forceinline__ void block_rank(uint32_t flags, int* counts, int (&at
 }
 
 // The threshold among this CTA's n keys (0: none, which no weight has): `picks`
-// of them stay, those above `cut` and the first `ties` at it.
-template <int ITEMS>
+// of them stay, those above `cut` and the first `ties` at it.  LIST: at most
+// kFew threads of one key, compared with each other at once.
+template <int ITEMS, bool LIST>
 __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, int picks, Exchange& ex,
                                           uint32_t& cut, int& ties) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = blockDim.x, warps = T >> 5;
   cut = 0xFFFFFFFFu;
   ties = 0;
   if (picks == 0) return;
-  int left = min(T, (n + 3) & ~3);       // keys in the list, `picks` of which stay
-  if (ITEMS == 1 && T <= kFew) {
+  int left = min(T, (n + 31) & ~31);     // keys in the list, `picks` of which stay
+  if constexpr (LIST) {
     ex.list[threadIdx.x] = key[0];
   } else {
     uint32_t top = 0, bottom = 0xFFFFFFFFu;
@@ -268,40 +274,41 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, i
         // (a warp's keys in one bin are one addition: equal weights are common)
         const uint32_t one = __shfl_sync(0xffffffffu, bin, 0);
         if (__all_sync(0xffffffffu, bin == one)) {
-          if (in && lane == 0) atomicAdd(&ex.bins[bin], 32);
+          if (in && lane == 0) atomicAdd(&ex.bins[kBins - 1 - bin], 32);
         } else if (in) {
-          atomicAdd(&ex.bins[bin], 1);
+          atomicAdd(&ex.bins[kBins - 1 - bin], 1);
         }
       }
       __syncthreads();
-      // Every warp: from the top, eight bins a lane (lane 0 has the highest).
-      int c[8], sum = 0;
+      if (warp == 0) {                   // from the top, eight bins a lane
+        const int4 u = *reinterpret_cast<const int4*>(ex.bins + 8 * lane);
+        const int4 v = *reinterpret_cast<const int4*>(ex.bins + 8 * lane + 4);
+        const int c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        const int sum = u.x + u.y + u.z + u.w + v.x + v.y + v.z + v.w;
+        int incl = sum;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        c[x] = ex.bins[kBins - 1 - 8 * lane - x];
-        sum += c[x];
-      }
-      int incl = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        int above = incl - sum;
+        if (above < picks && picks <= incl) {
+          int x = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      int above = incl - sum, bin = 0, n = 0;
-      bool here = false;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        if (!here) {
-          n = c[x];
-          bin = kBins - 1 - 8 * lane - x;
-          here = above < picks && picks <= above + n;
-          if (!here) above += n;
+          for (int k = 0; k < 7; ++k)
+            if (x == k && above + c[k] < picks) {
+              above += c[k];
+              ++x;
+            }
+          ex.bin = kBins - 1 - (8 * lane + x);
+          ex.above = above;
+          ex.left = ex.bins[8 * lane + x];
         }
       }
-      const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-      picks -= __shfl_sync(0xffffffffu, above, src);
-      left = __shfl_sync(0xffffffffu, n, src);
-      base += static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src)) << shift;
+      __syncthreads();
+      picks -= ex.above;
+      left = ex.left;
+      base += static_cast<uint32_t>(ex.bin) << shift;
       size = shift;
       if (left == picks) {               // all of them stay
         cut = base - 1;
@@ -314,7 +321,6 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, i
         return;
       }
       if (left <= kFew) break;
-      __syncthreads();                   // (the bins have been read)
       for (int x = threadIdx.x; x < kBins; x += T) ex.bins[x] = 0;
       __syncthreads();
     }
@@ -322,7 +328,7 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, i
     for (int k = 0; k < ITEMS; ++k)
       if (key[k] >= base && ((key[k] - base) >> size) == 0)
         ex.list[atomicAdd(&ex.few, 1)] = key[k];     // their order does not count
-    if (threadIdx.x < 4) ex.list[left + threadIdx.x] = 0;
+    if (threadIdx.x < 32) ex.list[left + threadIdx.x] = 0;
   }
   __syncthreads();
   // Every key of the list against all of them.  Those with fewer than `picks`
@@ -330,9 +336,13 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, i
   const uint32_t mine = static_cast<int>(threadIdx.x) < left ? ex.list[threadIdx.x] : 0u;
   int over = 0;
   if (warp * 32 < left) {
-    for (int x = 0; x < left; x += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(ex.list + x);
-      over += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+#pragma unroll 1
+    for (int x = 0; x < left; x += 32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(ex.list + x + 4 * k);
+        over += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+      }
     }
     const bool in = mine && over < picks;
     const unsigned all = __ballot_sync(0xffffffffu, in);
@@ -376,7 +386,7 @@ __device__ __forceinline__ void finish(const EvictArgs& e, int i, int seq, int n
 }
 
 // ITEMS blocks a thread, blockDim.x apart.
-template <int ITEMS>
+template <int ITEMS, bool LIST>
 __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) {
   __shared__ Exchange ex;
   __shared__ __align__(16) Entries en;
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kFastThreads) evict_kernel(const EvictArgs e) 
     key[k] = full && b >= f_lo && b < l_lo ? place[k] : 0u;
   }
   const int open = max(0, l_lo - f_lo);
-  if (full) threshold<ITEMS>(key, n, kept - (n - open), ex, cut, ties);
+  if (full) threshold<ITEMS, LIST>(key, n, kept - (n - open), ex, cut, ties);
   // Which blocks stay, and the columns they move to.
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
@@ -570,10 +580,10 @@ cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int ITEMS>
+template <int ITEMS, bool LIST = false>
 cudaError_t launch_items(const EvictArgs& a, cudaStream_t s) {
   const int threads = ((a.width + ITEMS - 1) / ITEMS + 31) / 32 * 32;
-  return launch(evict_kernel<ITEMS>, dim3(a.w.num_reqs), threads,
+  return launch(evict_kernel<ITEMS, LIST>, dim3(a.w.num_reqs), threads,
                 a.w.w && a.w.ids ? static_cast<size_t>(a.width) * 4 : 0, s, a);
 }
 
@@ -586,6 +596,7 @@ cudaError_t launch_accumulate(const WeightArgs& a, float* dst, int64_t dst_strid
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   // As many threads as it takes, up to kFastThreads, then more blocks a thread.
+  if (a.width <= kFew) return launch_items<1, true>(a, s);
   if (a.width <= kFastThreads) return launch_items<1>(a, s);
   if (a.width <= 2 * kFastThreads) return launch_items<2>(a, s);
   if (a.width <= 4 * kFastThreads) return launch_items<4>(a, s);
