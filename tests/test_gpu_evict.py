@@ -161,6 +161,35 @@ def test_thresholds_of_all_kinds(mm, n, budget, kind):
     assert torch.equal(r.weights[0, :budget].cpu(), x[0, kept[0]])
 
 
+@pytest.mark.parametrize("width", [5, 33, 256, 257, 1024, 1025, 2048, 8192])
+def test_thresholds_of_many_batches(mm, width):
+    """24 requests of random lengths, budgets and weights: a cluster a few units wide between far
+    outliers (the count goes over several levels), infinities, weights of 0 and below, ties."""
+    g = torch.Generator().manual_seed(width)
+    for budget in sorted({2, width // 3 + 2, width - 1}):
+        lens = torch.randint(1, width * 128 + 1, (24,), generator=g)
+        lens[0] = width * 128
+        x = torch.rand((24, width), generator=g)
+        x[::4] = 1.0 + torch.randint(0, 300, (6, width), generator=g).float() * 2.0 ** -23
+        x[1::4] = torch.randint(0, 4, (6, width), generator=g).float()
+        x[2::4] = torch.exp(3 * torch.randn((6, width), generator=g))
+        far = torch.rand((24, width), generator=g)
+        x = torch.where(far < 0.02, 1e30, torch.where(far > 0.98, -1e-30, x))
+        x = torch.where((far > 0.5) & (far < 0.51), float("inf"), x)
+        n = lens.tolist()
+        _, kept, _ = R.evict_ref(x, n, [], budget=budget, init=1, local=1, max_seq_len=width * 128)
+        table = torch.arange(width, dtype=torch.int32).repeat(24, 1).cuda()
+        r = mm.evict_blocks(x.cuda(), lens.int().cuda(), table, budget=budget, init_blocks=1,
+                            local_blocks=1, max_seq_len=width * 128)
+        for i in range(24):
+            ids = r.ids[i].tolist()
+            m = len(kept[i])
+            assert ids == kept[i] + [-1] * (budget - m), (budget, i)
+            assert torch.equal(r.weights[i, :m].cpu(), x[i, kept[i]])
+            gone = sorted(set(range((n[i] + 127) // 128)) - set(kept[i]))
+            assert r.freed[i, :len(gone)].tolist() == gone
+
+
 def test_ids_given_twice_and_outside(mm):
     acc = torch.ones((1, 4)).cuda()
     lens = torch.tensor([400], dtype=torch.int32).cuda()
