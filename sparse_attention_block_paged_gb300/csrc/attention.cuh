@@ -60,8 +60,8 @@
 //
 // What it measured (GB300, tables and caches dealt at random; K and V bytes
 // over the measured copy rate in brackets): 64 requests x 4 rows over 4K-32K
-// tokens, 8 heads a kv head, bf16: 191 us (94 %); 16 x 32K-128K e4m3: 214 us
-// (93 %); 64 x 4 rows of 16 selected blocks: 146 us; one request of 128K
+// tokens, 8 heads a kv head, bf16: 189 us (94 %); 16 x 32K-128K e4m3: 214 us
+// (93 %); 64 x 4 rows of 16 selected blocks: 145 us; one request of 128K
 // tokens, head_dim 64, pages of 16: 48 us (82 %; 9 us of it start and join);
 // 8 x 128K: 310 us (100 %).  From L2 (no HBM) a 64 KB tile takes 0.80 us with
 // up to 16 rows, 1.41 with 32 and 2.26 with 64, against 1.47 us at the HBM
