@@ -198,6 +198,13 @@ def test_ids_given_twice_and_outside(mm):
     mm.accumulate_weights(acc, w, lens, query_len=2, max_seq_len=512, ids=ids, decay=0.5)
     assert acc.tolist() == [[6.5, 10.5, 10.5, 5.5]]
     assert mm.get_device_error() == 0
+    # as many entries as there can be, all of one block but the last
+    acc = torch.ones((1, 4)).cuda()
+    ids = torch.full((32, 32), 1, dtype=torch.int32).cuda()
+    ids[31, 31] = 3
+    mm.accumulate_weights(acc, torch.full((32, 32), 2.0).cuda(), lens, query_len=32,
+                          max_seq_len=512, ids=ids)
+    assert acc.tolist() == [[1.0, 2047.0, 1.0, 3.0]]
 
 
 def test_lengths_out_of_bounds_are_clamped(mm):
