@@ -108,12 +108,13 @@ struct Row {
   const char* p;     // token 0
   const char* q;     // null: nothing is taken off
   int skew, end;     // tokens are x in [skew, end)
-  bool wide;         // q (if any) has its 16-byte boundaries where p has
+  int shift;         // bytes from a 16-byte boundary of q to q's elements of p's boundaries
 
   __device__ __forceinline__ Row(const char* p_, const char* q_, int vocab) : p(p_), q(q_) {
     skew = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / E::kSize;
     end = skew + vocab;
-    wide = !q || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    shift = q ? static_cast<int>(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15
+              : 0;
   }
   // kPer elements from x, 0 outside the row, one by one.
   __device__ __forceinline__ uint4 gather(const char* row, int x) const {
@@ -127,16 +128,52 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // One warp's elements of a step: kGroups x 32 x kPer from x0.
+  // 16 bytes from byte `shift` of the two vectors v, next.
+  __device__ __forceinline__ uint4 shifted(const uint4& v, const uint4& next) const {
+    uint32_t w[8] = {v.x, v.y, v.z, v.w, next.x, next.y, next.z, next.w};
+    if (shift & 8)
+#pragma unroll
+      for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    if (shift & 4)
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    const int bits = (shift & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  }
+  // One warp's elements of a step: kGroups x 32 x kPer from x0.  In rows of odd
+  // lengths q's boundaries lie elsewhere than p's.  16-bit vectors of q are then
+  // put together from two aligned ones, a lane's own and the next lane's (256 x
+  // 131073 bf16: 48 us, 68 element by element; four fp32 elements one by one
+  // cost no more than that: 57 us, 55).
   template <bool Q>
   __device__ __forceinline__ void load(int x0, uint4 (&vp)[kGroups], uint4 (&vq)[kGroups]) const {
     const int lane = threadIdx.x & 31;
-    if (wide && x0 >= skew && x0 + E::kStep <= end) {
-      const int64_t at = static_cast<int64_t>(x0 + lane * E::kPer - skew) * E::kSize;
+    const int64_t at = static_cast<int64_t>(x0 + lane * E::kPer - skew) * E::kSize;
+    if (shift == 0 && x0 >= skew && x0 + E::kStep <= end) {
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         vp[k] = stream(p + at + k * 512);
         if constexpr (Q) vq[k] = stream(q + at + k * 512);
+      }
+    } else if (Q && E::kSize == 2 && x0 - E::kPer >= skew && x0 + E::kStep + E::kPer <= end) {
+      const char* from = q + at - shift;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        vp[k] = stream(p + at + k * 512);
+        vq[k] = stream(from + k * 512);
+      }
+      uint4 after = make_uint4(0, 0, 0, 0);          // what follows the last lane's vector
+      if (lane == 0) after = stream(from + kGroups * 512);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const uint4 give = lane ? vq[k] : k + 1 < kGroups ? vq[k + 1 < kGroups ? k + 1 : k] : after;
+        const int src = (lane + 1) & 31;
+        const uint4 next = make_uint4(__shfl_sync(0xffffffffu, give.x, src),
+                                      __shfl_sync(0xffffffffu, give.y, src),
+                                      __shfl_sync(0xffffffffu, give.z, src),
+                                      __shfl_sync(0xffffffffu, give.w, src));
+        vq[k] = shifted(vq[k], next);
       }
     } else {
 #pragma unroll

@@ -68,6 +68,15 @@ def test_verify_matches_exact_integers(mm, case):
     assert mm.get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("vocab", [4097, 4098, 4099, 4100, 4101, 4102, 4103, 4104, 2047, 65535])
+def test_rows_of_odd_lengths(mm, dtype, vocab):
+    """Target and draft rows that begin anywhere in 16 bytes, in every distance from each other."""
+    target, tokens, u, draft, lens = inputs(12, 6, vocab, dtype, True, vocab, spread=4.0)
+    check(mm, target, tokens, u, draft, lens)
+    check(mm, target, tokens, u, draft)
+
+
 def test_edges_of_the_random_numbers(mm):
     """u = 0 takes the first token with weight, u just below 1 the last one; a draft with u q = p
     is rejected."""
