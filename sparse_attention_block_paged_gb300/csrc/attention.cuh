@@ -8,7 +8,9 @@
 // l = sum 2^(x_t - m) and the vector o = sum 2^(x_t - m) v_t, with
 // x_t = scale log2(e) q.k_t.  Two such triples join to m = max(m1, m2),
 // l = l1 2^(m1-m) + l2 2^(m2-m), o alike; the result is o / l, and
-// m + log2 l is the (base 2) log-sum-exp.  Every warp keeps a triple of its
+// m + log2 l is the (base 2) log-sum-exp.  A maximum passes over NaN, so scores
+// that are all NaN (or all masked) leave m = -inf; l and o tell them apart, and
+// every join carries them on: NaN times a factor of 0 is NaN.  Every warp keeps a triple of its
 // own over its part of the tokens, CTAs join their warps' through shared
 // memory, and a (request, kv head) that several CTAs share is joined by the
 // last of them to finish, in a fixed order, so a result never depends on timing.
@@ -1123,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < TJ; ++t) {
           const float2 x = ml[(t * RT + (r >> 4)) * 16 + (r & 15)];
-          if (top != -INFINITY) sum += x.y * ex2(x.x - top);
+          sum += top == -INFINITY ? x.y : x.y * ex2(x.x - top);
         }
         if (r < rows) {
           if (whole) {
@@ -1246,14 +1248,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float top = m[u];
 #pragma unroll
                 for (int k = 0; k < PB; ++k) top = fmaxf(top, x[u][k].x);
-                if (top == -INFINITY) continue;
-                const float f = ex2(m[u] - top);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                const float f = ex2(m[u] - ref);
                 m[u] = top;
                 l[u] *= f;
                 o[u].x *= f; o[u].y *= f; o[u].z *= f; o[u].w *= f;
 #pragma unroll
                 for (int k = 0; k < PB; ++k) {
-                  const float w = ex2(x[u][k].x - top);
+                  const float w = ex2(x[u][k].x - ref);
                   l[u] += x[u][k].y * w;
                   o[u].x += v[u][k].x * w; o[u].y += v[u][k].y * w;
                   o[u].z += v[u][k].z * w; o[u].w += v[u][k].w * w;
@@ -1303,9 +1305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               consumer_sync();
               for (int t = 1; t < turns && turn == 0; ++t) {
                 const float* from = red + (t * each + unit) * 6;
-                const float top = fmaxf(m, from[0]);
-                if (top == -INFINITY) continue;
-                const float f = ex2(m - top), w = ex2(from[0] - top);
+                const float top = fmaxf(m, from[0]), ref = top == -INFINITY ? 0.0f : top;
+                const float f = ex2(m - ref), w = ex2(from[0] - ref);
                 m = top;
                 l = l * f + from[1] * w;
                 o.x = o.x * f + from[2] * w; o.y = o.y * f + from[3] * w;
