@@ -326,7 +326,8 @@ __device__ __forceinline__ void threshold(const uint32_t (&key)[ITEMS], int n, i
     }
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-      if (key[k] >= base && ((key[k] - base) >> size) == 0)
+      // (key 0, none, is at base 0 in the interval of weights from -inf on: not of the list)
+      if (key[k] && key[k] >= base && ((key[k] - base) >> size) == 0)
         ex.list[atomicAdd(&ex.few, 1)] = key[k];     // their order does not count
     if (threadIdx.x < 32) ex.list[left + threadIdx.x] = 0;
   }

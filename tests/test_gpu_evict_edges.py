@@ -1,0 +1,50 @@
+"""Eviction and the sum of weights at their edges: weights of -inf."""
+
+import pytest
+import torch
+
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mm(cuda_device):
+    import sparse_attention_block_paged_gb300 as m
+    m.get_device_error()
+    return m
+
+
+@pytest.mark.parametrize("width", [200, 257, 1025, 4097, 8192, 8193])
+@pytest.mark.parametrize("few", [1, 5, 200, 256, 257, 700])
+def test_the_lowest_weights(mm, width, few):
+    """Blocks of weight -inf and of the type's lowest values, and a budget that keeps some of them:
+    the threshold lies in the lowest of all intervals, where forced blocks and the places behind a
+    request's last block (most of them in the short requests) do not count."""
+    g = torch.Generator().manual_seed(width + few)
+    n = [width, width - 3, max(few + 20, width // 3), min(few + 50, width)]
+    n = [min(x, width) for x in n]
+    acc = torch.randn((4, width), generator=g)
+    acc[1::2] = acc[1::2].abs()
+    low = torch.tensor([-float("inf"), -3.4028235e38, -1.8e38])
+    for i, x in enumerate(n):
+        at = torch.randperm(x, generator=g)[:few]
+        acc[i, at] = low[torch.randint(0, 3 if i < 2 else 1, (at.numel(),), generator=g)]
+    lens = [128 * x for x in n]
+    table = torch.arange(width, dtype=torch.int32).repeat(4, 1).cuda()
+    for init, local, less in ((0, 1, 1), (1, 20, few // 2 + 1), (2, 3, few)):
+        # the shortest request loses `less` blocks, the others more; then the longest does
+        for m in (min(n), max(n)):
+            budget = max(init + local, m - less)
+            _, kept, out_lens = R.evict_ref(acc, lens, [], budget=budget, init=init, local=local,
+                                            max_seq_len=128 * width)
+            r = mm.evict_blocks(acc.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table,
+                                budget=budget, init_blocks=init, local_blocks=local,
+                                max_seq_len=128 * width)
+            for i, stay in enumerate(kept):
+                assert r.ids[i].tolist() == stay + [-1] * (budget - len(stay)), (i, budget)
+                assert torch.equal(r.weights[i, :len(stay)].cpu(), acc[i, stay])
+                gone = sorted(set(range(n[i])) - set(stay))
+                assert r.freed[i].tolist() == gone + [-1] * (r.freed.shape[1] - len(gone))
+            assert r.seq_lens.tolist() == out_lens
+    assert mm.get_device_error() == 0
