@@ -468,9 +468,9 @@ typedef struct mm3idx_attention {
  * workspace: >= mm3idx_attention_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use and kept by the caller for the
  * next call, under the rules of mm3idx_decode (launches that share one must
- * not overlap; zero it again after MM3IDX_DEV_TIMEOUT).  One workspace, given
- * with the same size each time, serves every batch of a model whose num_reqs,
- * query_len, max_seq_len and block weights stay within those it was sized for.
+ * not overlap; zero it again after MM3IDX_DEV_TIMEOUT).  One workspace serves
+ * calls of any shapes and types, each of whose sizes it has; the size grows
+ * with head_dim, num_reqs, query_len, max_seq_len and block weights.
  * Outputs must not overlap inputs or each other.  A work list that could pass
  * 2^37 places (num_reqs * kv_heads * cdiv(group * query_len, 64) *
  * (cdiv(max_seq_len, 128) + 4)) is MM3IDX_ERR_INVALID_ARGUMENT.
@@ -483,8 +483,7 @@ int mm3idx_paged_attention(const mm3idx_attention_t *a, void *workspace, size_t 
 /*
  * mm3idx_attention_workspace_bytes -- workspace of mm3idx_paged_attention: the
  * partial results of requests that are split across CTAs, with block_weights
- * != 0 one fp32 per (row, query head, block), and a ticket per (request, kv
- * head).  Reads the current device's SM count; no allocation.
+ * != 0 one fp32 per (row, query head, block), and a ticket per CTA.  Reads the current device's SM count; no allocation.
  */
 int mm3idx_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                      int32_t num_reqs, int32_t query_len, int32_t max_seq_len,

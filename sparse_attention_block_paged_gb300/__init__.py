@@ -766,8 +766,8 @@ def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, num_re
 def new_attention_workspace(q_heads, kv_heads, head_dim, num_reqs, query_len, max_seq_len,
                             block_weights=False, device=None):
     """A zero-filled workspace for :func:`paged_attention`, reusable across
-    calls that follow one another on the GPU and whose batches stay within
-    these bounds."""
+    calls that follow one another on the GPU, whatever their heads and types,
+    whose own :func:`attention_workspace_bytes` is no more."""
     device = torch.device(device or "cuda")
     with _on(device):
         n = attention_workspace_bytes(q_heads, kv_heads, head_dim, num_reqs, query_len,

@@ -74,12 +74,12 @@ int check_attention(const mm3idx_attention_t* a) {
   return MM3IDX_OK;
 }
 
-// Workspace: [partial references and sums][partial outputs], for block weights
-// [rows' log-sum-exps][tiles' log-sum-exps], each 256-aligned, and the tickets
-// at its very end.  Tickets have to be zero when a call starts; at the end no
-// smaller batch's other parts reach where a larger one's tickets lie.
+// Workspace: [a ticket an SM][partial references and sums][partial outputs], for
+// block weights [rows' log-sum-exps][tiles' log-sum-exps], each 256-aligned.
+// Tickets have to be zero when a call starts; they come first and are as many
+// for every problem, so that calls of any shapes can share a workspace.
 struct AttentionWs {
-  size_t ml, o, row, tile, tickets, total;   // offsets (tickets: bytes), sum
+  size_t ml, o, row, tile, total;   // offsets (of the tickets: 0), sum
 };
 
 AttentionWs attention_ws(int sms, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -88,12 +88,11 @@ AttentionWs attention_ws(int sms, int32_t q_heads, int32_t kv_heads, int32_t hea
   const size_t tasks = static_cast<size_t>(num_reqs) * kv_heads * cdiv(rows, 64);
   const int r = static_cast<int>(rows < 64 ? rows : 64);
   AttentionWs w{};
-  w.ml = 0;
+  w.ml = align256(static_cast<size_t>(sms) * 4);
   w.o = w.ml + static_cast<size_t>(2 * sms) * 64 * 8;
   w.row = w.o + static_cast<size_t>(2 * sms) * 64 * head_dim * 4;
   w.tile = w.row + (weights ? align256(static_cast<size_t>(num_reqs) * query_len * q_heads * 4) : 0);
-  w.tickets = align256(tasks * 4);
-  w.total = w.tile + w.tickets +
+  w.total = w.tile +
             (weights ? align256(tasks * cdiv(max_seq_len, kBlock) * 16 *
                                 attention_row_tiles16(r) * 4)
                      : 0);
@@ -235,8 +234,7 @@ int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t 
     if (a.kv_heads % g == 0 && sms / g * g * 25 >= sms * 24) a.gang = g;
   a.tasks = a.kv_heads / a.gang * a.row_tiles;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.tickets = reinterpret_cast<unsigned int*>(ws + (workspace_bytes & ~static_cast<size_t>(255)) -
-                                              w.tickets);
+  a.tickets = reinterpret_cast<unsigned int*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   if (p->block_weights) {

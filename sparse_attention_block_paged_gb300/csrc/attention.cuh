@@ -1201,12 +1201,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!whole) {
         // Publish; the last CTA of the task joins the partial results.  (The
-        // barrier orders the CTA's stores before thread 0's release.)
+        // barrier orders the CTA's stores before thread 0's release.)  The ticket
+        // is the one of the CTA that has the task's first tile: only one task
+        // goes on past the end of its share.
         const long long pos = misc->share.lo + sg.pos, pb = pos + kTaskCost;
         const int lead = gang_of(pb, misc->share.total, misc->share.grid);
         const int parts = gang_of(pb + sg.nb - 1, misc->share.total, misc->share.grid) - lead + 1;
         if (threadIdx.x == 0)
-          misc->last = !dead && ticket(a.tickets + sg.unit, parts - 1) == parts - 1;
+          misc->last = !dead && ticket(a.tickets + lead * a.gang + static_cast<int>(blockIdx.x),
+                                       parts - 1) == parts - 1;
         consumer_sync();
         if (misc->last) {
           // Four columns of a row are a unit.  A thread takes up to UB units, their

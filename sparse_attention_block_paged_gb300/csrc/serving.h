@@ -77,7 +77,7 @@ struct AttentionArgs {
   int64_t w_stride;
   int32_t w_width;            // cdiv(max_seq_len, 128)
   // workspace
-  unsigned int* tickets;      // [num_reqs * kv_heads * row_tiles], 0 between calls
+  unsigned int* tickets;      // [grid], 0 between calls
   float2* part_ml;            // [2 * grid][64]: reference and sum of a CTA's share of a task
   float* part_o;              // [2 * grid][64][head_dim]
   float* row_lse;             // with weights: [rows, q heads], base 2

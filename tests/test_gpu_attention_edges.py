@@ -1,5 +1,6 @@
 """mm3idx_paged_attention where its arithmetic or its bookkeeping meets an
-edge: NaN in queries and keys of whole and split requests."""
+edge: NaN in queries and keys of whole and split requests, a workspace that
+problems of several shapes share."""
 
 import pytest
 import torch
@@ -69,4 +70,49 @@ def test_nan_in_the_keys_of_many_shares(mm, dtype, kv, group, kvh, d, nan):
     assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all() and torch.isnan(w[0]).all()
     for got, was in zip((out, lse, w), base):
         assert torch.equal(got[1], was[1])
+    assert mm.get_device_error() == 0
+
+
+def test_one_workspace_for_models_of_different_shapes(mm):
+    """Calls of different head counts, head sizes and types take turns on one workspace, called and
+    as two captured graphs: what one leaves in it does not disturb the next."""
+    made = [R.make_attention([200 + 7 * (i % 90) for i in range(400)], group=2, kvh=8, d=64, page=16,
+                             seed=73),
+            R.make_attention([300, 0, 9000, 40000], ql=8, group=8, kvh=2, d=128, page=64, seed=74),
+            R.make_attention([30000] * 3, group=32, kvh=1, d=128, page=128, kv=E4M3, seed=75)]
+    sizes = [mm.attention_workspace_bytes(s["q"].shape[1], s["k"].shape[2], s["q"].shape[2],
+                                          s["lens"].shape[0], s["ql"], s["max_seq_len"], k == 1)
+             for k, s in enumerate(made)]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    want = [call(mm, s, weights=k == 1) for k, s in enumerate(made)]
+
+    def same(got, k):
+        assert torch.equal(got[0], want[k][0]) and torch.equal(got[1], want[k][1])
+        assert k != 1 or torch.equal(got[2], want[k][2])
+
+    for k in (0, 1, 0, 2, 1, 2, 0):
+        same(call(mm, made[k], weights=k == 1, workspace=ws), k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for k, s in enumerate(made):
+            rows, heads = s["q"].shape[:2]
+            o = [torch.empty_like(s["q"]), torch.empty((rows, heads), device="cuda"),
+                 torch.empty((rows, R.cdiv(s["max_seq_len"], 128)), device="cuda")]
+            graphs.append(torch.cuda.CUDAGraph())
+            side.synchronize()
+            with torch.cuda.graph(graphs[k], stream=side):
+                mm.paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"],
+                                   query_len=s["ql"], max_seq_len=s["max_seq_len"],
+                                   sm_scale=s["sm_scale"], out=o[0], lse=o[1],
+                                   block_weights=o[2] if k == 1 else None, workspace=ws)
+            outs.append(o)
+        for k in (0, 1, 0, 2, 0, 1, 2, 2, 1):
+            for x in outs[k]:
+                x.fill_(5)
+            graphs[k].replay()
+            side.synchronize()
+            same(outs[k], k)
+    torch.cuda.synchronize()
     assert mm.get_device_error() == 0
