@@ -73,6 +73,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "../../include/mm3idx.h"
 #include "ptx.cuh"
 #include "serving.h"
@@ -776,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
       const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
 
-      float sc_a = a.scale * kLog2e, sc_b = sc_a;
+      // (kept finite and normal: 0 and infinity would make NaN of -inf and 0)
+      float sc_a = fminf(a.scale * kLog2e, FLT_MAX), sc_b = sc_a;
       if constexpr (kByte) {
         // fp16 queries, each row scaled by the power of two that brings its
         // largest element into [1, 2) (not at all where that is 0)
@@ -800,8 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int e = min(static_cast<int>(__float_as_uint(top[x]) >> 23), 253);
           down[x] = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
           const float up = e == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e) << 23);
-          if (x) sc_b *= up;
-          else sc_a *= up;
+          if (x) sc_b = fminf(fmaxf(sc_b * up, FLT_MIN), FLT_MAX);
+          else sc_a = fminf(fmaxf(sc_a * up, FLT_MIN), FLT_MAX);
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)

@@ -1,6 +1,6 @@
 """mm3idx_paged_attention where its arithmetic or its bookkeeping meets an
 edge: NaN in queries and keys of whole and split requests, a workspace that
-problems of several shapes share."""
+problems of several shapes share, scales at the ends of fp32's range."""
 
 import pytest
 import torch
@@ -115,4 +115,23 @@ def test_one_workspace_for_models_of_different_shapes(mm):
             side.synchronize()
             same(outs[k], k)
     torch.cuda.synchronize()
+    assert mm.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,kv,d", [(BF16, E4M3, 128), (FP16, E4M3, 64), (BF16, BF16, 128),
+                                        (FP16, FP16, 64)])
+def test_scales_beyond_the_range_of_their_product(mm, dtype, kv, d):
+    """Queries and scales whose product leaves fp32's range at either end while the scores are 0
+    or next to it: every visible token counts alike, and no masked one does."""
+    small, large = torch.finfo(dtype).tiny, torch.finfo(dtype).max
+    for size, sm_scale in ((small, 2.0 ** -120), (large / 2, 3e38)):
+        s = R.make_attention([300, 5, 1000], ql=2, group=4, kvh=2, d=d, page=64, dtype=dtype, kv=kv,
+                             seed=72)
+        s["q"] = (torch.sign(s["q"].float()) * size).to(dtype)
+        if size == large / 2:
+            s["k"] = torch.where(torch.isnan(s["k"].float()), s["k"].float(), 0.0).to(kv)
+        s["sm_scale"] = sm_scale
+        got, want = call(mm, s), R.attention_ref(s)
+        assert torch.isfinite(want[3]).all()
+        check(got, want)
     assert mm.get_device_error() == 0
