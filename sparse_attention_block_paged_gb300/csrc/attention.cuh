@@ -680,18 +680,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kSpare) {
       // ------------------------------------------- rows of empty requests
+      // (a request's rows dealt out to the CTAs where there are fewer requests:
+      // one CTA takes seconds for 2^20 rows of 128 heads)
       const int heads = a.kv_heads * a.group;
-      for (int i = cta(); i < a.num_reqs; i += gridDim.x * gridDim.y) {
+      const int64_t pieces = static_cast<int64_t>(heads) * (D / 8);   // of a row, 16 bytes each
+      const int ctas = static_cast<int>(gridDim.x * gridDim.y);
+      const int share = a.num_reqs < ctas ? ctas / a.num_reqs : 1;
+      for (int i = cta() / share; i < a.num_reqs; i += ctas / share) {
         if (request_len(a, i) > 0) continue;
-        const int per_row = heads * (D / 8);
-        for (int e = lane; e < a.query_len * per_row; e += 32) {
-          const int64_t row = static_cast<int64_t>(i) * a.query_len + e / per_row;
-          const int h = e % per_row / (D / 8), d = e % (D / 8) * 8;
-          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head + d;
-          *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
-          if (d == 0) {
-            if (a.lse) a.lse[row * a.lse_tok + h] = -INFINITY;
-            if (weigh) a.row_lse[row * heads + h] = -INFINITY;
+        for (int j = cta() % share; j < a.query_len; j += share) {
+          const int64_t row = static_cast<int64_t>(i) * a.query_len + j;
+          for (int64_t e = lane; e < pieces; e += 32) {
+            const int h = static_cast<int>(e / (D / 8)), d = static_cast<int>(e % (D / 8)) * 8;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.o_tok + h * a.o_head + d;
+            *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+            if (d == 0) {
+              if (a.lse) a.lse[row * a.lse_tok + h] = -INFINITY;
+              if (weigh) a.row_lse[row * heads + h] = -INFINITY;
+            }
           }
         }
       }

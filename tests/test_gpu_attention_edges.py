@@ -1,6 +1,7 @@
 """mm3idx_paged_attention where its arithmetic or its bookkeeping meets an
 edge: NaN in queries and keys of whole and split requests, a workspace that
-problems of several shapes share, scales at the ends of fp32's range."""
+problems of several shapes share, scales at the ends of fp32's range,
+an empty request of very many rows."""
 
 import pytest
 import torch
@@ -135,3 +136,25 @@ def test_scales_beyond_the_range_of_their_product(mm, dtype, kv, d):
         assert torch.isfinite(want[3]).all()
         check(got, want)
     assert mm.get_device_error() == 0
+
+
+def test_an_empty_request_of_very_many_rows(mm):
+    """An empty slot whose rows are 2^31 pieces of 16 bytes and more: zeros throughout."""
+    rows, heads, d = 2 ** 20 + 1, 128, 128
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB")
+    # queries of all rows lie over each other: 8 elements from one to the next
+    q = torch.zeros(8 * (rows + heads) + d, dtype=BF16, device="cuda")
+    q = q.as_strided((rows, heads, d), (8, 8, 1))
+    cache = torch.zeros((1, 128, 1, d), dtype=BF16, device="cuda")
+    out = torch.empty((rows, heads, d), dtype=BF16, device="cuda")
+    lse = torch.zeros((rows, heads), device="cuda")
+    at = [0, 1, 2 ** 18, 2 ** 19 - 1, 2 ** 19, 2 ** 20 - 1, 2 ** 20]
+    out[at] = 3.0
+    mm.paged_attention(q, cache, cache, torch.zeros((1, 8193), dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, dtype=torch.int32, device="cuda"), query_len=rows,
+                       max_seq_len=rows, sm_scale=1.0, out=out, lse=lse)
+    assert (out[at] == 0).all() and (lse == -float("inf")).all()
+    assert mm.get_device_error() == 0
+    del out
+    torch.cuda.empty_cache()
