@@ -4,8 +4,10 @@
 //
 // Mathematics.  acc' = decay acc + sum of the step's weights, carried as an
 // unevaluated sum of two floats (products by fma, sums by the two-sum of Knuth),
-// exact to about 2^-46, then rounded once to fp32: the order of the terms does
-// not show.  (fp64 instructions would do the same at a sixtieth of the rate:
+// good to about 2^-46 of the terms' magnitudes, then rounded once to fp32.  The
+// order of the terms is fixed (query rows, then places), so a call repeats
+// itself; another order can move a result next to a rounding border by a step.
+// (fp64 instructions would do the same at a sixtieth of the rate:
 // 128 requests of 8192 blocks took 52 us with them, most of it there.)  The
 // weights are ordered by the unsigned image of their bits (ordered_bits).  The
 // weight of the last block that stays is found in two steps: the keys between

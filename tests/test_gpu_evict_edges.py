@@ -1,4 +1,8 @@
-"""Eviction and the sum of weights at their edges: weights of -inf."""
+"""Eviction and the sum of weights at their edges: weights of -inf, sums next
+to a rounding border."""
+
+import itertools
+from fractions import Fraction
 
 import pytest
 import torch
@@ -48,3 +52,31 @@ def test_the_lowest_weights(mm, width, few):
                 assert r.freed[i].tolist() == gone + [-1] * (r.freed.shape[1] - len(gone))
             assert r.seq_lens.tolist() == out_lens
     assert mm.get_device_error() == 0
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_sums_next_to_a_rounding_border(mm, sparse):
+    """Terms whose exact sum lies next to the middle between two fp32 numbers, in every order.  The
+    second float takes up what each of the additions rounds off, at most k 2^-24 of the terms'
+    magnitudes after k of them, and rounds itself by 2^-24 of that: 6 2^-48 for three terms, beside
+    the half step of the one rounding at the end.  The same call gives the same."""
+    terms = [[2.0 ** -24, 2.0 ** -48, 2.0 ** -48], [2.0 ** -24, -2.0 ** -48, 2.0 ** -50],
+             [-2.0 ** -25, -2.0 ** -49, 2.0 ** -51], [2.0 ** -24, 2.0 ** -24, 2.0 ** -47],
+             [3.0, -3.0, 2.0 ** -24], [0.1, 0.2, 0.3]]
+    orders = [list(p) for t in terms for p in itertools.permutations(t)]
+    w = torch.tensor(orders).T.contiguous()              # [rows, blocks]: a block an order
+    n = w.shape[1]
+    ids = torch.arange(n, dtype=torch.int32).repeat(3, 1).contiguous() if sparse else None
+    true = [1 + sum(Fraction(float(x)) for x in col) for col in w.T]
+    size = [1 + sum(abs(Fraction(float(x))) for x in col) for col in w.T]
+    got = []
+    for _ in range(2):
+        acc = torch.ones((1, n)).cuda()
+        mm.accumulate_weights(acc, w.cuda(), torch.tensor([128 * n], dtype=torch.int32).cuda(),
+                              query_len=3, max_seq_len=128 * n,
+                              ids=None if ids is None else ids.cuda())
+        got.append(acc[0].cpu())
+    assert torch.equal(*got)
+    for x, t, a in zip(got[0], true, size):
+        step = Fraction(float(torch.nextafter(x, torch.tensor(9.0)) - x))
+        assert abs(Fraction(float(x)) - t) <= step / 2 + 6 * a / 2 ** 48
