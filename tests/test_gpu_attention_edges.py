@@ -1,7 +1,7 @@
 """mm3idx_paged_attention where its arithmetic or its bookkeeping meets an
 edge: NaN in queries and keys of whole and split requests, a workspace that
 problems of several shapes share, scales at the ends of fp32's range,
-an empty request of very many rows."""
+an empty request of very many rows, weights over e4m3 values."""
 
 import pytest
 import torch
@@ -158,3 +158,15 @@ def test_an_empty_request_of_very_many_rows(mm):
     assert mm.get_device_error() == 0
     del out
     torch.cuda.empty_cache()
+
+
+def test_fp16_weights_over_e4m3_values_are_pairs(mm, monkeypatch):
+    """fp16 output over e4m3 values: two tokens of opposite values, so that the output is the
+    difference of two weights, which a single fp16 number each would miss by up to 2^-12."""
+    monkeypatch.setitem(R.WEIGHT, E4M3, 2.0 ** -22)      # the square of half a step, as over fp16
+    s = R.make_attention([2] * 200, group=16, kvh=2, d=64, page=16, dtype=FP16, kv=E4M3, seed=76,
+                         q_scale=0.5)
+    v = torch.ones(s["v"].shape, device="cuda")
+    v[:, 1] = -1.0
+    s["v"] = v.to(E4M3)
+    check(call(mm, s), R.attention_ref(s))

@@ -1,5 +1,5 @@
 """Eviction and the sum of weights at their edges: weights of -inf, sums next
-to a rounding border."""
+to a rounding border, steps of selected blocks over wide tables."""
 
 import itertools
 from fractions import Fraction
@@ -80,3 +80,39 @@ def test_sums_next_to_a_rounding_border(mm, sparse):
     for x, t, a in zip(got[0], true, size):
         step = Fraction(float(torch.nextafter(x, torch.tensor(9.0)) - x))
         assert abs(Fraction(float(x)) - t) <= step / 2 + 6 * a / 2 ** 48
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("width", [257, 1025, 2049, 4097, 8192, 8193])
+def test_selected_blocks_over_wide_tables(mm, width, in_place):
+    """Steps of 4 rows x 32 ids, some given twice, some of no block, all over tables of 257 to 8193
+    blocks, most of which the requests do not reach."""
+    ql, topk = 4, 32
+    g = torch.Generator().manual_seed(width)
+    n = [width, width - 1, width // 2 + 1, 70, 1, 0]
+    reqs = len(n)
+    lens = torch.tensor([max(0, 128 * x - 5) for x in n], dtype=torch.int32)
+    acc = torch.exp(torch.randn((reqs, width), generator=g))
+    # a quarter of the ids next to the end of the table, the others anywhere, none's (-1), repeats
+    ids = torch.randint(0, width, (reqs * ql, topk), generator=g, dtype=torch.int32)
+    ids[:, ::4] = width - 1 - torch.randint(0, 40, (reqs * ql, topk // 4), generator=g,
+                                            dtype=torch.int32)
+    ids[:, 5], ids[:, 7], ids[1::ql, 9] = -1, ids[:, 6], ids[::ql, 9]
+    w = 4 * torch.exp(torch.randn((reqs * ql, topk), generator=g))
+    table = torch.randint(0, 10 ** 6, (reqs, width), generator=g, dtype=torch.int32)
+    budget = width // 2
+    new, kept, out_lens = R.evict_ref(acc, lens.tolist(), [], budget=budget, init=1, local=2,
+                                      max_seq_len=128 * width, weights=w, ids=ids, ql=ql, decay=0.9)
+    d = [t.cuda() for t in (acc, lens, table, w, ids)]
+    kw = dict(budget=budget, init_blocks=1, local_blocks=2, max_seq_len=128 * width,
+              block_weights=d[3], ids=d[4], query_len=ql, decay=0.9)
+    r = mm.evict_blocks(d[0], d[1], d[2], in_place=in_place, **kw)
+    for i, stay in enumerate(kept):
+        m, gone = len(stay), sorted(set(range(n[i])) - set(stay))
+        assert r.ids[i].tolist() == stay + [-1] * (budget - m)
+        assert int(r.seq_lens[i]) == out_lens[i]
+        assert torch.equal(r.weights[i, :m].cpu(), new[i][stay].float())
+        assert (r.weights[i, m:] == 0).all()
+        assert r.block_table[i, :budget].tolist() == table[i, stay].tolist() + [-1] * (budget - m)
+        assert r.freed[i].tolist() == table[i, gone].tolist() + [-1] * (r.freed.shape[1] - len(gone))
+    assert mm.get_device_error() == 0
