@@ -433,7 +433,7 @@ typedef struct mm3idx_attention {
     int32_t        num_reqs;       /* >= 0                                                  */
     int32_t        query_len;      /* query tokens a request, >= 1                          */
     int32_t        max_seq_len;    /* bound on seq_lens fixed across graph replays          */
-    float          sm_scale;       /* finite, > 0, and so (not subnormal) its product with k_scale */
+    float          sm_scale;       /* finite, > 0, and so (not subnormal, <= 2.35e38) its product with k_scale */
     void          *out;            /* [num_reqs * query_len, q_heads, head_dim] of q_type, d stride 1, 16-byte aligned */
     int64_t        out_token_stride, out_head_stride; /* multiples of 8 that do not overlap */
     float         *lse;            /* fp32 [num_reqs * query_len, q_heads], or NULL         */

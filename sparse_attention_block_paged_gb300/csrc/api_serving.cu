@@ -13,6 +13,8 @@ using namespace mm3idx;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;   // the kernel's scores are base 2
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MM3IDX_OK : MM3IDX_ERR_CUDA; }
@@ -34,7 +36,8 @@ int check_attention(const mm3idx_attention_t* a) {
   if (cdiv(a->max_seq_len, kBlock) >= 0xFFFF) return MM3IDX_ERR_TOO_MANY_BLOCKS;
   if (!(a->sm_scale > 0.0f) || !std::isfinite(a->sm_scale) || !(a->k_scale > 0.0f) ||
       !std::isfinite(a->k_scale) || !std::isfinite(a->v_scale) ||
-      !std::isnormal(a->sm_scale * a->k_scale))
+      !std::isnormal(a->sm_scale * a->k_scale) ||
+      !std::isfinite(a->sm_scale * a->k_scale * kLog2e))
     return MM3IDX_ERR_INVALID_ARGUMENT;
   const bool half = a->q_type == MM3IDX_TYPE_BF16 || a->q_type == MM3IDX_TYPE_FP16;
   if (!half || (a->kv_type != a->q_type && a->kv_type != MM3IDX_TYPE_E4M3) ||

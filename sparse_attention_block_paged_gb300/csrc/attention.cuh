@@ -784,11 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
       const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
 
-      // (kept finite and normal: 0 and infinity would make NaN of -inf and 0)
-      float sc_a = fminf(a.scale * kLog2e, FLT_MAX), sc_b = sc_a;
+      float sc_a = a.scale * kLog2e, sc_b = sc_a;
       if constexpr (kByte) {
         // fp16 queries, each row scaled by the power of two that brings its
-        // largest element into [1, 2) (not at all where that is 0)
+        // largest element into [1, 2) (not at all where that is 0).  The factor of
+        // the scores stays finite and normal: infinity and 0 would make NaN of a
+        // score of 0 and of a masked one's -inf.
         float top[2] = {0.0f, 0.0f}, down[2];
         auto floats = [&](uint32_t w) {
           if constexpr (kOutBf)
