@@ -1,7 +1,7 @@
 """mm3idx_paged_attention where its arithmetic or its bookkeeping meets an
 edge: NaN in queries and keys of whole and split requests, a workspace that
 problems of several shapes share, scales at the ends of fp32's range,
-an empty request of very many rows, weights over e4m3 values."""
+infinite scores, an empty request of very many rows, weights over e4m3 values."""
 
 import pytest
 import torch
@@ -170,3 +170,35 @@ def test_fp16_weights_over_e4m3_values_are_pairs(mm, monkeypatch):
     v[:, 1] = -1.0
     s["v"] = v.to(E4M3)
     check(call(mm, s), R.attention_ref(s))
+
+
+@pytest.mark.parametrize("dtype,group,d", [(BF16, 4, 128), (FP16, 8, 64)])
+def test_infinite_scores(mm, dtype, group, d):
+    """A score of -inf weighs nothing, whether a CTA has the request or many share it; one of +inf
+    makes NaN of the rows that see it, and of no other."""
+    lens = [500, 30000, 200]
+    s = R.make_attention(lens, ql=2, group=group, kvh=2, d=d, page=64, dtype=dtype, seed=77)
+    s["q"][:, :, 0] = 1.0
+    at = [(0, 100), (1, 20000), (1, 29999), (2, 199)]        # the last tokens: the later rows' alone
+
+    def with_key(value):
+        k = s["k"].clone()
+        for i, t in at:
+            k[int(s["table"][i, t // 64]), t % 64, :, 0] = value
+        return call(mm, {**s, "k": k})
+
+    low = with_key(-6e4)                                     # 2^-5000 of the others and less
+    for x, y in zip(with_key(-float("inf")), low):
+        assert torch.equal(x, y) and not torch.isnan(x).any()
+    out, lse, w = with_key(float("inf"))
+    want = R.attention_ref(s)
+    assert mm.get_device_error() == 0
+    for r in range(6):
+        seen = any(i == r // 2 and t < lens[i] - 1 + r % 2 for i, t in at)
+        blocks = R.cdiv(lens[r // 2] - 1 + r % 2, 128)
+        if seen:
+            assert torch.isnan(out[r]).all() and torch.isnan(lse[r]).all()
+            assert torch.isnan(w[r, :blocks]).all() and (w[r, blocks:] == 0).all()
+        else:
+            assert ((out[r].double() - want[0][r]).abs() <= want[3][r]).all()
+            assert ((lse[r].double() - want[1][r]).abs() <= want[4][r]).all()
