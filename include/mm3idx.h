@@ -455,8 +455,12 @@ typedef struct mm3idx_attention {
  * Masked tokens do not count whatever their keys and values hold, NaN and
  * infinity among it.  A row that sees nothing (an empty slot, pos < 0, pages
  * outside the cache) gets zeros and lse = -inf, as does one whose scores are
- * all -inf.  block_weights is written for all cdiv(max_seq_len, 128) columns,
- * 0 past the row's last block.
+ * all -inf.  A row that has NaN or +inf among its scores is NaN, its lse and
+ * its weights of every block it sees too; an infinite value that a row sees
+ * makes that element infinite or NaN.  Sums of weights and values are held in
+ * fp32 before they are divided, weights up to 2^8 (2^15 over fp16 and e4m3), so
+ * bf16 values near 2^119 / tokens overflow.  block_weights is written for all
+ * cdiv(max_seq_len, 128) columns, 0 past the row's last block.
  *
  * Attention over selected blocks is the same call on the page table of
  * mm3idx_decode_sparse_table: page_table = sparse_block_table_out, seq_lens =
@@ -511,8 +515,9 @@ typedef struct mm3idx_weights {
  * mm3idx_accumulate_weights -- acc[i, b] = decay * acc[i, b] + the sum of
  * request i's weights of block b, in place, for its blocks
  * b < cdiv(seq_lens[i], 128); the other columns are left as they are.  Summed
- * in twice fp32's digits and rounded once; an id given twice counts twice,
- * one outside the request's blocks is ignored.
+ * in the order of the rows and columns, in two floats (good to about 2^-46 of
+ * the terms' magnitudes), and rounded once; an id given twice counts twice, one
+ * outside the request's blocks is ignored.
  */
 int mm3idx_accumulate_weights(const mm3idx_weights_t *w, void *stream);
 

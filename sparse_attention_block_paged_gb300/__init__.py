@@ -835,7 +835,11 @@ def evict_blocks(acc, seq_lens, block_table, *, budget, init_blocks, local_block
     :class:`Eviction` of the compacted tables, weights and lengths; the
     inputs are left as they are, or with ``in_place`` overwritten by them
     (their columns from ``budget`` on stay as they were).  ``out``: an
-    Eviction of the same shapes to write into."""
+    Eviction of the same shapes to write into.
+
+    The tensors made by a call are parts of one allocation: keeping one keeps
+    the memory of all, and ``torch.save`` of one writes all (``clone()`` it
+    first)."""
     with _HERE if stream is None else _run_on(stream, acc):
         return tuple.__new__(Eviction, _binding.evict_blocks(
             acc, seq_lens, block_table, attention_block_table, block_weights, ids, budget,
@@ -854,7 +858,8 @@ def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, dra
     fp16; draft_tokens int32 [num_reqs, drafts]; uniforms fp32 in [0, 1)
     [num_reqs, drafts + 1]; draft_lens int32 [num_reqs] when requests have
     fewer.  Returns (tokens int32 [num_reqs, drafts + 1]: the accepted drafts,
-    the drawn token, then -1; the number accepted, int32 [num_reqs])."""
+    the drawn token, then -1; the number accepted, int32 [num_reqs]); the two,
+    where the call makes them, are parts of one allocation."""
     with _HERE if stream is None else _run_on(stream, target_probs):
         return _binding.verify_drafts(target_probs, draft_tokens, uniforms, draft_probs,
                                       draft_lens, out, accepted)
