@@ -391,6 +391,11 @@ int mm3idx_forward_workspace_bytes(int32_t heads, int32_t num_decodes, int32_t d
  * the page table of the selected blocks; these three are this library's own.
  * ------------------------------------------------------------------------ */
 
+/* int32 and fp32 arrays of these calls have to be 4-byte aligned; one that is
+ * not is refused (lengths: MM3IDX_ERR_INVALID_ARGUMENT, other inputs:
+ * _TABLE_LAYOUT, outputs: _OUT_LAYOUT, lse and weights of the attention:
+ * _ATTENTION_LAYOUT). */
+
 /* element types */
 #define MM3IDX_TYPE_BF16  0
 #define MM3IDX_TYPE_FP16  1

@@ -17,6 +17,11 @@ constexpr float kLog2e = 1.4426950408889634f;   // the kernel's scores are base 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// int32 and fp32 arrays (null is aligned)
+template <class... P>
+bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MM3IDX_OK : MM3IDX_ERR_CUDA; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -54,6 +59,9 @@ int check_attention(const mm3idx_attention_t* a) {
   if (a->num_reqs == 0) return MM3IDX_OK;
   if (!a->q || !a->k_cache || !a->v_cache || !a->page_table || !a->seq_lens || !a->out)
     return MM3IDX_ERR_INVALID_ARGUMENT;
+  if (!aligned4(a->seq_lens)) return MM3IDX_ERR_INVALID_ARGUMENT;
+  if (!aligned4(a->page_table)) return MM3IDX_ERR_TABLE_LAYOUT;
+  if (!aligned4(a->lse, a->block_weights)) return MM3IDX_ERR_ATTENTION_LAYOUT;
   if (a->num_pages < 1) return MM3IDX_ERR_CACHE_LAYOUT;
   const int kb = a->kv_type == MM3IDX_TYPE_E4M3 ? 1 : 2;
   if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->out) ||
@@ -139,7 +147,9 @@ int check_weights(const mm3idx_weights_t* w) {
   if (w->num_reqs == 0) return MM3IDX_OK;
   const int64_t width = cdiv(w->max_seq_len, kBlock);
   if (!w->acc || !w->seq_lens) return MM3IDX_ERR_INVALID_ARGUMENT;
-  if (w->acc_stride < width) return MM3IDX_ERR_OUT_LAYOUT;
+  if (!aligned4(w->seq_lens)) return MM3IDX_ERR_INVALID_ARGUMENT;
+  if (!aligned4(w->block_weights, w->ids)) return MM3IDX_ERR_TABLE_LAYOUT;
+  if (w->acc_stride < width || !aligned4(w->acc)) return MM3IDX_ERR_OUT_LAYOUT;
   if (!w->block_weights) return w->ids ? MM3IDX_ERR_INVALID_ARGUMENT : MM3IDX_OK;
   if (!w->ids) return w->weights_stride < width ? MM3IDX_ERR_TABLE_LAYOUT : MM3IDX_OK;
   if (w->topk < 1) return MM3IDX_ERR_TOPK;
@@ -285,7 +295,7 @@ int mm3idx_evict_blocks(const mm3idx_weights_t* w, const mm3idx_eviction_t* e, v
   const int64_t width = cdiv(w->max_seq_len, kBlock);
   if (!e->acc_out || !e->seq_lens_out) return MM3IDX_ERR_INVALID_ARGUMENT;
   if (e->acc_out_stride < width || (e->acc_out == w->acc && e->acc_out_stride != w->acc_stride) ||
-      (e->ids && e->ids_stride < e->budget))
+      (e->ids && e->ids_stride < e->budget) || !aligned4(e->ids, e->acc_out, e->seq_lens_out))
     return MM3IDX_ERR_OUT_LAYOUT;
   const int64_t gone = width > e->budget ? width - e->budget : 1;
   for (const mm3idx_evict_table_t& t : e->tables) {
@@ -294,9 +304,9 @@ int mm3idx_evict_blocks(const mm3idx_weights_t* w, const mm3idx_eviction_t* e, v
       continue;
     }
     if (!t.out) return MM3IDX_ERR_INVALID_ARGUMENT;
-    if (t.in_stride < width) return MM3IDX_ERR_TABLE_LAYOUT;
+    if (t.in_stride < width || !aligned4(t.in)) return MM3IDX_ERR_TABLE_LAYOUT;
     if (t.out_stride < e->budget || (t.out == t.in && t.out_stride != t.in_stride) ||
-        (t.freed && t.freed_stride < gone))
+        (t.freed && t.freed_stride < gone) || !aligned4(t.out, t.freed))
       return MM3IDX_ERR_OUT_LAYOUT;
   }
   int sms = 0;
@@ -337,9 +347,10 @@ int mm3idx_verify_drafts(const mm3idx_drafts_t* d, void* stream) {
                     (d->num_reqs > 1 && d->draft_req_stride < d->vocab))))
     return MM3IDX_ERR_VOCAB;
   if ((d->drafts > 0 && d->num_reqs > 1 && d->tokens_stride < d->drafts) ||
-      (d->num_reqs > 1 && d->uniforms_stride < d->drafts + 1))
+      (d->num_reqs > 1 && d->uniforms_stride < d->drafts + 1) ||
+      !aligned4(d->tokens, d->draft_lens, d->uniforms))
     return MM3IDX_ERR_TABLE_LAYOUT;
-  if (d->out_stride < d->drafts + 1) return MM3IDX_ERR_OUT_LAYOUT;
+  if (d->out_stride < d->drafts + 1 || !aligned4(d->out, d->accepted)) return MM3IDX_ERR_OUT_LAYOUT;
   int sms = 0;
   int32_t* status = nullptr;
   const int rc = library_device(&sms, &status);
