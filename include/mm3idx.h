@@ -87,6 +87,8 @@ extern "C" {
 #define MM3IDX_DEV_SEQ_TOO_SHORT 4  /* seq_lens[i] < query_len              */
 #define MM3IDX_DEV_TIMEOUT       8  /* an on-chip pipeline wait gave up; outputs of that launch are invalid */
 #define MM3IDX_DEV_BAD_ROWS     16  /* ragged calls: cu_seqlens_q does not run from 0 to total_q without decreasing */
+#define MM3IDX_DEV_NO_PAGES     64  /* page pool: fewer free pages than were asked for */
+#define MM3IDX_DEV_NOT_HELD    128  /* mm3idx_release_pages: a page without a reference (left at 0) */
 #define MM3IDX_DEV_BAD_TOKEN    32  /* mm3idx_verify_drafts: a drafted token outside [0, vocab) (rejected) */
 
 #define MM3IDX_MAX_TOPK            32  /* largest topk served                  */
@@ -464,7 +466,9 @@ typedef struct mm3idx_attention {
  * its weights of every block it sees too; an infinite value that a row sees
  * makes that element infinite or NaN.  Sums of weights and values are held in
  * fp32 before they are divided, weights up to 2^8 (2^15 over fp16 and e4m3), so
- * bf16 values near 2^119 / tokens overflow.  block_weights is written for all
+ * bf16 values near 2^119 / tokens overflow. Scores are rounded to fp32 before
+ * the row's largest is taken from them, so one of 2^24 and more in magnitude may
+ * make its row NaN.  block_weights is written for all
  * cdiv(max_seq_len, 128) columns, 0 past the row's last block.
  *
  * Attention over selected blocks is the same call on the page table of
@@ -603,6 +607,182 @@ typedef struct mm3idx_drafts {
  * Outputs must not overlap inputs.
  */
 int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The life of a paged cache: pages taken, written, shared and given back.
+ * ------------------------------------------------------------------------ */
+
+#define MM3IDX_ERR_PAGES (-17) /* page pool: cache count, page bytes, strides, page size or table not served */
+
+#define MM3IDX_MAX_CACHES 64   /* caches of one page pool that a call takes     */
+
+/* One fp32 scale a page and kv head of an e4m3 cache.  Host struct of device
+ * pointers (4-byte aligned); strides count elements and are >= 0.  Scales
+ * are used as if clamped to [2^-60, 2^60] (NaN: 2^-60). */
+typedef struct mm3idx_kv_scales {
+    float  *k;                     /* [num_pages, kv_heads]                                 */
+    int64_t k_page_stride, k_head_stride;
+    float  *v;
+    int64_t v_page_stride, v_head_stride;
+} mm3idx_kv_scales_t;
+
+/*
+ * mm3idx_paged_attention_scaled -- mm3idx_paged_attention over e4m3 pages
+ * (kv_type MM3IDX_TYPE_E4M3, else MM3IDX_ERR_ATTENTION_SHAPE) with a scale for
+ * each page and kv head: a key element is code * k_scale * s->k[page, head],
+ * a value element code * v_scale * s->v[page, head].  s is only read.  The
+ * weights' products with a page's scale keep the precision that the call
+ * without scales gives them, as long as the scales of the values that a row
+ * sees lie within a factor of 2^80 of each other.  Everything else as there;
+ * the workspace too.
+ */
+int mm3idx_paged_attention_scaled(const mm3idx_attention_t *a, const mm3idx_kv_scales_t *s,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* New tokens' keys and values on their way into the cache.  Host struct of
+ * device pointers; strides count elements. */
+typedef struct mm3idx_append {
+    const void    *k;              /* [rows, kv_heads, head_dim], d stride 1, 16-byte aligned */
+    int64_t        k_token_stride, k_head_stride; /* positive multiples of 8              */
+    const void    *v;              /* as k                                                  */
+    int64_t        v_token_stride, v_head_stride;
+    int32_t        type;           /* MM3IDX_TYPE_BF16 or _FP16                             */
+    int32_t        kv_type;        /* type, or MM3IDX_TYPE_E4M3                             */
+    int32_t        kv_heads;       /* >= 1                                                  */
+    int32_t        head_dim;       /* 64 or 128                                             */
+    void          *k_cache;        /* as in mm3idx_attention_t                              */
+    int64_t        k_page_stride, k_page_token_stride, k_page_head_stride;
+    void          *v_cache;
+    int64_t        v_page_stride, v_page_token_stride, v_page_head_stride;
+    float          k_scale;        /* a key element is stored divided by it (finite, > 0, normal) */
+    float          v_scale;
+    mm3idx_kv_scales_t scales;     /* k and v both NULL: none; else kv_type e4m3            */
+    int32_t        num_pages;
+    int32_t        page_size;      /* 16, 32, 64 or 128                                     */
+    const int32_t *page_table;     /* int32 [num_reqs, table_stride]                        */
+    int64_t        table_stride;
+    int32_t        table_width;    /* >= cdiv(max_seq_len, page_size)                       */
+    const int32_t *seq_lens;       /* int32 [num_reqs], the new tokens included             */
+    int32_t        num_reqs;
+    int32_t        query_len;      /* new tokens a request; with cu_seqlens_q the most of one */
+    int32_t        max_seq_len;
+    const int32_t *cu_seqlens_q;   /* NULL, or int32 [num_reqs + 1] from 0 to total_q: ragged */
+    int32_t        total_q;        /* rows; num_reqs * query_len where cu_seqlens_q is NULL */
+} mm3idx_append_t;
+
+/*
+ * mm3idx_append_kv -- new tokens into their requests' pages.  Row j of request
+ * i's n rows goes to position pos = seq_lens[i] - n + j, slot pos % page_size of
+ * page page_table[i, pos / page_size]; rows with pos < 0 (an empty slot of the
+ * batch) are dropped, as are those of a page outside the cache
+ * (MM3IDX_DEV_BAD_PAGE) and, with a length above max_seq_len (clamped,
+ * MM3IDX_DEV_SEQ_TOO_LONG), the positions follow the clamped length.  With
+ * y = x / k_scale (one fp32 division; values alike):
+ *   without scales   the element is y rounded to the nearest, e4m3 saturated
+ *                    at 448; NaN stays NaN;
+ *   with scales      of a page and head that get tokens, A = the largest |y|
+ *                    among its finite new elements and need = the least power of
+ *                    two, in [2^-60, 2^60], with A / need <= 448.  The page's
+ *                    scale becomes need where the new tokens start at slot 0,
+ *                    else the larger of need and its old scale.  Where it grows
+ *                    the codes before the first new slot become code * (old /
+ *                    new), rounded (exact but for e4m3's subnormals, both being
+ *                    powers of two).  New codes are y / scale, rounded and
+ *                    saturated.
+ * Nothing else of a page is written.  A page that gets tokens must belong to
+ * one request alone (mm3idx_fork_pages gives a request its own last page).
+ * Inputs must not overlap the caches.
+ */
+int mm3idx_append_kv(const mm3idx_append_t *a, void *stream);
+
+/* One cache of a page pool: page p is the page_bytes bytes from data + p *
+ * page_stride. */
+typedef struct mm3idx_cache {
+    void          *data;           /* device pointer                                        */
+    int64_t        page_stride;    /* bytes, >= page_bytes                                  */
+    int64_t        page_bytes;     /* 1..2^24                                               */
+} mm3idx_cache_t;
+
+/* A pool of pages and the requests' tables in it.  A page belongs to refs[page]
+ * table entries and is free where that is 0.  Host struct of device pointers. */
+typedef struct mm3idx_pool {
+    int32_t       *refs;           /* int32 [num_pages]                                     */
+    int32_t        num_pages;      /* 1..2^30                                               */
+    int32_t        page_size;      /* tokens a page, >= 1 (not used by release without lengths, nor compaction) */
+    int32_t       *page_table;     /* int32 [num_reqs, table_stride], -1: no page           */
+    int64_t        table_stride;   /* >= table_width                                        */
+    int32_t        table_width;    /* columns, >= 0                                         */
+    const int32_t *seq_lens;       /* int32 [num_reqs]                                      */
+    int32_t        num_reqs;       /* 0..2^20                                               */
+} mm3idx_pool_t;
+
+/*
+ * mm3idx_pages_workspace_bytes -- workspace of the calls below that take one,
+ * for a pool of num_pages and forks into at most num_forks requests.  256-byte
+ * aligned; it need not be cleared, and nothing is kept in it between calls.
+ */
+int mm3idx_pages_workspace_bytes(int32_t num_pages, int32_t num_forks, size_t *bytes);
+
+/*
+ * mm3idx_allocate_pages -- pages for new tokens: every entry < 0 among the columns
+ * of request i that hold positions seq_lens[i] - query_len .. seq_lens[i] - 1
+ * (as far as the table is wide) gets a free page, the lowest ones first, in
+ * the order of requests and columns; its reference count becomes 1.  Entries that
+ * name a page stay (a draft that was taken back left it).  With fewer free
+ * pages than entries the last entries get -1 and MM3IDX_DEV_NO_PAGES is set.  A
+ * length beyond the table's width * page_size sets MM3IDX_DEV_SEQ_TOO_LONG.
+ */
+int mm3idx_allocate_pages(const mm3idx_pool_t *p, int32_t query_len, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * mm3idx_release_pages -- one reference less for every page that the table names
+ * (an entry given twice counts twice; entries < 0 are none): all columns, or with
+ * seq_lens the first cdiv(seq_lens[i], page_size).  The table is only read.
+ * Entries >= num_pages set MM3IDX_DEV_BAD_PAGE; a page that has no reference
+ * left stays at 0 and sets MM3IDX_DEV_NOT_HELD.
+ */
+int mm3idx_release_pages(const mm3idx_pool_t *p, void *stream);
+
+/*
+ * mm3idx_fork_pages -- requests continued by others: for k < num_forks, row k of
+ * `out` becomes request i = parents[k]'s pages for seq_lens[i] tokens and
+ * out_lens[k] its length.  Full pages are shared (their counts grow by one); a
+ * last page that is partly filled is copied, in all caches, into a free page
+ * (the lowest ones first, in the order of k), which belongs to the new row
+ * alone.  Columns behind them become -1.  A parent < 0 gives an empty row, one
+ * >= num_reqs too (MM3IDX_DEV_BAD_ROWS).  Without a free page the entry is -1
+ * (MM3IDX_DEV_NO_PAGES).  Entries outside the pool become -1
+ * (MM3IDX_DEV_BAD_PAGE); a length beyond the table is clamped to it
+ * (MM3IDX_DEV_SEQ_TOO_LONG).  What rows of `out` and out_lens held before is
+ * not released.  They must not overlap rows that are parents in this call, nor
+ * anything else that is read; other rows of p->page_table and p->seq_lens they
+ * may be.  num_caches 0..MM3IDX_MAX_CACHES; num_forks 0..2^20.
+ */
+int mm3idx_fork_pages(const mm3idx_pool_t *p, const int32_t *parents, int32_t num_forks,
+                      int32_t *out, int64_t out_stride, int32_t *out_lens,
+                      const mm3idx_cache_t *caches, int32_t num_caches, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * mm3idx_compact_pages -- the pool's L pages that are not free become pages
+ * 0..L-1: the k-th page (by id) of those at L and behind it moves, in all caches,
+ * to the k-th free one before L; pages before L stay.  refs_out and table_out
+ * (which may be p->refs and p->page_table with its stride) get the counts and
+ * the table (all columns; entries that name a free page, or none, stay) as they
+ * then are, *live (an int32 on the device) L.
+ */
+int mm3idx_compact_pages(const mm3idx_pool_t *p, int32_t *refs_out, int32_t *table_out,
+                         int64_t table_out_stride, int32_t *live, const mm3idx_cache_t *caches,
+                         int32_t num_caches, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mm3idx_copy_pages -- page src[k] to page dst[k], k < count, in all caches.  A
+ * pair with an entry < 0 is skipped, one with an entry >= num_pages too
+ * (MM3IDX_DEV_BAD_PAGE).  No dst may be another pair's dst or src.
+ */
+int mm3idx_copy_pages(const mm3idx_cache_t *caches, int32_t num_caches, int32_t num_pages,
+                      const int32_t *src, const int32_t *dst, int32_t count, void *stream);
 
 /*
  * mm3idx_get_device_error -- synchronises `stream`, then reads and clears the

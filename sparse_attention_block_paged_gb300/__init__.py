@@ -26,6 +26,15 @@ and the operators that use the selection in a decode step:
 * :func:`accumulate_weights` -- the attention weight that the blocks have taken
 * :func:`evict_blocks`       -- the lightest blocks out of the cache
 * :func:`verify_drafts`      -- drafted tokens against the target's probabilities
+
+and those of the cache's pages:
+
+* :func:`append_kv`      -- new tokens' keys and values into their pages
+* :func:`allocate_pages` -- pages for them
+* :func:`release_pages`  -- pages given back
+* :func:`fork_pages`     -- requests that go on from another's tokens
+* :func:`compact_pages`  -- the pages in use moved to the front of the pool
+* :func:`copy_pages`     -- pages copied in all caches
 """
 
 from __future__ import annotations
@@ -50,9 +59,10 @@ MAX_TOPK = 32
 MAX_DECODE_ROWS = 32
 STATIC_SCRATCH_BYTES = 8 << 20
 DEV_BAD_PAGE, DEV_SEQ_TOO_LONG, DEV_SEQ_TOO_SHORT, DEV_TIMEOUT, DEV_BAD_ROWS = 1, 2, 4, 8, 16
-DEV_BAD_TOKEN = 32
+DEV_BAD_TOKEN, DEV_NO_PAGES, DEV_NOT_HELD = 32, 64, 128
 MAX_DRAFTS = 31
 MAX_WEIGHT_ENTRIES = 1024
+MAX_CACHES = 64
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 
 
@@ -207,6 +217,79 @@ class Drafts(ctypes.Structure):
     ]
 
 
+class KvScales(ctypes.Structure):
+    """mm3idx_kv_scales_t."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
+class Append(ctypes.Structure):
+    """mm3idx_append_t."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+        ("kv_type", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("k_cache", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_page_token_stride", ctypes.c_int64),
+        ("k_page_head_stride", ctypes.c_int64),
+        ("v_cache", ctypes.c_void_p),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_page_token_stride", ctypes.c_int64),
+        ("v_page_head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("scales", KvScales),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("num_reqs", ctypes.c_int32),
+        ("query_len", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("cu_seqlens_q", ctypes.c_void_p),
+        ("total_q", ctypes.c_int32),
+    ]
+
+
+class Cache(ctypes.Structure):
+    """mm3idx_cache_t."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("page_bytes", ctypes.c_int64),
+    ]
+
+
+class Pool(ctypes.Structure):
+    """mm3idx_pool_t."""
+    _fields_ = [
+        ("refs", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("num_reqs", ctypes.c_int32),
+    ]
+
+
 SYMBOLS = {
     "mm3idx_version": (ctypes.c_int32, []),
     "mm3idx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -273,6 +356,26 @@ SYMBOLS = {
     "mm3idx_evict_blocks": (ctypes.c_int, [ctypes.POINTER(Weights), ctypes.POINTER(EvictionArgs),
                                            ctypes.c_void_p]),
     "mm3idx_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Drafts), ctypes.c_void_p]),
+    "mm3idx_paged_attention_scaled": (ctypes.c_int, [ctypes.POINTER(Attention),
+                                                     ctypes.POINTER(KvScales), ctypes.c_void_p,
+                                                     ctypes.c_size_t, ctypes.c_void_p]),
+    "mm3idx_append_kv": (ctypes.c_int, [ctypes.POINTER(Append), ctypes.c_void_p]),
+    "mm3idx_pages_workspace_bytes": (ctypes.c_int, [ctypes.c_int32] * 2 +
+                                     [ctypes.POINTER(ctypes.c_size_t)]),
+    "mm3idx_allocate_pages": (ctypes.c_int, [ctypes.POINTER(Pool), ctypes.c_int32, ctypes.c_void_p,
+                                             ctypes.c_size_t, ctypes.c_void_p]),
+    "mm3idx_release_pages": (ctypes.c_int, [ctypes.POINTER(Pool), ctypes.c_void_p]),
+    "mm3idx_fork_pages": (ctypes.c_int, [ctypes.POINTER(Pool), ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.POINTER(Cache), ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_void_p]),
+    "mm3idx_compact_pages": (ctypes.c_int, [ctypes.POINTER(Pool), ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.POINTER(Cache),
+                                            ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.c_void_p]),
+    "mm3idx_copy_pages": (ctypes.c_int, [ctypes.POINTER(Cache), ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_void_p]),
 }
 
 
@@ -776,14 +879,17 @@ def new_attention_workspace(q_heads, kv_heads, head_dim, num_reqs, query_len, ma
 
 
 def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max_seq_len,
-                    sm_scale, k_scale=1.0, v_scale=1.0, out=None, lse=None, block_weights=None,
-                    workspace=None, stream=None):
+                    sm_scale, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None, out=None,
+                    lse=None, block_weights=None, workspace=None, stream=None):
     """Attention of ``query_len`` new tokens a request over its paged keys and
     values, causal: q [num_reqs * query_len, q_heads, head_dim] bf16 or fp16,
     caches [pages, page_size, kv_heads, head_dim] of the same type or
     float8_e4m3fn (times ``k_scale`` / ``v_scale``) with any 16-byte strides,
     int32 page table [num_reqs, >= cdiv(max_seq_len, page_size)] and lengths
     (0: an empty slot, its rows become 0).  Returns ``out``, like q.
+
+    ``k_scales`` and ``v_scales``, fp32 [pages, kv_heads]: scales of each page
+    and head of float8_e4m3fn caches, as :func:`append_kv` writes them.
 
     ``lse`` fp32 [rows, q_heads] and ``block_weights`` fp32 [rows,
     cdiv(max_seq_len, 128)] are written when given: the log-sum-exp of each
@@ -796,7 +902,7 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max
     with _HERE if stream is None else _run_on(stream, q):
         return _binding.paged_attention(q, k_cache, v_cache, page_table, seq_lens, query_len,
                                         max_seq_len, sm_scale, k_scale, v_scale, out, lse,
-                                        block_weights, workspace)
+                                        block_weights, workspace, k_scales, v_scales)
 
 
 def accumulate_weights(acc, block_weights, seq_lens, *, query_len, max_seq_len, ids=None,
@@ -863,6 +969,113 @@ def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, dra
     with _HERE if stream is None else _run_on(stream, target_probs):
         return _binding.verify_drafts(target_probs, draft_tokens, uniforms, draft_probs,
                                       draft_lens, out, accepted)
+
+
+# ------------------------------------------------------ a cache's pages
+
+def append_kv(k, v, k_cache, v_cache, page_table, seq_lens, *, query_len, max_seq_len, k_scale=1.0,
+              v_scale=1.0, k_scales=None, v_scales=None, cu_seqlens_q=None, stream=None):
+    """New tokens' keys and values [rows, kv_heads, head_dim], bf16 or fp16, into
+    the caches of :func:`paged_attention`: row j of request i's ``query_len``
+    rows goes to position ``seq_lens[i] - query_len + j`` (the lengths count
+    the new tokens; positions below 0 are dropped).  Ragged batches give
+    ``cu_seqlens_q`` int32 [num_reqs + 1], and ``query_len`` as the most rows
+    of a request.
+
+    Elements are divided by ``k_scale`` / ``v_scale`` and rounded to the caches' type
+    (float8_e4m3fn saturates at 448).  With ``k_scales`` and ``v_scales``, fp32
+    [pages, kv_heads], a page's codes have a power of two as their scale, the least
+    that holds its tokens: a page whose first slot is written starts with the new
+    tokens' scale; in others it only grows, and the older codes follow it.
+
+    Pages that get tokens must not be shared (:func:`fork_pages` copies the
+    one that its new rows go on with)."""
+    with _HERE if stream is None else _run_on(stream, k):
+        _binding.append_kv(k, v, k_cache, v_cache, page_table, seq_lens, query_len, max_seq_len,
+                           k_scale, v_scale, k_scales, v_scales, cu_seqlens_q)
+
+
+def pages_workspace_bytes(num_pages: int, num_forks: int = 0) -> int:
+    size, n = lib.mm3idx_pages_workspace_bytes, ctypes.c_size_t(0)
+    _check(size(num_pages, num_forks, ctypes.byref(n)), "mm3idx_pages_workspace_bytes")
+    return n.value
+
+
+def new_pages_workspace(num_pages, num_forks=0, device=None):
+    """Scratch for :func:`allocate_pages`, :func:`fork_pages` (into up to
+    ``num_forks`` requests) and :func:`compact_pages` of a pool, reusable by
+    calls that follow one another on the GPU."""
+    return torch.empty(pages_workspace_bytes(num_pages, num_forks), dtype=torch.uint8,
+                       device=torch.device(device or "cuda"))
+
+
+def allocate_pages(refs, page_table, seq_lens, *, query_len, page_size, workspace=None,
+                   stream=None):
+    """Pages for new tokens, in place: of the columns that hold positions
+    ``seq_lens - query_len`` .. ``seq_lens - 1`` those without a page (below 0)
+    get a free one, the lowest first.  ``refs`` int32 [num_pages] counts the
+    table entries that name a page; 0: it is free.  Where pages run out entries
+    become -1 (DEV_NO_PAGES in the device status).
+
+    Columns that hold no page must be -1: after :func:`evict_blocks` with
+    ``in_place``, which leaves the columns from its budget on as they were, set
+    them so.  Returns ``page_table``."""
+    with _HERE if stream is None else _run_on(stream, refs):
+        _binding.allocate_pages(refs, page_table, seq_lens, query_len, page_size, workspace)
+    return page_table
+
+
+def release_pages(refs, page_table, *, seq_lens=None, page_size=None, stream=None):
+    """One reference less for every page in ``page_table`` (int32, 2-D; entries
+    below 0 are none): rows of finished requests, or what :func:`evict_blocks`
+    returns as ``freed``.  With ``seq_lens`` and ``page_size`` only the columns that
+    the lengths reach.  The table is left as it is.  Returns ``refs``."""
+    with _HERE if stream is None else _run_on(stream, refs):
+        _binding.release_pages(refs, page_table, seq_lens, page_size)
+    return refs
+
+
+def fork_pages(refs, page_table, seq_lens, parents, caches, *, page_size, out=None, out_lens=None,
+               workspace=None, stream=None):
+    """Requests that go on from others' tokens: row k of the result continues request
+    ``parents[k]`` (int32; below 0: an empty row).  Full pages are shared (their
+    counts in ``refs`` grow), the last page, partly filled, is copied in every one of
+    ``caches`` (up to 64 tensors [num_pages, ...], pages without gaps) into a
+    free one.  Returns (table int32 [forks, columns], lengths int32 [forks]).
+
+    ``out`` / ``out_lens`` may be other rows of ``page_table`` and ``seq_lens``
+    than the parents', e.g. a batch's free slots; what they held is not
+    released."""
+    with _HERE if stream is None else _run_on(stream, refs):
+        return _binding.fork_pages(refs, page_table, seq_lens, parents, caches, page_size, out,
+                                   out_lens, workspace)
+
+
+class Compaction(NamedTuple):
+    """What :func:`compact_pages` leaves: the counts, the table, and how many pages
+    are in use (int32 [1], on the GPU)."""
+    refs: torch.Tensor
+    page_table: torch.Tensor
+    live: torch.Tensor
+
+
+def compact_pages(refs, page_table, caches, *, in_place=False, workspace=None, stream=None):
+    """Moves the L pages in use (``refs`` not 0) into pages 0..L-1, in every one of
+    ``caches`` (up to 64 tensors [num_pages, ...], pages without gaps): the k-th of
+    those from L on goes to the k-th free one before L.  Returns a
+    :class:`Compaction`; ``refs`` and ``page_table`` (all tables of the pool, as
+    rows of one tensor) are left as they are, or with ``in_place`` overwritten."""
+    with _HERE if stream is None else _run_on(stream, refs):
+        return tuple.__new__(Compaction, _binding.compact_pages(refs, page_table, caches, in_place,
+                                                                workspace))
+
+
+def copy_pages(caches, src, dst, *, stream=None):
+    """Page ``src[k]`` to page ``dst[k]`` (int32) in every one of ``caches`` (up to
+    64 tensors [num_pages, ...], pages without gaps).  Pairs with an entry below 0 are
+    skipped; no ``dst`` may be another pair's ``dst`` or ``src``."""
+    with _HERE if stream is None else _run_on(stream, src):
+        _binding.copy_pages(caches, src, dst)
 
 
 def _stream_device(stream):

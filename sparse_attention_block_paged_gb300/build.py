@@ -24,10 +24,11 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmm3idx.so")
 SOURCES = ["api.cu", "decode.cu", "decode_fp4.cu", "prefill.cu", "select.cu", "dequant.cu",
            "sparse_table.cu", "api_serving.cu", "attention.cu", "attention_bf16.cu",
-           "attention_fp16.cu", "attention_bf16_e4m3.cu", "attention_fp16_e4m3.cu", "evict.cu",
-           "verify.cu"]
+           "attention_fp16.cu", "attention_bf16_e4m3.cu", "attention_fp16_e4m3.cu",
+           "attention_bf16_e4m3_scaled.cu", "attention_fp16_e4m3_scaled.cu", "evict.cu",
+           "verify.cu", "api_pages.cu", "append.cu", "pages.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "warp_select.cuh", "decode_common.cuh", "nvfp4.cuh",
-           "serving.h", "attention.cuh"]
+           "serving.h", "attention.cuh", "pages.h"]
 
 BINDING = os.path.join(OUT_DIR, "_binding.so")
 

@@ -693,6 +693,9 @@ const char* mm3idx_status_string(int status) {
       return "eviction needs init >= 0, local >= 1, init + local <= budget and a decay in 0..1";
     case MM3IDX_ERR_VOCAB:
       return "verification needs vocab >= 1, 0..31 drafts and rows that do not overlap";
+    case MM3IDX_ERR_PAGES:
+      return "a page pool needs 1..2^30 pages, page sizes of at least one token, 0..64 caches and pages of 1 byte to 16 MB "
+             "that do not overlap";
     default: return "unknown status";
   }
 }

@@ -85,6 +85,14 @@ int check_attention(const mm3idx_attention_t* a) {
   return MM3IDX_OK;
 }
 
+int check_scales(const mm3idx_kv_scales_t* s) {
+  if (!s || !s->k || !s->v) return MM3IDX_ERR_INVALID_ARGUMENT;
+  if (!aligned4(s->k, s->v) || s->k_page_stride < 0 || s->k_head_stride < 0 ||
+      s->v_page_stride < 0 || s->v_head_stride < 0)
+    return MM3IDX_ERR_ATTENTION_LAYOUT;
+  return MM3IDX_OK;
+}
+
 // Workspace: [a ticket an SM][partial references and sums][partial outputs], for
 // block weights [rows' log-sum-exps][tiles' log-sum-exps], each 256-aligned.
 // Tickets have to be zero when a call starts; they come first and are as many
@@ -136,6 +144,88 @@ int make_cache_map(const mm3idx_attention_t* p, bool values, CUtensorMap* m) {
                          row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MM3IDX_OK : MM3IDX_ERR_ATTENTION_LAYOUT;
+}
+
+// The launch of a checked problem that has requests.
+int attend(const mm3idx_attention_t* p, const mm3idx_kv_scales_t* s, void* workspace,
+           size_t workspace_bytes, void* stream) {
+  int sms = 0;
+  int32_t* status = nullptr;
+  int rc = library_device(&sms, &status);
+  if (rc) return rc;
+  const AttentionWs w = attention_ws(sms, p->q_heads, p->kv_heads, p->head_dim, p->num_reqs,
+                                     p->query_len, p->max_seq_len, p->block_weights != nullptr);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return MM3IDX_ERR_WORKSPACE;
+  AttentionArgs a{};
+  a.q = p->q;
+  a.q_tok = p->q_token_stride;
+  a.q_head = p->q_head_stride;
+  a.kv_heads = p->kv_heads;
+  a.group = p->q_heads / p->kv_heads;
+  a.head_dim = p->head_dim;
+  a.q_type = p->q_type;
+  a.kv_type = p->kv_type;
+  a.num_pages = p->num_pages;
+  a.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.table_width = p->table_width;
+  a.seq_lens = p->seq_lens;
+  a.num_reqs = p->num_reqs;
+  a.query_len = p->query_len;
+  a.max_seq_len = p->max_seq_len;
+  a.scale = p->sm_scale * p->k_scale;
+  a.v_scale = p->v_scale;
+  if (s) {
+    a.k_scales = s->k;
+    a.v_scales = s->v;
+    a.ks_page = s->k_page_stride;
+    a.ks_head = s->k_head_stride;
+    a.vs_page = s->v_page_stride;
+    a.vs_head = s->v_head_stride;
+  }
+  a.out = p->out;
+  a.o_tok = p->out_token_stride;
+  a.o_head = p->out_head_stride;
+  a.lse = p->lse;
+  a.lse_tok = p->lse_token_stride;
+  a.weights = p->block_weights;
+  a.w_stride = p->block_weights_stride;
+  a.w_width = static_cast<int32_t>(cdiv(p->max_seq_len, kBlock));
+  a.status = status;
+  const int rows = a.group * a.query_len;
+  a.row_tiles = static_cast<int32_t>(cdiv(rows, 64));
+  // The most kv heads side by side that leave no more than one SM in 25 idle.
+  a.gang = 1;
+  for (int g = 2; g <= a.kv_heads && g <= sms; ++g)
+    if (a.kv_heads % g == 0 && sms / g * g * 25 >= sms * 24) a.gang = g;
+  a.tasks = a.kv_heads / a.gang * a.row_tiles;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.tickets = reinterpret_cast<unsigned int*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  if (p->block_weights) {
+    a.row_lse = reinterpret_cast<float*>(ws + w.row);
+    a.tile_lse = reinterpret_cast<float*>(ws + w.tile);
+  }
+  CUtensorMap kmap, vmap;
+  if ((rc = make_cache_map(p, false, &kmap)) || (rc = make_cache_map(p, true, &vmap))) return rc;
+  // One CTA an SM; no more than there can be tiles.
+  const int64_t most = static_cast<int64_t>(p->num_reqs) * a.tasks * (cdiv(p->max_seq_len, kBlock) + 2);
+  const int gangs = static_cast<int>(most < sms / a.gang ? most : sms / a.gang);
+  const int grid = gangs * a.gang;
+  const int32_t deal = (a.num_reqs + gangs - 1) / gangs;
+  a.deal = Divisor(deal);
+  a.deal_full = a.num_reqs / deal;
+  a.deal_rest = a.num_reqs % deal;
+  a.by_tasks = Divisor(a.tasks);
+  a.by_row_tiles = Divisor(a.row_tiles);
+  a.by_group = Divisor(a.group);
+  const int64_t list = static_cast<int64_t>(p->num_reqs) * a.tasks *
+                       (cdiv(p->max_seq_len, kBlock) + kTaskCost);
+  a.few = p->num_reqs <= 32 && list <= UINT32_MAX / gangs;
+  return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
 }
 
 int check_weights(const mm3idx_weights_t* w) {
@@ -200,77 +290,18 @@ int mm3idx_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t 
 
 int mm3idx_paged_attention(const mm3idx_attention_t* p, void* workspace, size_t workspace_bytes,
                            void* stream) {
+  const int rc = check_attention(p);
+  return rc || p->num_reqs == 0 ? rc : attend(p, nullptr, workspace, workspace_bytes, stream);
+}
+
+int mm3idx_paged_attention_scaled(const mm3idx_attention_t* p, const mm3idx_kv_scales_t* s,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_attention(p);
   if (rc) return rc;
+  if (p->kv_type != MM3IDX_TYPE_E4M3) return MM3IDX_ERR_ATTENTION_SHAPE;
   if (p->num_reqs == 0) return MM3IDX_OK;
-  int sms = 0;
-  int32_t* status = nullptr;
-  if ((rc = library_device(&sms, &status))) return rc;
-  const AttentionWs w = attention_ws(sms, p->q_heads, p->kv_heads, p->head_dim, p->num_reqs,
-                                     p->query_len, p->max_seq_len, p->block_weights != nullptr);
-  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return MM3IDX_ERR_WORKSPACE;
-  AttentionArgs a{};
-  a.q = p->q;
-  a.q_tok = p->q_token_stride;
-  a.q_head = p->q_head_stride;
-  a.kv_heads = p->kv_heads;
-  a.group = p->q_heads / p->kv_heads;
-  a.head_dim = p->head_dim;
-  a.q_type = p->q_type;
-  a.kv_type = p->kv_type;
-  a.num_pages = p->num_pages;
-  a.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
-  a.table = p->page_table;
-  a.table_stride = p->table_stride;
-  a.table_width = p->table_width;
-  a.seq_lens = p->seq_lens;
-  a.num_reqs = p->num_reqs;
-  a.query_len = p->query_len;
-  a.max_seq_len = p->max_seq_len;
-  a.scale = p->sm_scale * p->k_scale;
-  a.v_scale = p->v_scale;
-  a.out = p->out;
-  a.o_tok = p->out_token_stride;
-  a.o_head = p->out_head_stride;
-  a.lse = p->lse;
-  a.lse_tok = p->lse_token_stride;
-  a.weights = p->block_weights;
-  a.w_stride = p->block_weights_stride;
-  a.w_width = static_cast<int32_t>(cdiv(p->max_seq_len, kBlock));
-  a.status = status;
-  const int rows = a.group * a.query_len;
-  a.row_tiles = static_cast<int32_t>(cdiv(rows, 64));
-  // The most kv heads side by side that leave no more than one SM in 25 idle.
-  a.gang = 1;
-  for (int g = 2; g <= a.kv_heads && g <= sms; ++g)
-    if (a.kv_heads % g == 0 && sms / g * g * 25 >= sms * 24) a.gang = g;
-  a.tasks = a.kv_heads / a.gang * a.row_tiles;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.tickets = reinterpret_cast<unsigned int*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
-  if (p->block_weights) {
-    a.row_lse = reinterpret_cast<float*>(ws + w.row);
-    a.tile_lse = reinterpret_cast<float*>(ws + w.tile);
-  }
-  CUtensorMap kmap, vmap;
-  if ((rc = make_cache_map(p, false, &kmap)) || (rc = make_cache_map(p, true, &vmap))) return rc;
-  // One CTA an SM; no more than there can be tiles.
-  const int64_t most = static_cast<int64_t>(p->num_reqs) * a.tasks * (cdiv(p->max_seq_len, kBlock) + 2);
-  const int gangs = static_cast<int>(most < sms / a.gang ? most : sms / a.gang);
-  const int grid = gangs * a.gang;
-  const int32_t deal = (a.num_reqs + gangs - 1) / gangs;
-  a.deal = Divisor(deal);
-  a.deal_full = a.num_reqs / deal;
-  a.deal_rest = a.num_reqs % deal;
-  a.by_tasks = Divisor(a.tasks);
-  a.by_row_tiles = Divisor(a.row_tiles);
-  a.by_group = Divisor(a.group);
-  const int64_t list = static_cast<int64_t>(p->num_reqs) * a.tasks *
-                       (cdiv(p->max_seq_len, kBlock) + kTaskCost);
-  a.few = p->num_reqs <= 32 && list <= UINT32_MAX / gangs;
-  return cuda_status(launch_attention(kmap, vmap, a, grid, static_cast<cudaStream_t>(stream)));
+  if ((rc = check_scales(s))) return rc;
+  return attend(p, s, workspace, workspace_bytes, stream);
 }
 
 int mm3idx_accumulate_weights(const mm3idx_weights_t* w, void* stream) {

@@ -1,0 +1,273 @@
+// append.cu -- new tokens' keys and values into their requests' pages
+// (include/mm3idx.h, mm3idx_append_kv).
+//
+// Mathematics.  y = x / k_scale.  With a scale a page and head: A = max |y| of the
+// page's finite new elements, need = the least power of two with A / need <= 448;
+// the scale S is need in a page that starts with them, else max(need, old S).
+// Codes are y / S to the nearest e4m3.  A power of two costs no precision (e4m3
+// is a floating type) but at most one of its 18 binades, and makes growing
+// exact: older codes times old / new only move their exponents, until they
+// meet e4m3's subnormals.
+//
+// What bounds it.  2 bytes read and 1 (2) written an element: HBM for prompts,
+// for a decode step a chain of dependent loads (length, page, old scale).  So a
+// (page, head) of the keys or of the values is one group of threads' that holds
+// its new elements in registers between the maximum and the rounding: one pass
+// over the data, nothing exchanged between CTAs.  A group is as large as the
+// page's new tokens need at 8 pieces of 16 bytes a thread: a warp for up to 16
+// tokens of 128 elements, a CTA for a whole page of 128.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pages.h"
+
+namespace mm3idx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 8;              // of 16 bytes, a thread
+constexpr float kLowScale = 0x1p-60f, kHighScale = 0x1p60f;
+
+template <bool BF16>
+__device__ __forceinline__ float2 floats(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t halves(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four floats as e4m3, to the nearest, saturated at 448 (infinities too); NaN
+// stays NaN.
+__device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ float2 widen(uint16_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The least power of two, in the scales' range, that brings `top` to 448 or
+// less: 448 = 1.75 2^8, so it is the exponent of top less 8, or less 7 where its
+// fraction is above 1.75.
+__device__ __forceinline__ float least_scale(float top) {
+  const uint32_t bits = __float_as_uint(top);
+  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, 127 - 60), 127 + 60)) << 23);
+}
+
+// Division by a number: a product with its reciprocal where that is exact.
+struct By {
+  float d, inv;
+  bool exact;
+  __device__ __forceinline__ float operator()(float x) const { return exact ? x * inv : x / d; }
+};
+
+__device__ __forceinline__ By division(float x) {
+  return By{x, 1.0f / x, (__float_as_uint(x) & 0x7fffffu) == 0};
+}
+
+enum { kCopy = 0, kCodes = 1, kScaled = 2 };
+
+// BF16: type of the new elements.  MODE: a cache of that type, of e4m3, or of e4m3
+// with scales.  G: threads a (page, head).
+template <bool BF16, int MODE, int G>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float tops[kThreads / 32];
+  const int unit = static_cast<int>(blockIdx.x) * (kThreads / G) + static_cast<int>(threadIdx.x) / G;
+  const int t = threadIdx.x % G;
+  // unit = ((request * touched + page) * 2 + side) * kv_heads + head: neighbours
+  // read neighbouring heads of the same tokens
+  const int outer = a.by_heads.quotient(min(unit, a.units - 1));
+  const int head = unit - outer * a.kv_heads, which = outer & 1;
+  const int req = a.by_touched.quotient(outer >> 1), turn = (outer >> 1) - req * a.touched;
+  const AppendSide& side = a.side[which];
+  const int size = 1 << a.page_shift;
+
+  // The page's new slots [from, to) and the row of the first of them.
+  int from = 0, to = 0, page = -1;
+  int64_t row = 0;
+  if (unit < a.units) {
+    const int raw = __ldg(a.seq_lens + req);
+    const int len = min(max(raw, 0), a.max_seq_len);
+    int rows = a.query_len, bits = raw > a.max_seq_len ? MM3IDX_DEV_SEQ_TOO_LONG : 0;
+    int64_t row0 = static_cast<int64_t>(req) * a.query_len;
+    if (a.cu) {
+      const int c0 = __ldg(a.cu + req), c1 = __ldg(a.cu + req + 1);
+      const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total_q && c1 - c0 <= a.query_len;
+      if (!ok || (req == 0 && c0 != 0) || (req == a.num_reqs - 1 && c1 != a.total_q))
+        bits |= MM3IDX_DEV_BAD_ROWS;
+      rows = ok ? c1 - c0 : 0;
+      row0 = c0;
+    }
+    const int begin = max(len - rows, 0);               // first new position
+    const int p = (begin >> a.page_shift) + turn;       // page of the request
+    const int lo = max(begin, p << a.page_shift), hi = min(len, (p + 1) << a.page_shift);
+    if (lo < hi) {
+      page = __ldg(a.table + req * a.table_stride + p);
+      if (page < 0 || page >= a.num_pages) {
+        bits |= MM3IDX_DEV_BAD_PAGE;
+      } else {
+        from = lo & (size - 1);
+        to = from + hi - lo;
+        row = row0 + (lo - (len - rows));
+      }
+    }
+    if (bits && t == 0 && head == 0 && which == 0) atomicOr(a.status, bits);
+  }
+
+  const int shift = a.head_dim == 128 ? 4 : 3;           // pieces of a row, log2
+  const int pieces = (to - from) << shift;
+  const uint16_t* x = side.x + row * side.x_tok + head * side.x_head;
+  uint4 v[kPieces];
+#pragma unroll
+  for (int m = 0; m < kPieces; ++m) {
+    const int k = t + m * G;
+    if (k < pieces)
+      v[m] = __ldg(reinterpret_cast<const uint4*>(x + (k >> shift) * side.x_tok) +
+                   (k & ((1 << shift) - 1)));
+    else
+      v[m] = make_uint4(0, 0, 0, 0);
+  }
+  const bool plain = side.scale == 1.0f;
+  const By by = division(side.scale);
+  uint8_t* base = side.cache + page * side.c_page + head * side.c_head;
+  if constexpr (MODE == kCopy) {
+#pragma unroll
+    for (int m = 0; m < kPieces; ++m) {
+      const int k = t + m * G;
+      if (k >= pieces) continue;
+      uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+      if (!plain)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = floats<BF16>(w[e]);
+          w[e] = halves<BF16>(by(f.x), by(f.y));
+        }
+      *reinterpret_cast<uint4*>(base + (from + (k >> shift)) * side.c_tok +
+                                (k & ((1 << shift) - 1)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
+  float scale = 1.0f;
+  if constexpr (MODE == kScaled) {
+    float* at = side.scales + page * side.s_page + head * side.s_head;
+    const float old = from > 0 ? fminf(fmaxf(*at, kLowScale), kHighScale) : 0.0f;
+    // The largest magnitude (a maximum passes over NaN); where that is infinite,
+    // once more without the infinities.
+    auto largest = [&](bool finite) {
+      float top = 0.0f;
+#pragma unroll
+      for (int m = 0; m < kPieces; ++m) {
+        const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 f = floats<BF16>(w[e]);
+          if (!plain) f = make_float2(by(f.x), by(f.y));
+          f = make_float2(fabsf(f.x), fabsf(f.y));
+          if (finite) f = make_float2(f.x < INFINITY ? f.x : 0.0f, f.y < INFINITY ? f.y : 0.0f);
+          top = fmaxf(top, fmaxf(f.x, f.y));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if constexpr (G > 32) {
+        __syncthreads();               // (the last use of tops)
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < G / 32; ++k)
+          top = fmaxf(top, tops[(threadIdx.x / G) * (G / 32) + k]);
+      }
+      return top;
+    };
+    float top = largest(false);
+    bool again = top == INFINITY;
+    if constexpr (G > 32) again = __syncthreads_or(again);
+    if (again) {
+      const float without = largest(true);
+      if (top == INFINITY) top = without;
+    }
+    scale = fmaxf(least_scale(top), old);
+    __syncwarp();                      // every lane has the old scale (larger groups met above)
+    if (pieces > 0) {
+      if (from > 0 && scale != old) {
+        // the older tokens' codes, 16 of them a piece
+        const float f = old / scale;
+        for (int k = t; k < from << (shift - 1); k += G) {
+          uint4* c = reinterpret_cast<uint4*>(base + (k >> (shift - 1)) * side.c_tok) +
+                     (k & ((1 << (shift - 1)) - 1));
+          uint4 q = *c;
+          uint32_t* w = &q.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 l = widen(static_cast<uint16_t>(w[e])), h = widen(static_cast<uint16_t>(w[e] >> 16));
+            w[e] = codes(l.x * f, l.y * f, h.x * f, h.y * f);
+          }
+          *c = q;
+        }
+      }
+      if (t == 0) *at = scale;
+    }
+  }
+  const By to_codes = division(scale);
+#pragma unroll
+  for (int m = 0; m < kPieces; ++m) {
+    const int k = t + m * G;
+    if (k >= pieces) continue;
+    const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float2 y = floats<BF16>(w[e]);
+      if (!plain) y = make_float2(by(y.x), by(y.y));
+      f[2 * e] = MODE == kScaled ? to_codes(y.x) : y.x;
+      f[2 * e + 1] = MODE == kScaled ? to_codes(y.y) : y.y;
+    }
+    *reinterpret_cast<uint2*>(base + (from + (k >> shift)) * side.c_tok +
+                              (k & ((1 << shift) - 1)) * 8) =
+        make_uint2(codes(f[0], f[1], f[2], f[3]), codes(f[4], f[5], f[6], f[7]));
+  }
+}
+
+template <bool BF16, int MODE>
+cudaError_t launch_mode(const AppendArgs& a, cudaStream_t s) {
+  const int g = append_threads(a.query_len, 1 << a.page_shift, a.head_dim);
+  const int per = kThreads / g;
+  const dim3 grid((a.units - 1) / per + 1);
+  if (g == 32) return launch_dependent(append_kernel<BF16, MODE, 32>, grid, kThreads, 1, a, s);
+  if (g == 64) return launch_dependent(append_kernel<BF16, MODE, 64>, grid, kThreads, 1, a, s);
+  if (g == 128) return launch_dependent(append_kernel<BF16, MODE, 128>, grid, kThreads, 1, a, s);
+  return launch_dependent(append_kernel<BF16, MODE, 256>, grid, kThreads, 1, a, s);
+}
+
+template <bool BF16>
+cudaError_t launch_type(const AppendArgs& a, cudaStream_t s) {
+  if (a.kv_type != MM3IDX_TYPE_E4M3) return launch_mode<BF16, kCopy>(a, s);
+  if (a.side[0].scales) return launch_mode<BF16, kScaled>(a, s);
+  return launch_mode<BF16, kCodes>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+  return a.type == MM3IDX_TYPE_BF16 ? launch_type<true>(a, s) : launch_type<false>(a, s);
+}
+
+}  // namespace mm3idx

@@ -52,6 +52,9 @@ cudaError_t launch_attention(const CUtensorMap& kmap, const CUtensorMap& vmap,
   cudaError_t e;
   if (a.kv_type == MM3IDX_TYPE_BF16) e = launch_attention_bf16(kmap, vmap, a, grid, s);
   else if (a.kv_type == MM3IDX_TYPE_FP16) e = launch_attention_fp16(kmap, vmap, a, grid, s);
+  else if (a.k_scales) e = a.q_type == MM3IDX_TYPE_BF16
+                               ? launch_attention_bf16_e4m3_scaled(kmap, vmap, a, grid, s)
+                               : launch_attention_fp16_e4m3_scaled(kmap, vmap, a, grid, s);
   else if (a.q_type == MM3IDX_TYPE_BF16) e = launch_attention_bf16_e4m3(kmap, vmap, a, grid, s);
   else e = launch_attention_fp16_e4m3(kmap, vmap, a, grid, s);
   if (e != cudaSuccess || !a.weights) return e;

@@ -95,10 +95,13 @@ constexpr int kTile = kBlock;                    // tokens of a tile
 constexpr int kRedStride = 40;                   // floats of a 32-column row in the join buffer
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowScale = 0x1p-60f, kHighScale = 0x1p60f;   // of pages
 
-template <int KV, int D>
+// SC: e4m3 pages with a scale for each page and kv head.
+template <int KV, int D, bool SC>
 struct Cfg {
   static constexpr bool kByte = KV == MM3IDX_TYPE_E4M3;
+  static_assert(kByte || !SC, "scales belong to e4m3 pages");
   static constexpr int kElem = kByte ? 1 : 2;
   static constexpr int kRow = D * kElem > 128 ? 128 : D * kElem;  // bytes of a row in a copy
   static constexpr int kHalves = D * kElem / kRow;                // copies of a page
@@ -117,7 +120,9 @@ struct Cfg {
   static constexpr int oBar = oSlice + kSlots / 2 * kConsumers * 16 * 4;
   static constexpr int oMask = oBar + 3 * kBars * 8;
   static constexpr int oMisc = oMask + kSlots * 4;
-  static constexpr int kSmem = oMisc + 128 + 1024;
+  static constexpr int oScale = oMisc + 128;       // [tile of the ring][page of a tile]
+  static constexpr int kPages = kTile / 16;        // most pages of a tile
+  static constexpr int kSmem = oScale + (SC ? kSlots / 2 * kPages * 16 : 0) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -484,9 +489,68 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
   return r;
 }
 
+// The factor of a slice's scores: a row's by its page's scale, finite and normal
+// (see the queries' scaling).
+__device__ __forceinline__ float factor(float row, float page) {
+  return fminf(fmaxf(row * page, FLT_MIN), FLT_MAX);
+}
+
 // The halves of a pair (tokens t and t + 1) that lie below `end`.
 __device__ __forceinline__ uint32_t below(int t, int end) {
   return (t < end ? 0x0000ffffu : 0u) | (t + 1 < end ? 0xffff0000u : 0u);
+}
+
+// The scales of the ring's tiles, by a warp of its own: they hang on the page
+// table, and that chain of two loads would hold up the copies' issue.  A lane
+// has one of 32 pages; the next 32 are under way meanwhile.  A page outside
+// the cache, or behind the last token, has scales of 1.
+template <class C, int NB>
+__device__ __forceinline__ void load_scales(const AttentionArgs& a, Walker walk, float4* scales,
+                                            uint64_t* full, uint64_t* empty,
+                                            volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const int per = kTile >> a.page_shift, batch = 32 / per;   // pages of a tile; tiles of 32 pages
+  uint32_t tile = 0, bar = 0, items = 0, wait = 0, wait_phase = 0;
+  Segment sg;
+  while (walk.next(a, sg)) {
+    const int32_t* table = a.table + static_cast<int64_t>(sg.req) * a.table_stride;
+    const int pages = (sg.len + (1 << a.page_shift) - 1) >> a.page_shift;
+    const float* ks = a.k_scales + sg.head * a.ks_head;
+    const float* vs = a.v_scales + sg.head * a.vs_head;
+    auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
+    auto both_of = [&](int id) {
+      if (id < 0 || id >= a.num_pages) return make_float2(1.0f, 1.0f);
+      return make_float2(__ldg(ks + id * a.ks_page), __ldg(vs + id * a.vs_page));
+    };
+    int ids = ids_from(sg.b0 * per + 32), k = 0;
+    float2 now = both_of(ids_from(sg.b0 * per)), next = make_float2(1.0f, 1.0f);
+    for (int b = sg.b0; b < sg.b1; ++b, ++k) {
+      if (k == batch) {
+        k = 0;
+        now = next;
+        ids = ids_from(b * per + 32);
+      }
+      if (k == batch / 2) next = both_of(ids);
+      // (the scale of a value, then its logarithm, are exact for powers of two)
+      const float v = fminf(fmaxf(now.y, kLowScale), kHighScale);
+      const float4 x = make_float4(fminf(fmaxf(now.x, kLowScale), kHighScale), lg2(v), 1.0f / v, 0.0f);
+      if (items >= C::kSlots / 2) {
+        if (!warp_wait(&empty[wait], wait_phase, abort_flag)) return;
+        wait += 2;
+        if (wait >= NB) {
+          wait = 0;
+          wait_phase ^= 1;
+        }
+      }
+      if (lane / per == k) scales[tile * C::kPages + lane % per] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[bar]);
+      ++items;
+      if (++tile == C::kSlots / 2) tile = 0;
+      bar += 2;
+      if (bar >= NB) bar = 0;
+    }
+  }
 }
 
 // ------------------------------------------------------------------- kernel
@@ -499,18 +563,26 @@ __device__ __forceinline__ uint32_t below(int t, int end) {
 // of output tile 4 t + i is d = 32 t + 4 n + i, so that a thread loads four
 // neighbouring bytes of a value row.
 
-template <int KV, int D>
+template <int D>
 struct State {
   float o[D / 8][4];
   float m0, m1, l0, l1;
 };
 
+// Scales of pages.  A slice of 16 tokens lies in one page, so a slice has one
+// pair (ks, vs).  ks joins the factor of the slice's scores.  vs joins the
+// exponent: the weights of the second product are 2^(x + log2 vs - m), m the
+// reference of x + log2 vs, so that they have the range and the precision that
+// weights without scales have, whatever the pages' scales are; their sum l
+// takes each slice's by 1 / vs.  (m, l, o) then mean what they always do, and
+// the joins are the same.
+//
 // Q: type of the queries and the output.  KV: of the cache, Q or e4m3.
-template <int Q, int KV, int D, int RT>
+template <int Q, int KV, int D, int RT, bool SC>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const AttentionArgs a) {
-  using C = Cfg<KV, D>;
+  using C = Cfg<KV, D, SC>;
   constexpr int S = C::kSlots, NB = C::kBars;       // data slots; barriers (a multiple of them)
   constexpr bool kByte = C::kByte;
   constexpr bool kBf = KV == MM3IDX_TYPE_BF16;      // bf16 products (else fp16)
@@ -540,13 +612,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = empty + NB;                             // values' barriers: the tile's weights are there
   uint32_t* mask = reinterpret_cast<uint32_t*>(sm + C::oMask);
   Misc* misc = reinterpret_cast<Misc*>(sm + C::oMisc);
+  // ks, log2 vs and 1 / vs of a tile's pages; the keys' barriers guard them
+  float4* scales = reinterpret_cast<float4*>(sm + C::oScale);
   volatile int* abort_flag = &misc->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool weigh = a.tile_lse != nullptr;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NB; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], SC && !(s & 1) ? 2 : 1);   // (the keys': and the scales)
       mbar_init(&empty[s], kConsumers / ALT + ((s & 1) && weigh ? 1 : 0));
       mbar_init(&done[s], kConsumers / ALT);
     }
@@ -679,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kSpare) {
+      if constexpr (SC) load_scales<C, NB>(a, walk, scales, full, empty, abort_flag);
       // ------------------------------------------- rows of empty requests
       // (a request's rows dealt out to the CTAs where there are fewer requests:
       // one CTA takes seconds for 2^20 rows of 128 heads)
@@ -708,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c = lane & 3, g = lane >> 2;
     const int rt = warp % RT, tj = warp / RT, tg = tj % TG, alt = tj / TG;
     const uint32_t ring = smem_u32(sm);
-    State<KV, D> st;
+    State<D> st;
     uint32_t slot = 0, bar = 0, phase = 0, turn = 0;
     bool dead = false;       // a wait gave up: go through the motions to the end
     // Weights as pairs.  (Known to the compiler: the second numbers' registers and
@@ -899,6 +974,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        float4 psc[NS];          // of each slice's page
+        if constexpr (SC) {
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            psc[n] = scales[(slot >> 1) * C::kPages + ((first + n * 16) >> a.page_shift)];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[bar]);
         ++slot;      // the values' (both counts are even)
@@ -922,15 +1003,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         float top_a = -INFINITY, top_b = -INFINITY;
+        if constexpr (SC) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            top_a = max3(top_a, s[n][x][0], s[n][x][1]);
-            top_b = max3(top_b, s[n][x][2], s[n][x][3]);
+          for (int n = 0; n < NS; ++n) {
+            const float va = max3(fmaxf(s[n][0][0], s[n][0][1]), s[n][1][0], s[n][1][1]);
+            const float vb = max3(fmaxf(s[n][0][2], s[n][0][3]), s[n][1][2], s[n][1][3]);
+            top_a = fmaxf(top_a, fmaf(va, factor(sc_a, psc[n].x), psc[n].y));
+            top_b = fmaxf(top_b, fmaf(vb, factor(sc_b, psc[n].x), psc[n].y));
           }
-        top_a *= sc_a;
-        top_b *= sc_b;
+        } else {
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              top_a = max3(top_a, s[n][x][0], s[n][x][1]);
+              top_b = max3(top_b, s[n][x][2], s[n][x][3]);
+            }
+          top_a *= sc_a;
+          top_b *= sc_b;
+        }
         if (__any_sync(0xffffffffu, top_a > st.m0 + kHead + kRaise || top_b > st.m1 + kHead + kRaise)) {
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
@@ -957,15 +1048,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t p[NS][4], pr[NS][4];
         float sum_a = 0.0f, sum_b = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int n = 0; n < NS; ++n) {
+          // factor and offset of the exponents, the slice's sums
+          const float fa = SC ? factor(sc_a, psc[n].x) : sc_a, fb = SC ? factor(sc_b, psc[n].x) : sc_b;
+          const float oa = SC ? psc[n].y - ref_a : -ref_a, ob = SC ? psc[n].y - ref_b : -ref_b;
+          float part_a = 0.0f, part_b = 0.0f;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float w0 = ex2(fmaf(s[n][x][0], sc_a, -ref_a));
-            const float w1 = ex2(fmaf(s[n][x][1], sc_a, -ref_a));
-            const float w2 = ex2(fmaf(s[n][x][2], sc_b, -ref_b));
-            const float w3 = ex2(fmaf(s[n][x][3], sc_b, -ref_b));
-            sum_a += w0 + w1;
-            sum_b += w2 + w3;
+            const float w0 = ex2(fmaf(s[n][x][0], fa, oa));
+            const float w1 = ex2(fmaf(s[n][x][1], fa, oa));
+            const float w2 = ex2(fmaf(s[n][x][2], fb, ob));
+            const float w3 = ex2(fmaf(s[n][x][3], fb, ob));
+            if constexpr (SC) {
+              part_a += w0 + w1;
+              part_b += w2 + w3;
+            } else {
+              sum_a += w0 + w1;
+              sum_b += w2 + w3;
+            }
             p[n][2 * x] = pack2<kBf>(w0, w1);
             p[n][2 * x + 1] = pack2<kBf>(w2, w3);
             if (rest) {
@@ -973,6 +1073,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               pr[n][2 * x + 1] = pack2_rest<kBf>(w2, w3, p[n][2 * x + 1]);
             }
           }
+          if constexpr (SC) {
+            sum_a = fmaf(part_a, psc[n].z, sum_a);
+            sum_b = fmaf(part_b, psc[n].z, sum_b);
+          }
+        }
         st.l0 += sum_a;
         st.l1 += sum_b;
 
@@ -1338,19 +1443,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && misc->abort) atomicOr(a.status, MM3IDX_DEV_TIMEOUT);
 }
 
-template <int Q, int KV, int D, int RT>
+template <int Q, int KV, int D, int RT, bool SC>
 cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                       int grid, cudaStream_t s) {
-  using C = Cfg<KV, D>;
+  using C = Cfg<KV, D, SC>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {
     // The register split waits for what the launch does not have: never
     // launch a build that got fewer.
     cudaFuncAttributes at;
-    const cudaError_t err = cudaFuncGetAttributes(&at, attention_kernel<Q, KV, D, RT>);
+    const cudaError_t err = cudaFuncGetAttributes(&at, attention_kernel<Q, KV, D, RT, SC>);
     if (err != cudaSuccess) return err;
     if (at.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(attention_kernel<Q, KV, D, RT>,
+    return cudaFuncSetAttribute(attention_kernel<Q, KV, D, RT, SC>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
@@ -1364,23 +1469,23 @@ cudaError_t launch_rt(const CUtensorMap& kmap, const CUtensorMap& vmap, const At
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel<Q, KV, D, RT>, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, attention_kernel<Q, KV, D, RT, SC>, kmap, vmap, a);
 }
 
-template <int Q, int KV, int D>
+template <int Q, int KV, int D, bool SC>
 cudaError_t launch_d(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                      int grid, cudaStream_t s) {
   const int tiles = attention_row_tiles16(a.group * a.query_len);
-  if (tiles == 1) return launch_rt<Q, KV, D, 1>(kmap, vmap, a, grid, s);
-  if (tiles == 2) return launch_rt<Q, KV, D, 2>(kmap, vmap, a, grid, s);
-  return launch_rt<Q, KV, D, 4>(kmap, vmap, a, grid, s);
+  if (tiles == 1) return launch_rt<Q, KV, D, 1, SC>(kmap, vmap, a, grid, s);
+  if (tiles == 2) return launch_rt<Q, KV, D, 2, SC>(kmap, vmap, a, grid, s);
+  return launch_rt<Q, KV, D, 4, SC>(kmap, vmap, a, grid, s);
 }
 
-template <int Q, int KV>
+template <int Q, int KV, bool SC = false>
 cudaError_t launch_kv(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttentionArgs& a,
                       int grid, cudaStream_t s) {
-  return a.head_dim == 128 ? launch_d<Q, KV, 128>(kmap, vmap, a, grid, s)
-                           : launch_d<Q, KV, 64>(kmap, vmap, a, grid, s);
+  return a.head_dim == 128 ? launch_d<Q, KV, 128, SC>(kmap, vmap, a, grid, s)
+                           : launch_d<Q, KV, 64, SC>(kmap, vmap, a, grid, s);
 }
 
 }  // namespace attn

@@ -138,6 +138,21 @@ int32_t type_of(at::ScalarType t) {
          : t == at::kFloat ? MM3IDX_TYPE_FP32 : MM3IDX_TYPE_E4M3;
 }
 
+// Scales of an e4m3 cache's pages: none, or both.
+bool scales_of(PyObject* ko, PyObject* vo, const at::Tensor& cache, mm3idx_kv_scales_t* out) {
+  const at::Tensor *k = maybe(ko, "k_scales"), *v = maybe(vo, "v_scales");
+  if (!k && !v) return false;
+  need(k && v && cache.scalar_type() == at::kFloat8_e4m3fn,
+       "k_scales and v_scales go together, with float8_e4m3fn caches");
+  for (const at::Tensor* t : {k, v})
+    need(is(*t, at::kFloat, 2) && t->size(0) == cache.size(0) && t->size(1) == cache.size(2) &&
+             t->device() == cache.device(),
+         "k_scales and v_scales must be fp32 [pages, kv_heads] on the caches' GPU");
+  *out = mm3idx_kv_scales_t{static_cast<float*>(k->data_ptr()), k->stride(0), k->stride(1),
+                            static_cast<float*>(v->data_ptr()), v->stride(0), v->stride(1)};
+  return true;
+}
+
 PyObject* paged_attention(PyObject* const* args) {
   const at::Tensor &q = tensor(args[0], "q"), &k = tensor(args[1], "k_cache"),
                    &v = tensor(args[2], "v_cache"), &table = tensor(args[3], "page_table"),
@@ -229,8 +244,14 @@ PyObject* paged_attention(PyObject* const* args) {
     need(workspace.device() == q.device() && workspace.is_contiguous(),
          "workspace must be a contiguous tensor on the inputs' GPU");
   }
-  check(mm3idx_paged_attention(&a, workspace.data_ptr(), workspace.nbytes(), stream_of(q)),
-        "mm3idx_paged_attention");
+  mm3idx_kv_scales_t scales{};
+  if (scales_of(args[14], args[15], k, &scales))
+    check(mm3idx_paged_attention_scaled(&a, &scales, workspace.data_ptr(), workspace.nbytes(),
+                                        stream_of(q)),
+          "mm3idx_paged_attention_scaled");
+  else
+    check(mm3idx_paged_attention(&a, workspace.data_ptr(), workspace.nbytes(), stream_of(q)),
+          "mm3idx_paged_attention");
   return THPVariable_Wrap(std::move(out));
 }
 
@@ -429,6 +450,261 @@ PyObject* verify_drafts(PyObject* const* args) {
   return result;
 }
 
+PyObject* append_kv(PyObject* const* args) {
+  const at::Tensor &k = tensor(args[0], "k"), &v = tensor(args[1], "v"),
+                   &kc = tensor(args[2], "k_cache"), &vc = tensor(args[3], "v_cache"),
+                   &table = tensor(args[4], "page_table"), &lens = tensor(args[5], "seq_lens");
+  const int32_t query_len = integer(args[6]), max_seq_len = integer(args[7]);
+  const at::Tensor* cu = maybe(args[12], "cu_seqlens_q");
+  const at::ScalarType type = k.scalar_type(), kv = kc.scalar_type();
+  need(k.dim() == 3 && (type == at::kBFloat16 || type == at::kHalf) && v.scalar_type() == type &&
+           k.sizes() == v.sizes() && unit_inner(k) && unit_inner(v),
+       "new keys and values must be bf16 or fp16 [tokens, kv_heads, head_dim] with contiguous "
+       "head_dim");
+  const int64_t rows = k.size(0), heads = k.size(1), dim = k.size(2);
+  need(kc.dim() == 4 && kc.sizes() == vc.sizes() && kv == vc.scalar_type() &&
+           (kv == type || kv == at::kFloat8_e4m3fn) && kc.size(2) == heads && kc.size(3) == dim &&
+           unit_inner(kc) && unit_inner(vc),
+       "caches must be [pages, page_size, kv_heads, head_dim] with contiguous head_dim, of the new "
+       "tokens' type or float8_e4m3fn");
+  need(is(table, at::kInt, 2) && unit_inner(table) && is(lens, at::kInt, 1) && lens.is_contiguous(),
+       "page table and lengths must be int32 with unit stride");
+  same_gpu(k, {&v, &kc, &vc, &table, &lens, cu});
+  const int64_t reqs = lens.size(0);
+  need(table.size(0) == reqs, "the page table must have one row per request");
+  need(!cu || (is(*cu, at::kInt, 1) && cu->size(0) == reqs + 1 && cu->is_contiguous()),
+       "cu_seqlens_q must be contiguous int32 [num_reqs + 1]");
+  need(cu ? rows <= reqs * query_len : rows == reqs * query_len,
+       cu ? "more new tokens than num_reqs * query_len"
+          : "new keys and values must have batch * query_len rows");
+  const int64_t pages = kc.size(0), size = kc.size(1);
+  need(pages <= INT32_MAX, "more pages than 32 bits count");
+  const c10::cuda::CUDAGuard guard(k.device());
+  mm3idx_append_t a{};
+  a.k = k.data_ptr();
+  a.k_token_stride = rows > 1 ? k.stride(0) : heads * dim;
+  a.k_head_stride = heads > 1 ? k.stride(1) : dim;
+  a.v = v.data_ptr();
+  a.v_token_stride = rows > 1 ? v.stride(0) : heads * dim;
+  a.v_head_stride = heads > 1 ? v.stride(1) : dim;
+  a.type = type_of(type);
+  a.kv_type = type_of(kv);
+  a.kv_heads = static_cast<int32_t>(heads);
+  a.head_dim = static_cast<int32_t>(dim);
+  a.k_cache = kc.data_ptr();
+  a.k_page_stride = pages > 1 ? kc.stride(0) : size * heads * dim;
+  a.k_page_token_stride = size > 1 ? kc.stride(1) : heads * dim;
+  a.k_page_head_stride = heads > 1 ? kc.stride(2) : dim;
+  a.v_cache = vc.data_ptr();
+  a.v_page_stride = pages > 1 ? vc.stride(0) : size * heads * dim;
+  a.v_page_token_stride = size > 1 ? vc.stride(1) : heads * dim;
+  a.v_page_head_stride = heads > 1 ? vc.stride(2) : dim;
+  a.k_scale = static_cast<float>(number(args[8]));
+  a.v_scale = static_cast<float>(number(args[9]));
+  scales_of(args[10], args[11], kc, &a.scales);
+  a.num_pages = static_cast<int32_t>(pages);
+  a.page_size = static_cast<int32_t>(size);
+  a.page_table = static_cast<const int32_t*>(table.data_ptr());
+  a.table_stride = row_stride(table);
+  a.table_width = static_cast<int32_t>(table.size(1));
+  a.seq_lens = static_cast<const int32_t*>(lens.data_ptr());
+  a.num_reqs = static_cast<int32_t>(reqs);
+  a.query_len = query_len;
+  a.max_seq_len = max_seq_len;
+  a.cu_seqlens_q = cu ? static_cast<const int32_t*>(cu->data_ptr()) : nullptr;
+  a.total_q = static_cast<int32_t>(rows);
+  check(mm3idx_append_kv(&a, stream_of(k)), "mm3idx_append_kv");
+  Py_RETURN_NONE;
+}
+
+// The checks of mm3idx_pool_t.
+mm3idx_pool_t pool_of(const at::Tensor& refs, const at::Tensor& table, const at::Tensor* lens,
+                      int32_t page_size) {
+  need(is(refs, at::kInt, 1) && refs.is_contiguous() && refs.size(0) <= INT32_MAX,
+       "reference counts must be contiguous int32 [num_pages]");
+  need(is(table, at::kInt, 2) && unit_inner(table) && table.size(0) <= INT32_MAX &&
+           table.size(1) <= INT32_MAX,
+       "page tables must be int32 [num_reqs, columns] with unit inner stride");
+  need(!lens || (is(*lens, at::kInt, 1) && lens->is_contiguous() && lens->size(0) == table.size(0)),
+       "lengths must be contiguous int32, one per row of the page table");
+  same_gpu(refs, {&table, lens});
+  mm3idx_pool_t p{};
+  p.refs = static_cast<int32_t*>(refs.data_ptr());
+  p.num_pages = static_cast<int32_t>(refs.size(0));
+  p.page_size = page_size;
+  p.page_table = static_cast<int32_t*>(table.data_ptr());
+  p.table_stride = row_stride(table);
+  p.table_width = static_cast<int32_t>(table.size(1));
+  p.seq_lens = lens ? static_cast<const int32_t*>(lens->data_ptr()) : nullptr;
+  p.num_reqs = static_cast<int32_t>(table.size(0));
+  return p;
+}
+
+// A sequence of caches: tensors whose first dimension is the page, the rest of a
+// page without gaps, in any order.
+struct Caches {
+  mm3idx_cache_t at[MM3IDX_MAX_CACHES];
+  int32_t count = 0, pages = 0;   // pages: of the first one
+  Caches(PyObject* o, const at::Tensor& like, int64_t num_pages) {
+    const bool list = PyList_Check(o) || PyTuple_Check(o);
+    need(list, "caches must be a list or tuple of tensors");
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    need(n <= MM3IDX_MAX_CACHES, "more caches than a call takes");
+    for (Py_ssize_t k = 0; k < n; ++k) {
+      const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(o, k), "caches");
+      if (num_pages < 0) num_pages = t.dim() >= 1 ? t.size(0) : 0;
+      need(t.dim() >= 1 && t.size(0) == num_pages && t.device() == like.device() &&
+               t.layout() == at::kStrided && t.numel() > 0 && num_pages <= INT32_MAX,
+           "caches must be tensors of the pool's number of pages on its GPU");
+      const int64_t count_of_page = t.numel() / num_pages;
+      int64_t dense = 1;                       // the dimensions of a page, innermost first
+      for (;;) {
+        int64_t d = 1;
+        while (d < t.dim() && !(t.stride(d) == dense && t.size(d) > 1)) ++d;
+        if (d == t.dim()) break;
+        dense *= t.size(d);
+      }
+      need(dense == count_of_page && (num_pages == 1 || t.stride(0) >= count_of_page),
+           "a cache's page must lie in memory without gaps, and pages must not overlap");
+      const int64_t size = t.element_size();
+      at[k] = mm3idx_cache_t{t.data_ptr(), (num_pages > 1 ? t.stride(0) : count_of_page) * size,
+                             count_of_page * size};
+      pages = static_cast<int32_t>(num_pages);
+    }
+    count = static_cast<int32_t>(n);
+  }
+};
+
+at::Tensor pages_workspace(PyObject* given, const at::Tensor& refs, int32_t forks) {
+  if (given == Py_None) {
+    size_t bytes = 0;
+    check(mm3idx_pages_workspace_bytes(static_cast<int32_t>(refs.size(0)), forks, &bytes),
+          "mm3idx_pages_workspace_bytes");
+    return at::empty({static_cast<int64_t>(bytes)}, refs.options().dtype(at::kByte));
+  }
+  const at::Tensor& t = tensor(given, "workspace");
+  need(t.device() == refs.device() && t.is_contiguous(),
+       "workspace must be a contiguous tensor on the inputs' GPU");
+  return t;
+}
+
+PyObject* allocate_pages(PyObject* const* args) {
+  const at::Tensor &refs = tensor(args[0], "refs"), &table = tensor(args[1], "page_table"),
+                   &lens = tensor(args[2], "seq_lens");
+  const mm3idx_pool_t p = pool_of(refs, table, &lens, integer(args[4]));
+  const c10::cuda::CUDAGuard guard(refs.device());
+  const at::Tensor ws = pages_workspace(args[5], refs, 0);
+  check(mm3idx_allocate_pages(&p, integer(args[3]), ws.data_ptr(), ws.nbytes(), stream_of(refs)),
+        "mm3idx_allocate_pages");
+  Py_RETURN_NONE;
+}
+
+PyObject* release_pages(PyObject* const* args) {
+  const at::Tensor &refs = tensor(args[0], "refs"), &table = tensor(args[1], "page_table");
+  const at::Tensor* lens = maybe(args[2], "seq_lens");
+  need((args[3] == Py_None) == !lens, "seq_lens and page_size go together");
+  const mm3idx_pool_t p = pool_of(refs, table, lens, lens ? integer(args[3]) : 1);
+  const c10::cuda::CUDAGuard guard(refs.device());
+  check(mm3idx_release_pages(&p, stream_of(refs)), "mm3idx_release_pages");
+  Py_RETURN_NONE;
+}
+
+PyObject* pair_of(at::Tensor first, at::Tensor second) {
+  PyObject* a = THPVariable_Wrap(std::move(first));
+  PyObject* b = a ? THPVariable_Wrap(std::move(second)) : nullptr;
+  PyObject* result = b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  if (!result) throw Raised();
+  return result;
+}
+
+// (table, lengths)
+PyObject* fork_pages(PyObject* const* args) {
+  const at::Tensor &refs = tensor(args[0], "refs"), &table = tensor(args[1], "page_table"),
+                   &lens = tensor(args[2], "seq_lens"), &parents = tensor(args[3], "parents");
+  const at::Tensor *out = maybe(args[6], "out"), *out_lens = maybe(args[7], "out_lens");
+  const mm3idx_pool_t p = pool_of(refs, table, &lens, integer(args[5]));
+  need(is(parents, at::kInt, 1) && parents.is_contiguous() && parents.size(0) <= INT32_MAX,
+       "parents must be contiguous int32 [forks]");
+  const int64_t n = parents.size(0), width = table.size(1);
+  need(!out || (is(*out, at::kInt, 2) && shaped(*out, {n, width}) && unit_inner(*out)),
+       "out must be int32 [forks, columns of the page table] with unit inner stride");
+  need(!out_lens || (is(*out_lens, at::kInt, 1) && out_lens->size(0) == n && out_lens->is_contiguous()),
+       "out_lens must be contiguous int32 [forks]");
+  same_gpu(refs, {&parents, out, out_lens});
+  const Caches caches(args[4], refs, refs.size(0));
+  const c10::cuda::CUDAGuard guard(refs.device());
+  at::Tensor results[2];
+  Outputs<2> made;
+  if (out) results[0] = *out;
+  else made.add(0, at::kInt, {n, width});
+  if (out_lens) results[1] = *out_lens;
+  else made.add(1, at::kInt, {n});
+  if (!out || !out_lens) made.allocate(refs, results);
+  const at::Tensor ws = pages_workspace(args[8], refs, static_cast<int32_t>(n));
+  check(mm3idx_fork_pages(&p, static_cast<const int32_t*>(parents.data_ptr()),
+                          static_cast<int32_t>(n), static_cast<int32_t*>(results[0].data_ptr()),
+                          row_stride(results[0]), static_cast<int32_t*>(results[1].data_ptr()),
+                          caches.at, caches.count, ws.data_ptr(), ws.nbytes(), stream_of(refs)),
+        "mm3idx_fork_pages");
+  return pair_of(std::move(results[0]), std::move(results[1]));
+}
+
+// (refs, table, live)
+PyObject* compact_pages(PyObject* const* args) {
+  const at::Tensor &refs = tensor(args[0], "refs"), &table = tensor(args[1], "page_table");
+  const bool in_place = truth(args[3]);
+  const mm3idx_pool_t p = pool_of(refs, table, nullptr, 1);
+  const Caches caches(args[2], refs, refs.size(0));
+  const c10::cuda::CUDAGuard guard(refs.device());
+  at::Tensor out[3];
+  Outputs<3> made;
+  if (in_place) {
+    out[0] = refs;
+    out[1] = table;
+  } else {
+    made.add(0, at::kInt, {refs.size(0)});
+    made.add(1, at::kInt, {table.size(0), table.size(1)});
+  }
+  made.add(2, at::kInt, {1});
+  made.allocate(refs, out);
+  const at::Tensor ws = pages_workspace(args[4], refs, 0);
+  check(mm3idx_compact_pages(&p, static_cast<int32_t*>(out[0].data_ptr()),
+                             static_cast<int32_t*>(out[1].data_ptr()), row_stride(out[1]),
+                             static_cast<int32_t*>(out[2].data_ptr()), caches.at, caches.count,
+                             ws.data_ptr(), ws.nbytes(), stream_of(refs)),
+        "mm3idx_compact_pages");
+  PyObject* result = PyTuple_New(3);
+  if (!result) throw Raised();
+  for (int k = 0; k < 3; ++k) {
+    PyObject* o = THPVariable_Wrap(std::move(out[k]));
+    if (!o) {
+      Py_DECREF(result);
+      throw Raised();
+    }
+    PyTuple_SET_ITEM(result, k, o);
+  }
+  return result;
+}
+
+PyObject* copy_pages(PyObject* const* args) {
+  const at::Tensor &src = tensor(args[1], "src"), &dst = tensor(args[2], "dst");
+  need(is(src, at::kInt, 1) && is(dst, at::kInt, 1) && src.sizes() == dst.sizes() &&
+           src.is_contiguous() && dst.is_contiguous() && src.size(0) <= INT32_MAX,
+       "src and dst must be contiguous int32 of one length");
+  same_gpu(src, {&dst});
+  const Caches caches(args[0], src, -1);
+  need(caches.count > 0, "at least one cache");
+  const c10::cuda::CUDAGuard guard(src.device());
+  check(mm3idx_copy_pages(caches.at, caches.count, caches.pages,
+                          static_cast<const int32_t*>(src.data_ptr()),
+                          static_cast<const int32_t*>(dst.data_ptr()),
+                          static_cast<int32_t>(src.size(0)), stream_of(src)),
+        "mm3idx_copy_pages");
+  Py_RETURN_NONE;
+}
+
 // Every exception becomes Python's; `N` positional arguments.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -458,10 +734,16 @@ PyCFunction fast(F f) {
 
 PyMethodDef methods[] = {
     {"set_error", set_error, METH_O, nullptr},
-    {"paged_attention", fast(entry<paged_attention, 14>), METH_FASTCALL, nullptr},
+    {"paged_attention", fast(entry<paged_attention, 16>), METH_FASTCALL, nullptr},
     {"accumulate_weights", fast(entry<accumulate_weights, 7>), METH_FASTCALL, nullptr},
     {"evict_blocks", fast(entry<evict_blocks, 14>), METH_FASTCALL, nullptr},
     {"verify_drafts", fast(entry<verify_drafts, 7>), METH_FASTCALL, nullptr},
+    {"append_kv", fast(entry<append_kv, 13>), METH_FASTCALL, nullptr},
+    {"allocate_pages", fast(entry<allocate_pages, 6>), METH_FASTCALL, nullptr},
+    {"release_pages", fast(entry<release_pages, 4>), METH_FASTCALL, nullptr},
+    {"fork_pages", fast(entry<fork_pages, 9>), METH_FASTCALL, nullptr},
+    {"compact_pages", fast(entry<compact_pages, 5>), METH_FASTCALL, nullptr},
+    {"copy_pages", fast(entry<copy_pages, 3>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

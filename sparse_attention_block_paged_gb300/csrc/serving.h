@@ -69,6 +69,9 @@ struct AttentionArgs {
   bool few;                   // at most 32 requests, and a list whose positions times gangs fit 32 bits
   float scale;                // sm_scale * k_scale
   float v_scale;
+  const float* k_scales;      // of a page and kv head, by the strides below; null: none
+  const float* v_scales;
+  int64_t ks_page, ks_head, vs_page, vs_head;
   void* out;
   int64_t o_tok, o_head;
   float* lse;                 // may be null
@@ -165,6 +168,10 @@ cudaError_t launch_attention_bf16_e4m3(const CUtensorMap& kmap, const CUtensorMa
                                        const AttentionArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_attention_fp16_e4m3(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                        const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_bf16_e4m3_scaled(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                              const AttentionArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_attention_fp16_e4m3_scaled(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                              const AttentionArgs& a, int grid, cudaStream_t s);
 // dst may be a.acc itself.
 cudaError_t launch_accumulate(const WeightArgs& a, float* dst, int64_t dst_stride, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
