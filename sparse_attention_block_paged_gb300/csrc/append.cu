@@ -13,9 +13,11 @@
 // for a decode step a chain of dependent loads (length, page, old scale).  So a
 // (page, head) of the keys or of the values is one group of threads' that holds
 // its new elements in registers between the maximum and the rounding: one pass
-// over the data, nothing exchanged between CTAs.  A group is as large as the
-// page's new tokens need at 8 pieces of 16 bytes a thread: a warp for up to 16
-// tokens of 128 elements, a CTA for a whole page of 128.
+// over the data, nothing exchanged between CTAs.  A thread holds four pieces of
+// 16 bytes at most, so that a whole SM of threads fits, and asks for them as soon
+// as it knows the length, before the page table (with eight pieces, two CTAs of
+// 256 threads an SM and the page first, four prompts of 8192 tokens took 104 us;
+// now see below).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,8 +26,6 @@
 namespace mm3idx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPieces = 8;              // of 16 bytes, a thread
 constexpr float kLowScale = 0x1p-60f, kHighScale = 0x1p60f;
 
 template <bool BF16>
@@ -84,9 +84,13 @@ __device__ __forceinline__ By division(float x) {
 enum { kCopy = 0, kCodes = 1, kScaled = 2 };
 
 // BF16: type of the new elements.  MODE: a cache of that type, of e4m3, or of e4m3
-// with scales.  G: threads a (page, head).
-template <bool BF16, int MODE, int G>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+// with scales.  UNIT: both divisors are 1.  G: threads a (page, head).  N: pieces of
+// 16 bytes a thread.
+template <bool BF16, int MODE, bool UNIT, int G, int N>
+__global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 ? 3 : 6)
+                                                      : G > 256 ? 2 : 5)
+    append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kThreads = G > 256 ? G : 256;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float tops[kThreads / 32];
@@ -98,15 +102,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int head = unit - outer * a.kv_heads, which = outer & 1;
   const int req = a.by_touched.quotient(outer >> 1), turn = (outer >> 1) - req * a.touched;
   const AppendSide& side = a.side[which];
-  const int size = 1 << a.page_shift;
+  const int shift = a.head_dim == 128 ? 4 : 3;           // pieces of a row, log2
+  const int mask = (1 << shift) - 1;
 
   // The page's new slots [from, to) and the row of the first of them.
-  int from = 0, to = 0, page = -1;
+  int from = 0, pieces = 0, column = 0, bits = 0;
   int64_t row = 0;
   if (unit < a.units) {
     const int raw = __ldg(a.seq_lens + req);
     const int len = min(max(raw, 0), a.max_seq_len);
-    int rows = a.query_len, bits = raw > a.max_seq_len ? MM3IDX_DEV_SEQ_TOO_LONG : 0;
+    int rows = a.query_len;
+    bits = raw > a.max_seq_len ? MM3IDX_DEV_SEQ_TOO_LONG : 0;
     int64_t row0 = static_cast<int64_t>(req) * a.query_len;
     if (a.cu) {
       const int c0 = __ldg(a.cu + req), c1 = __ldg(a.cu + req + 1);
@@ -117,69 +123,70 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       row0 = c0;
     }
     const int begin = max(len - rows, 0);               // first new position
-    const int p = (begin >> a.page_shift) + turn;       // page of the request
-    const int lo = max(begin, p << a.page_shift), hi = min(len, (p + 1) << a.page_shift);
+    column = (begin >> a.page_shift) + turn;            // page of the request
+    const int lo = max(begin, column << a.page_shift), hi = min(len, (column + 1) << a.page_shift);
     if (lo < hi) {
-      page = __ldg(a.table + req * a.table_stride + p);
-      if (page < 0 || page >= a.num_pages) {
-        bits |= MM3IDX_DEV_BAD_PAGE;
-      } else {
-        from = lo & (size - 1);
-        to = from + hi - lo;
-        row = row0 + (lo - (len - rows));
-      }
+      from = lo & ((1 << a.page_shift) - 1);
+      pieces = (hi - lo) << shift;
+      row = row0 + (lo - (len - rows));
     }
-    if (bits && t == 0 && head == 0 && which == 0) atomicOr(a.status, bits);
   }
-
-  const int shift = a.head_dim == 128 ? 4 : 3;           // pieces of a row, log2
-  const int pieces = (to - from) << shift;
   const uint16_t* x = side.x + row * side.x_tok + head * side.x_head;
-  uint4 v[kPieces];
+  uint4 v[N];
 #pragma unroll
-  for (int m = 0; m < kPieces; ++m) {
+  for (int m = 0; m < N; ++m) {
     const int k = t + m * G;
-    if (k < pieces)
-      v[m] = __ldg(reinterpret_cast<const uint4*>(x + (k >> shift) * side.x_tok) +
-                   (k & ((1 << shift) - 1)));
-    else
-      v[m] = make_uint4(0, 0, 0, 0);
+    v[m] = make_uint4(0, 0, 0, 0);
+    if (k < pieces) v[m] = __ldcs(reinterpret_cast<const uint4*>(x + (k >> shift) * side.x_tok) + (k & mask));
   }
-  const bool plain = side.scale == 1.0f;
+  int page = -1;
+  if (pieces > 0) {
+    page = __ldg(a.table + req * a.table_stride + column);
+    if (page < 0 || page >= a.num_pages) {
+      bits |= MM3IDX_DEV_BAD_PAGE;
+      pieces = 0;
+    }
+  }
+  if (bits && t == 0 && head == 0 && which == 0) atomicOr(a.status, bits);
+
   const By by = division(side.scale);
+  auto pair = [&](uint32_t w) {
+    const float2 f = floats<BF16>(w);
+    if constexpr (UNIT) return f;
+    return make_float2(by(f.x), by(f.y));
+  };
   uint8_t* base = side.cache + page * side.c_page + head * side.c_head;
   if constexpr (MODE == kCopy) {
 #pragma unroll
-    for (int m = 0; m < kPieces; ++m) {
+    for (int m = 0; m < N; ++m) {
       const int k = t + m * G;
       if (k >= pieces) continue;
       uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-      if (!plain)
+      if constexpr (!UNIT)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 f = floats<BF16>(w[e]);
-          w[e] = halves<BF16>(by(f.x), by(f.y));
+          const float2 f = pair(w[e]);
+          w[e] = halves<BF16>(f.x, f.y);
         }
-      *reinterpret_cast<uint4*>(base + (from + (k >> shift)) * side.c_tok +
-                                (k & ((1 << shift) - 1)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(base + (from + (k >> shift)) * side.c_tok + (k & mask) * 16) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
     return;
   }
-  float scale = 1.0f;
+  By to_codes{1.0f, 1.0f, true};
   if constexpr (MODE == kScaled) {
     float* at = side.scales + page * side.s_page + head * side.s_head;
-    const float old = from > 0 ? fminf(fmaxf(*at, kLowScale), kHighScale) : 0.0f;
+    const float old = pieces > 0 && from > 0 ? fminf(fmaxf(*at, kLowScale), kHighScale) : 0.0f;
     // The largest magnitude (a maximum passes over NaN); where that is infinite,
     // once more without the infinities.
     auto largest = [&](bool finite) {
       float top = 0.0f;
 #pragma unroll
-      for (int m = 0; m < kPieces; ++m) {
+      for (int m = 0; m < N; ++m) {
         const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float2 f = floats<BF16>(w[e]);
-          if (!plain) f = make_float2(by(f.x), by(f.y));
+          float2 f = pair(w[e]);
           f = make_float2(fabsf(f.x), fabsf(f.y));
           if (finite) f = make_float2(f.x < INFINITY ? f.x : 0.0f, f.y < INFINITY ? f.y : 0.0f);
           top = fmaxf(top, fmaxf(f.x, f.y));
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const float without = largest(true);
       if (top == INFINITY) top = without;
     }
-    scale = fmaxf(least_scale(top), old);
+    const float scale = fmaxf(least_scale(top), old);
     __syncwarp();                      // every lane has the old scale (larger groups met above)
     if (pieces > 0) {
       if (from > 0 && scale != old) {
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         const float f = old / scale;
         for (int k = t; k < from << (shift - 1); k += G) {
           uint4* c = reinterpret_cast<uint4*>(base + (k >> (shift - 1)) * side.c_tok) +
-                     (k & ((1 << (shift - 1)) - 1));
+                     (k & (mask >> 1));
           uint4 q = *c;
           uint32_t* w = &q.x;
 #pragma unroll
@@ -225,43 +232,66 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       }
       if (t == 0) *at = scale;
     }
+    to_codes = division(scale);
   }
-  const By to_codes = division(scale);
 #pragma unroll
-  for (int m = 0; m < kPieces; ++m) {
+  for (int m = 0; m < N; ++m) {
     const int k = t + m * G;
     if (k >= pieces) continue;
     const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
     float f[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float2 y = floats<BF16>(w[e]);
-      if (!plain) y = make_float2(by(y.x), by(y.y));
-      f[2 * e] = MODE == kScaled ? to_codes(y.x) : y.x;
-      f[2 * e + 1] = MODE == kScaled ? to_codes(y.y) : y.y;
+      const float2 y = pair(w[e]);
+      f[2 * e] = y.x;
+      f[2 * e + 1] = y.y;
     }
-    *reinterpret_cast<uint2*>(base + (from + (k >> shift)) * side.c_tok +
-                              (k & ((1 << shift) - 1)) * 8) =
+    if constexpr (MODE == kScaled) {
+      if (to_codes.exact) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= to_codes.inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] /= to_codes.d;
+      }
+    }
+    *reinterpret_cast<uint2*>(base + (from + (k >> shift)) * side.c_tok + (k & mask) * 8) =
         make_uint2(codes(f[0], f[1], f[2], f[3]), codes(f[4], f[5], f[6], f[7]));
   }
 }
 
-template <bool BF16, int MODE>
+template <bool BF16, int MODE, bool UNIT, int G, int N>
+cudaError_t launch_group(const AppendArgs& a, cudaStream_t s) {
+  constexpr int kThreads = G > 256 ? G : 256, per = kThreads / G;
+  return launch_dependent(append_kernel<BF16, MODE, UNIT, G, N>, dim3((a.units - 1) / per + 1),
+                          kThreads, 1, a, s);
+}
+
+// The fewest threads that hold the most new tokens of a page, four pieces each; a
+// warp less than that.
+template <bool BF16, int MODE, bool UNIT>
 cudaError_t launch_mode(const AppendArgs& a, cudaStream_t s) {
-  const int g = append_threads(a.query_len, 1 << a.page_shift, a.head_dim);
-  const int per = kThreads / g;
-  const dim3 grid((a.units - 1) / per + 1);
-  if (g == 32) return launch_dependent(append_kernel<BF16, MODE, 32>, grid, kThreads, 1, a, s);
-  if (g == 64) return launch_dependent(append_kernel<BF16, MODE, 64>, grid, kThreads, 1, a, s);
-  if (g == 128) return launch_dependent(append_kernel<BF16, MODE, 128>, grid, kThreads, 1, a, s);
-  return launch_dependent(append_kernel<BF16, MODE, 256>, grid, kThreads, 1, a, s);
+  const int page = 1 << a.page_shift;
+  const int pieces = (a.query_len < page ? a.query_len : page) * (a.head_dim / 8);
+  if (pieces <= 32) return launch_group<BF16, MODE, UNIT, 32, 1>(a, s);
+  if (pieces <= 128) return launch_group<BF16, MODE, UNIT, 32, 4>(a, s);
+  if (pieces <= 256) return launch_group<BF16, MODE, UNIT, 64, 4>(a, s);
+  if (pieces <= 512) return launch_group<BF16, MODE, UNIT, 128, 4>(a, s);
+  if (pieces <= 1024) return launch_group<BF16, MODE, UNIT, 256, 4>(a, s);
+  return launch_group<BF16, MODE, UNIT, 512, 4>(a, s);
+}
+
+template <bool BF16, bool UNIT>
+cudaError_t launch_cache(const AppendArgs& a, cudaStream_t s) {
+  if (a.kv_type != MM3IDX_TYPE_E4M3) return launch_mode<BF16, kCopy, UNIT>(a, s);
+  if (a.side[0].scales) return launch_mode<BF16, kScaled, UNIT>(a, s);
+  return launch_mode<BF16, kCodes, UNIT>(a, s);
 }
 
 template <bool BF16>
 cudaError_t launch_type(const AppendArgs& a, cudaStream_t s) {
-  if (a.kv_type != MM3IDX_TYPE_E4M3) return launch_mode<BF16, kCopy>(a, s);
-  if (a.side[0].scales) return launch_mode<BF16, kScaled>(a, s);
-  return launch_mode<BF16, kCodes>(a, s);
+  return a.side[0].scale == 1.0f && a.side[1].scale == 1.0f ? launch_cache<BF16, true>(a, s)
+                                                            : launch_cache<BF16, false>(a, s);
 }
 
 }  // namespace

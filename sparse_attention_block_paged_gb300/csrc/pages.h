@@ -35,14 +35,6 @@ struct AppendArgs {
   int32_t* status;
 };
 
-// Threads that share a (page, head) of the keys or the values: each holds up to
-// 8 pieces of 16 bytes.
-inline int append_threads(int32_t query_len, int32_t page_size, int32_t head_dim) {
-  const int rows = query_len < page_size ? query_len : page_size;
-  const int pieces = rows * (head_dim / 8);
-  return pieces <= 256 ? 32 : pieces <= 512 ? 64 : pieces <= 1024 ? 128 : 256;
-}
-
 struct Cache {
   uint8_t* data;
   int64_t page_stride, page_bytes;
