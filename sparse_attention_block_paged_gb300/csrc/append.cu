@@ -132,13 +132,14 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
     }
   }
   const uint16_t* x = side.x + row * side.x_tok + head * side.x_head;
+  auto load = [&](int m) {
+    const int k = t + m * G;
+    if (k >= pieces) return make_uint4(0, 0, 0, 0);
+    return __ldg(reinterpret_cast<const uint4*>(x + (k >> shift) * side.x_tok) + (k & mask));
+  };
   uint4 v[N];
 #pragma unroll
-  for (int m = 0; m < N; ++m) {
-    const int k = t + m * G;
-    v[m] = make_uint4(0, 0, 0, 0);
-    if (k < pieces) v[m] = __ldcs(reinterpret_cast<const uint4*>(x + (k >> shift) * side.x_tok) + (k & mask));
-  }
+  for (int m = 0; m < N; ++m) v[m] = load(m);
   int page = -1;
   if (pieces > 0) {
     page = __ldg(a.table + req * a.table_stride + column);
@@ -178,20 +179,19 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
     float* at = side.scales + page * side.s_page + head * side.s_head;
     const float old = pieces > 0 && from > 0 ? fminf(fmaxf(*at, kLowScale), kHighScale) : 0.0f;
     // The largest magnitude (a maximum passes over NaN); where that is infinite,
-    // once more without the infinities.
-    auto largest = [&](bool finite) {
-      float top = 0.0f;
+    // once more without the infinities, from memory (registers are not indexed).
+    auto larger = [&](float top, uint4 q, bool finite) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int m = 0; m < N; ++m) {
-        const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float2 f = pair(w[e]);
-          f = make_float2(fabsf(f.x), fabsf(f.y));
-          if (finite) f = make_float2(f.x < INFINITY ? f.x : 0.0f, f.y < INFINITY ? f.y : 0.0f);
-          top = fmaxf(top, fmaxf(f.x, f.y));
-        }
+      for (int e = 0; e < 4; ++e) {
+        float2 f = pair(w[e]);
+        f = make_float2(fabsf(f.x), fabsf(f.y));
+        if (finite) f = make_float2(f.x < INFINITY ? f.x : 0.0f, f.y < INFINITY ? f.y : 0.0f);
+        top = fmaxf(top, fmaxf(f.x, f.y));
       }
+      return top;
+    };
+    auto joined = [&](float top) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if constexpr (G > 32) {
@@ -204,11 +204,17 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
       }
       return top;
     };
-    float top = largest(false);
+    float top = 0.0f;
+#pragma unroll
+    for (int m = 0; m < N; ++m) top = larger(top, v[m], false);
+    top = joined(top);
     bool again = top == INFINITY;
     if constexpr (G > 32) again = __syncthreads_or(again);
     if (again) {
-      const float without = largest(true);
+      float without = 0.0f;
+#pragma unroll 1
+      for (int m = 0; m < N; ++m) without = larger(without, load(m), true);
+      without = joined(without);
       if (top == INFINITY) top = without;
     }
     const float scale = fmaxf(least_scale(top), old);
@@ -234,30 +240,28 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
     }
     to_codes = division(scale);
   }
-#pragma unroll
-  for (int m = 0; m < N; ++m) {
+  auto store = [&](int m, uint4 q, auto scaled) {
     const int k = t + m * G;
-    if (k >= pieces) continue;
-    const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-    float f[8];
+    if (k >= pieces) return;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t c[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 y = pair(w[e]);
-      f[2 * e] = y.x;
-      f[2 * e + 1] = y.y;
-    }
-    if constexpr (MODE == kScaled) {
-      if (to_codes.exact) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= to_codes.inv;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] /= to_codes.d;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const float2 lo = pair(w[2 * h]), hi = pair(w[2 * h + 1]);
+      c[h] = codes(scaled(lo.x), scaled(lo.y), scaled(hi.x), scaled(hi.y));
     }
     *reinterpret_cast<uint2*>(base + (from + (k >> shift)) * side.c_tok + (k & mask) * 8) =
-        make_uint2(codes(f[0], f[1], f[2], f[3]), codes(f[4], f[5], f[6], f[7]));
+        make_uint2(c[0], c[1]);
+  };
+  if (MODE == kScaled && !to_codes.exact) {
+    // an old scale that is no power of two: divisions, from memory again
+#pragma unroll 1
+    for (int m = 0; m < N; ++m) store(m, load(m), [&](float f) { return f / to_codes.d; });
+    return;
   }
+#pragma unroll
+  for (int m = 0; m < N; ++m)
+    store(m, v[m], [&](float f) { return MODE == kScaled ? f * to_codes.inv : f; });
 }
 
 template <bool BF16, int MODE, bool UNIT, int G, int N>
