@@ -22,6 +22,8 @@ namespace {
 constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kAhead = 8;               // loads of a lane in flight
+constexpr int kNear = 2048;             // entries of a list in shared memory
+constexpr int64_t kSmall = 16384;       // pages and entries that one CTA scans
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -44,10 +46,12 @@ __device__ __forceinline__ int64_t remote(const int64_t* p, uint32_t rank) {
   return v;
 }
 
-// One of a kernel's scans over [0, n): this warp's part, the marked entries before it
-// and in all.
+// One of a kernel's scans over [0, n): the part of one of `warps` warps a CTA (a CTA's
+// first warps, or those after others), the marked entries before it and in all, and
+// what the first round found (parts longer than a round look again).
 struct Part {
   int64_t lo, hi, before, total;
+  int found[kAhead];
 };
 
 struct Counts {
@@ -55,52 +59,69 @@ struct Counts {
   int64_t cta;
 };
 
-__device__ __forceinline__ Part part_of(int64_t n) {
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kScanWarps;
-  const int64_t w = static_cast<int64_t>(cluster_rank()) * kScanWarps + (threadIdx.x >> 5);
-  const int64_t per = ((n + warps - 1) / warps + 31) & ~int64_t{31};
-  Part p;
-  p.lo = min(w * per, n);
-  p.hi = min(p.lo + per, n);
+// `first`: the first of the CTA's warps that share it; others get an empty part.
+__device__ __forceinline__ void split(Part& p, int64_t n, int first, int warps) {
+  const int w = static_cast<int>(threadIdx.x >> 5) - first;
+  const int64_t all = static_cast<int64_t>(gridDim.x) * warps;
+  const int64_t per = ((n + all - 1) / all + 31) & ~int64_t{31};
+  const int64_t at = static_cast<int64_t>(cluster_rank()) * warps + w;
+  const bool mine = w >= 0 && w < warps;
+  p.lo = mine ? min(at * per, n) : 0;
+  p.hi = mine ? min(p.lo + per, n) : 0;
   p.before = p.total = 0;
-  return p;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) p.found[k] = -1;
 }
 
-// The number of entries in the warp's part for which f says so.
+// f(entry) is what a marked entry stands for (>= 0), or -1.
 template <class F>
-__device__ __forceinline__ int64_t count(const Part& p, F f) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void look(const Part& p, int64_t i, F f, int (&found)[kAhead]) {
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int64_t at = i + 32 * k + (threadIdx.x & 31);
+    found[k] = at < p.hi ? f(at) : -1;
+  }
+}
+
+// The number of marked entries in the warp's part, the first round's known.
+template <class F>
+__device__ __forceinline__ int64_t count_rest(const Part& p, F f) {
   int64_t sum = 0;
-  for (int64_t i = p.lo; i < p.hi; i += 32 * kAhead) {
-    bool on[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t at = i + 32 * k + lane;
-      on[k] = at < p.hi && f(at);
-    }
+  for (int k = 0; k < kAhead; ++k) sum += __popc(__ballot_sync(0xffffffffu, p.found[k] >= 0));
+  for (int64_t i = p.lo + 32 * kAhead; i < p.hi; i += 32 * kAhead) {
+    int found[kAhead];
+    look(p, i, f, found);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) sum += __popc(__ballot_sync(0xffffffffu, on[k]));
+    for (int k = 0; k < kAhead; ++k) sum += __popc(__ballot_sync(0xffffffffu, found[k] >= 0));
   }
   return sum;
 }
 
-// f(entry, its rank) of the marked entries below rank `most`.
-template <class M, class F>
-__device__ __forceinline__ void each(const Part& p, int64_t most, M marked, F f) {
+template <class F>
+__device__ __forceinline__ int64_t count(Part& p, F f) {
+  if (p.lo < p.hi) look(p, p.lo, f, p.found);
+  return count_rest(p, f);
+}
+
+// g(entry, what it stands for, its rank) of the marked entries below rank `most`.
+template <class F, class G>
+__device__ __forceinline__ void each(const Part& p, int64_t most, F f, G g) {
   const int lane = threadIdx.x & 31;
   int64_t rank = p.before;
   for (int64_t i = p.lo; i < p.hi && rank < most; i += 32 * kAhead) {
-    bool on[kAhead];
+    int found[kAhead];
+    if (i == p.lo) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t at = i + 32 * k + lane;
-      on[k] = at < p.hi && marked(at);
+      for (int k = 0; k < kAhead; ++k) found[k] = p.found[k];
+    } else {
+      look(p, i, f, found);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const unsigned all = __ballot_sync(0xffffffffu, on[k]);
+      const unsigned all = __ballot_sync(0xffffffffu, found[k] >= 0);
       const int64_t r = rank + __popc(all & ((1u << lane) - 1u));
-      if (on[k] && r < most) f(i + 32 * k + lane, r);
+      if (found[k] >= 0 && r < most) g(i + 32 * k + lane, found[k], r);
       rank += __popc(all);
     }
   }
@@ -129,12 +150,16 @@ __device__ __forceinline__ void prefixes(Counts* c, const int64_t (&mine)[N], Pa
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     int64_t before = warp > 0 ? c[k].warp[warp - 1] : 0, total = 0;
-    const int64_t theirs = lane < static_cast<int>(gridDim.x) ? remote(&c[k].cta, lane) : 0;
+    if (gridDim.x == 1) {
+      total = c[k].cta;
+    } else {
+      const int64_t theirs = lane < static_cast<int>(gridDim.x) ? remote(&c[k].cta, lane) : 0;
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
-      const int64_t x = __shfl_sync(0xffffffffu, theirs, r);
-      total += x;
-      if (r < static_cast<int>(rank)) before += x;
+      for (int r = 0; r < kCluster; ++r) {
+        const int64_t x = __shfl_sync(0xffffffffu, theirs, r);
+        total += x;
+        if (r < static_cast<int>(rank)) before += x;
+      }
     }
     parts[k]->before = before;
     parts[k]->total = total;
@@ -150,12 +175,12 @@ __device__ __forceinline__ int clamped_len(const ScanArgs& a, int i, bool* over)
 
 // Entry k of an allocation: request k / columns, one of the columns that its new
 // tokens lie in; null where there is none.
-__device__ __forceinline__ int32_t* allocation_entry(const ScanArgs& a, int64_t k, bool report) {
+__device__ __forceinline__ int32_t* allocation_entry(const ScanArgs& a, int64_t k) {
   const int i = a.by_columns.quotient(static_cast<int>(k));
   const int turn = static_cast<int>(k) - i * a.columns;
   bool over;
   const int len = clamped_len(a, i, &over);
-  if (over && report) atomicOr(a.status, MM3IDX_DEV_SEQ_TOO_LONG);
+  if (over && turn == 0) atomicOr(a.status, MM3IDX_DEV_SEQ_TOO_LONG);
   const int first = max(len - a.query_len, 0) / a.page_size, end = (len + a.page_size - 1) / a.page_size;
   return first + turn < end ? a.table + i * a.table_stride + first + turn : nullptr;
 }
@@ -171,48 +196,48 @@ __device__ __forceinline__ int last_page(const ScanArgs& a, int64_t k) {
   return page >= 0 && page < a.num_pages ? page : -1;
 }
 
-// Free pages for the entries that want one.  FORK: (source, new page) pairs.
+// Free pages for the entries that want one.  FORK: (source, new page) pairs.  An
+// entry hangs on two or three loads in a row, a count on one: half of the warps
+// each.
 template <bool FORK>
 __global__ void __launch_bounds__(kScanThreads) claim_kernel(const __grid_constant__ ScanArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Counts counts[2];
-  Part items = part_of(a.items), pages = part_of(a.num_pages);
+  __shared__ int32_t near[kNear];        // a single CTA's list
+  Part items, pages;
+  split(items, a.items, 0, kScanWarps / 2);
+  split(pages, a.num_pages, kScanWarps / 2, kScanWarps / 2);
   auto wants = [&](int64_t k) {
-    if constexpr (FORK) return last_page(a, k) >= 0;
-    const int32_t* e = allocation_entry(a, k, false);
-    return e && __ldcg(e) < 0;
+    if constexpr (FORK) return last_page(a, k);
+    const int32_t* e = allocation_entry(a, k);
+    return e && __ldcg(e) < 0 ? 0 : -1;
   };
-  auto is_free = [&](int64_t p) { return __ldcg(a.refs + p) == 0; };
+  auto is_free = [&](int64_t p) { return __ldcg(a.refs + p) == 0 ? static_cast<int>(p) : -1; };
   const int64_t mine[2] = {count(items, wants), count(pages, is_free)};
   Part* parts[2] = {&items, &pages};
   prefixes(counts, mine, parts);
   const int64_t most = min(items.total, pages.total);
-  each(pages, most, is_free, [&](int64_t p, int64_t r) {
-    a.list[r] = static_cast<int32_t>(p);
+  int32_t* list = gridDim.x == 1 && most <= kNear ? near : a.list;
+  each(pages, most, is_free, [&](int64_t p, int, int64_t r) {
+    list[r] = static_cast<int32_t>(p);
     a.refs[p] = 1;
   });
   if (threadIdx.x == 0 && cluster_rank() == 0 && items.total > pages.total)
     atomicOr(a.status, MM3IDX_DEV_NO_PAGES);
   cluster_sync();
+  auto entry = [&](int64_t r) { return list == near ? near[r] : __ldcg(list + r); };
   if constexpr (FORK) {
     for (int64_t k = items.lo + (threadIdx.x & 31); k < items.hi; k += 32) a.src[k] = a.dst[k] = -1;
     __syncwarp();
-    each(items, most, wants, [&](int64_t k, int64_t r) {
-      a.src[k] = last_page(a, k);
-      a.dst[k] = __ldcg(a.list + r);
+    each(items, most, wants, [&](int64_t k, int from, int64_t r) {
+      a.src[k] = from;
+      a.dst[k] = entry(r);
     });
   } else {
-    each(items, items.total, wants, [&](int64_t k, int64_t r) {
-      *allocation_entry(a, k, true) = r < most ? __ldcg(a.list + r) : -1;
+    each(items, items.total, wants, [&](int64_t k, int, int64_t r) {
+      *allocation_entry(a, k) = r < most ? entry(r) : -1;
     });
-    // lengths beyond the table
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x; i < a.num_reqs;
-         i += static_cast<int64_t>(gridDim.x) * kScanThreads) {
-      bool over;
-      clamped_len(a, static_cast<int>(i), &over);
-      if (over) atomicOr(a.status, MM3IDX_DEV_SEQ_TOO_LONG);
-    }
   }
   cluster_sync();                        // no CTA leaves while its counts may be read
 }
@@ -222,27 +247,34 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Counts first[1], second[2];
-  Part all = part_of(a.num_pages);
-  auto is_live = [&](int64_t p) { return __ldcg(a.refs + p) != 0; };
+  Part all;
+  split(all, a.num_pages, 0, kScanWarps);
+  auto used = [&](int64_t p) { return __ldcg(a.refs + p) != 0 ? static_cast<int>(p) : -1; };
   {
-    const int64_t mine[1] = {count(all, is_live)};
+    const int64_t mine[1] = {count(all, used)};
     Part* parts[1] = {&all};
     prefixes(first, mine, parts);
   }
   const int64_t live = all.total;
-  Part holes = part_of(a.num_pages), movers = holes;
-  auto is_hole = [&](int64_t p) { return p < live && __ldcg(a.refs + p) == 0; };
-  auto is_mover = [&](int64_t p) { return p >= live && __ldcg(a.refs + p) != 0; };
+  Part holes = all, movers = all;
+  auto hole = [&](int64_t p) { return p < live && __ldcg(a.refs + p) == 0 ? static_cast<int>(p) : -1; };
+  auto mover = [&](int64_t p) { return p >= live && __ldcg(a.refs + p) != 0 ? static_cast<int>(p) : -1; };
   // a warp's part lies before `live`, behind it, or is the one around it
-  const int64_t mine[2] = {holes.lo < live ? count(holes, is_hole) : 0,
-                           movers.hi > live ? count(movers, is_mover) : 0};
+  if (holes.lo >= live) holes.lo = holes.hi;
+  if (movers.hi <= live) movers.lo = movers.hi;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int64_t p = all.lo + 32 * k + (threadIdx.x & 31);
+    const bool in = p < all.hi, free = all.found[k] < 0;
+    holes.found[k] = in && free && p < live ? static_cast<int>(p) : -1;
+    movers.found[k] = in && !free && p >= live ? static_cast<int>(p) : -1;
+  }
+  const int64_t mine[2] = {count_rest(holes, hole), count_rest(movers, mover)};
   Part* parts[2] = {&holes, &movers};
   prefixes(second, mine, parts);
   const int64_t none = int64_t{1} << 62;
-  if (holes.lo < live)
-    each(holes, none, is_hole, [&](int64_t p, int64_t r) { a.dst[r] = static_cast<int32_t>(p); });
-  if (movers.hi > live)
-    each(movers, none, is_mover, [&](int64_t p, int64_t r) { a.src[r] = static_cast<int32_t>(p); });
+  each(holes, none, hole, [&](int64_t, int p, int64_t r) { a.dst[r] = p; });
+  each(movers, none, mover, [&](int64_t, int p, int64_t r) { a.src[r] = p; });
   if (threadIdx.x == 0 && cluster_rank() == 0) {
     *a.live = static_cast<int32_t>(live);
     *a.moves = static_cast<int32_t>(movers.total);
@@ -270,7 +302,7 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const __grid_constan
 
 // ------------------------------------------------------------------- copies
 
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kMoveCtas = 5;   // CTAs an SM
 constexpr int kPieces = 8;               // of a lane, in flight
 
 template <class T>
@@ -289,10 +321,12 @@ __device__ __forceinline__ void copy_chunk(uint8_t* to, const uint8_t* from, int
   }
 }
 
+// (The tables fall to the last CTAs first: the first ones have the copies.)
 __device__ __forceinline__ void fork_rows(const MoveArgs& a) {
+  const unsigned last = gridDim.x - 1 - blockIdx.x;
   const int64_t all = static_cast<int64_t>(a.pairs) * max(a.width, 1);
   int bits = 0;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; e < all;
+  for (int64_t e = static_cast<int64_t>(last) * kMoveThreads + threadIdx.x; e < all;
        e += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
     const int k = static_cast<int>(e / max(a.width, 1)), c = static_cast<int>(e - static_cast<int64_t>(k) * max(a.width, 1));
     const int i = __ldg(a.parents + k);
@@ -325,9 +359,10 @@ __device__ __forceinline__ void fork_rows(const MoveArgs& a) {
 }
 
 __device__ __forceinline__ void mapped_rows(const MoveArgs& a) {
+  const unsigned last = gridDim.x - 1 - blockIdx.x;
   const int64_t all = static_cast<int64_t>(a.num_reqs) * a.width;
   const int live = __ldcg(a.live);
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; e < all;
+  for (int64_t e = static_cast<int64_t>(last) * kMoveThreads + threadIdx.x; e < all;
        e += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
     const int64_t i = e / a.width, c = e - i * a.width;
     int32_t page = __ldcg(a.table + i * a.table_stride + c);
@@ -403,20 +438,37 @@ __global__ void __launch_bounds__(kMoveThreads) release_kernel(const __grid_cons
 
 }  // namespace
 
+// A small pool is scanned by one CTA (which does without the cluster's barriers and
+// its list's way through global memory), others by a cluster.
+template <class K>
+cudaError_t launch_scan(K kernel, const ScanArgs& a, cudaStream_t s) {
+  const int cluster = a.num_pages + a.items <= kSmall ? 1 : kCluster;
+  return launch_dependent(kernel, dim3(cluster), kScanThreads, cluster, a, s);
+}
+
 cudaError_t launch_allocate(const ScanArgs& a, cudaStream_t s) {
-  return launch_dependent(claim_kernel<false>, dim3(kCluster), kScanThreads, kCluster, a, s);
+  return launch_scan(claim_kernel<false>, a, s);
 }
 
 cudaError_t launch_fork_plan(const ScanArgs& a, cudaStream_t s) {
-  return launch_dependent(claim_kernel<true>, dim3(kCluster), kScanThreads, kCluster, a, s);
+  return launch_scan(claim_kernel<true>, a, s);
 }
 
 cudaError_t launch_compact_plan(const ScanArgs& a, cudaStream_t s) {
-  return launch_dependent(plan_kernel, dim3(kCluster), kScanThreads, kCluster, a, s);
+  return launch_scan(plan_kernel, a, s);
 }
 
+// CTAs for the most items and table entries that there can be, as many as fit at
+// most.
 cudaError_t launch_move(const MoveArgs& a, int sms, cudaStream_t s) {
-  return launch_dependent(move_kernel, dim3(sms * 5), kMoveThreads, 1, a, s);
+  const int64_t pairs = a.count ? a.num_pages / 2 : a.pairs;
+  const int64_t rows = a.parents ? static_cast<int64_t>(a.pairs) * (a.width > 0 ? a.width : 1)
+                       : a.map ? static_cast<int64_t>(a.num_reqs) * a.width : 0;
+  const int64_t warps = kMoveThreads / 32;
+  const int64_t ctas = (pairs * a.chunks + warps - 1) / warps + (rows + kMoveThreads - 1) / kMoveThreads;
+  const int64_t most = static_cast<int64_t>(sms) * kMoveCtas;
+  return launch_dependent(move_kernel, dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas < most ? ctas : most)),
+                          kMoveThreads, 1, a, s);
 }
 
 cudaError_t launch_release(const ReleaseArgs& a, int sms, cudaStream_t s) {
