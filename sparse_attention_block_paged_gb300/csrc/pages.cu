@@ -23,7 +23,10 @@ constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kAhead = 8;               // loads of a lane in flight
 constexpr int kNear = 2048;             // entries of a list in shared memory
-constexpr int64_t kSmall = 16384;       // pages and entries that one CTA scans
+// Pages and entries that one CTA scans (allocation of 16 pages and compaction without
+// caches, one CTA and a cluster, us: 512 pages 5.8 and 7.4, 6.9 and 9.0; 8192 7.6 and 8.6,
+// 9.3 and 10.0; 16384 8.6 and 8.5, 16.4 and 10.8; 65536 17.9 and 9.5, 52 and 12.4).
+constexpr int64_t kSmall = 8192;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -280,12 +283,19 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const __grid_constan
     *a.moves = static_cast<int32_t>(movers.total);
   }
   // Pages that stay keep their count (or their place in the map, behind `live`).
-  for (int64_t p = all.lo + (threadIdx.x & 31); p < all.hi; p += 32) {
-    const int32_t n = __ldcg(a.refs + p);
-    if (p < live && n != 0) a.refs_out[p] = n;
-    if (p >= live && n == 0) {
-      a.refs_out[p] = 0;
-      a.map[p] = static_cast<int32_t>(p);
+  for (int64_t i = all.lo + (threadIdx.x & 31); i < all.hi; i += 32 * kAhead) {
+    int32_t n[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) n[k] = i + 32 * k < all.hi ? __ldcg(a.refs + i + 32 * k) : 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t p = i + 32 * k;
+      if (p >= all.hi) break;
+      if (p < live && n[k] != 0) a.refs_out[p] = n[k];
+      if (p >= live && n[k] == 0) {
+        a.refs_out[p] = 0;
+        a.map[p] = static_cast<int32_t>(p);
+      }
     }
   }
   cluster_sync();
@@ -302,7 +312,9 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const __grid_constan
 
 // ------------------------------------------------------------------- copies
 
-constexpr int kMoveThreads = 256, kMoveCtas = 5;   // CTAs an SM
+// CTAs an SM at most (half of 16384 pages of 128 KB live: 3, 5, 8 CTAs 185, 180 and
+// 178 us, where registers allow no more than 3).
+constexpr int kMoveThreads = 256, kMoveCtas = 8;
 constexpr int kPieces = 8;               // of a lane, in flight
 
 template <class T>
