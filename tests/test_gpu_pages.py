@@ -300,3 +300,38 @@ def test_pages_on_streams_and_graphs(mm):
     side.synchronize()
     assert t3.tolist() == rows
     mm.get_device_error()
+
+
+def test_binding_refuses_caches_and_outputs(mm):
+    r, t, n, p = gpu([1, 0, 0]), gpu([[0, -1]]), gpu([5]), gpu([0])
+    ok = torch.zeros((3, 4, 8), device="cuda")
+    wide = torch.zeros((6, 4, 8), device="cuda")
+    for bad in (ok.cpu(), ok[:2], ok[:, ::2], ok[:, :, ::2], ok[:, :1, :].expand(3, 4, 8),
+                wide.view(3, 2, 4, 8)[:, 0].transpose(0, 1)[:3], torch.zeros((), device="cuda"),
+                torch.zeros((3, 0), device="cuda"), ok[:1].expand(3, 4, 8)):
+        with pytest.raises(ValueError):
+            mm.fork_pages(r, t, n, p, [ok, bad], page_size=16)
+        with pytest.raises(ValueError):
+            mm.compact_pages(r, t, [ok, bad])
+    with pytest.raises(TypeError):
+        mm.copy_pages([ok, 3], p, p)
+    with pytest.raises(ValueError):
+        mm.copy_pages(ok, p, p)
+    with pytest.raises(ValueError):
+        mm.copy_pages([ok] * 65, p, p)
+    with pytest.raises(ValueError):
+        mm.copy_pages([], p, p)
+    for kw in (dict(out=gpu([[0, 0, 0]])), dict(out=t.long()), dict(out_lens=gpu([0, 0])),
+               dict(out=t.cpu()), dict(workspace=torch.zeros(4096, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            mm.fork_pages(r, t, n, p, [ok], page_size=16, **kw)
+    with pytest.raises(mm.Mm3idxError):
+        mm.fork_pages(r, t, n, p, [ok], page_size=16, workspace=torch.zeros(64, dtype=torch.uint8,
+                                                                            device="cuda"))
+    with pytest.raises(mm.Mm3idxError):
+        mm.fork_pages(r, t, n, p, [ok], page_size=0)
+    assert r.tolist() == [1, 0, 0] and mm.get_device_error() == 0
+    # what a page may be: strides between pages, dimensions in any order
+    for good in (ok.transpose(1, 2), wide[::2], wide.view(3, 2, 4, 8)[:, 1]):
+        mm.copy_pages([good], gpu([0]), gpu([2]))
+    assert mm.get_device_error() == 0
