@@ -610,6 +610,8 @@ int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
 
 /* ------------------------------------------------------------------------
  * The life of a paged cache: pages taken, written, shared and given back.
+ * Calls on one pool (its counts, tables and caches) must follow one another on
+ * the GPU, as those that share a workspace must.
  * ------------------------------------------------------------------------ */
 
 #define MM3IDX_ERR_PAGES (-17) /* page pool: cache count, page bytes, strides, page size or table not served */
@@ -696,7 +698,8 @@ typedef struct mm3idx_append {
 int mm3idx_append_kv(const mm3idx_append_t *a, void *stream);
 
 /* One cache of a page pool: page p is the page_bytes bytes from data + p *
- * page_stride. */
+ * page_stride.  Caches of one call must not overlap: keys and values that lie next
+ * to each other in one block are one cache of such blocks. */
 typedef struct mm3idx_cache {
     void          *data;           /* device pointer                                        */
     int64_t        page_stride;    /* bytes, >= page_bytes                                  */

@@ -1043,6 +1043,9 @@ def fork_pages(refs, page_table, seq_lens, parents, caches, *, page_size, out=No
     ``caches`` (up to 64 tensors [num_pages, ...], pages without gaps) into a
     free one.  Returns (table int32 [forks, columns], lengths int32 [forks]).
 
+    Keys and values next to each other in one block are one cache of such blocks.
+    Calls on one pool must follow one another on the GPU.
+
     ``out`` / ``out_lens`` may be other rows of ``page_table`` and ``seq_lens``
     than the parents', e.g. a batch's free slots; what they held is not
     released."""
