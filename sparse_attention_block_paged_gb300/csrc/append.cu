@@ -34,6 +34,15 @@ __device__ __forceinline__ float2 floats(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// The larger of two pairs; a NaN loses.
+template <bool BF16>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t halves(float lo, float hi) {
   uint32_t r;
@@ -205,8 +214,20 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
       return top;
     };
     float top = 0.0f;
+    if constexpr (UNIT) {              // as they came, two at a time
+      uint32_t two = 0;
 #pragma unroll
-    for (int m = 0; m < N; ++m) top = larger(top, v[m], false);
+      for (int m = 0; m < N; ++m) {
+        const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) two = larger2<BF16>(two, w[e] & 0x7fff7fffu);
+      }
+      const float2 f = floats<BF16>(two);
+      top = fmaxf(f.x, f.y);
+    } else {
+#pragma unroll
+      for (int m = 0; m < N; ++m) top = larger(top, v[m], false);
+    }
     top = joined(top);
     bool again = top == INFINITY;
     if constexpr (G > 32) again = __syncthreads_or(again);

@@ -124,6 +124,7 @@ struct Cfg {
   static constexpr int kPages = kTile / 16;        // most pages of a tile
   static constexpr int kSmem = oScale + (SC ? kSlots / 2 * kPages * 16 : 0) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert((!SC || oScale % 16 == 0) && oMisc % 8 == 0 && oBar % 8 == 0, "alignment");
 };
 
 template <int V>
