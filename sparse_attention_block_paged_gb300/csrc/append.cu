@@ -13,11 +13,15 @@
 // for a decode step a chain of dependent loads (length, page, old scale).  So a
 // (page, head) of the keys or of the values is one group of threads' that holds
 // its new elements in registers between the maximum and the rounding: one pass
-// over the data, nothing exchanged between CTAs.  A thread holds four pieces of
-// 16 bytes at most, so that a whole SM of threads fits, and asks for them as soon
-// as it knows the length, before the page table (with eight pieces, two CTAs of
-// 256 threads an SM and the page first, four prompts of 8192 tokens took 104 us;
-// now see below).
+// over the data, nothing exchanged between CTAs.  Elements are asked for as soon as
+// the length is known, before the page table; what is rare (an infinity, an old
+// scale that is no power of two) reads them again instead of holding registers.
+//
+// What it measured (GB300): four prompts of 8192 tokens, 8 heads of 128, into e4m3
+// pages of 64: 32 us (92 % of the measured copy rate; with the page first, 107
+// registers and two CTAs an SM 104 us); pieces of 32 prompts, 134 MB, in 16 bits: 22 us
+// (90 %); a decode step's tokens (64 x 1, 2 heads): 2.0 us; 256 x 4 drafts, 8 heads
+// of 64: 3.5 us, both a chain of four dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,6 +30,7 @@
 namespace mm3idx {
 namespace {
 
+constexpr int kThreads = 256;
 constexpr float kLowScale = 0x1p-60f, kHighScale = 0x1p60f;
 
 template <bool BF16>
@@ -96,10 +101,8 @@ enum { kCopy = 0, kCodes = 1, kScaled = 2 };
 // with scales.  UNIT: both divisors are 1.  G: threads a (page, head).  N: pieces of
 // 16 bytes a thread.
 template <bool BF16, int MODE, bool UNIT, int G, int N>
-__global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 ? 3 : 6)
-                                                      : G > 256 ? 2 : 5)
+__global__ void __launch_bounds__(kThreads, N > 4 ? 4 : MODE == kScaled ? 5 : 6)
     append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kThreads = G > 256 ? G : 256;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float tops[kThreads / 32];
@@ -287,23 +290,24 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, MODE != kScaled ? (G > 256 
 
 template <bool BF16, int MODE, bool UNIT, int G, int N>
 cudaError_t launch_group(const AppendArgs& a, cudaStream_t s) {
-  constexpr int kThreads = G > 256 ? G : 256, per = kThreads / G;
+  constexpr int per = kThreads / G;
   return launch_dependent(append_kernel<BF16, MODE, UNIT, G, N>, dim3((a.units - 1) / per + 1),
                           kThreads, 1, a, s);
 }
 
-// The fewest threads that hold the most new tokens of a page, four pieces each; a
-// warp less than that.
+// The threads that hold the most new tokens of a page, eight pieces each (few
+// tokens: one or four pieces of one warp).  Four prompts of 8192 tokens, pages of
+// 64: 256 threads with four pieces 35.7 us, 128 with eight 32.1, 512 with two 64.
 template <bool BF16, int MODE, bool UNIT>
 cudaError_t launch_mode(const AppendArgs& a, cudaStream_t s) {
   const int page = 1 << a.page_shift;
   const int pieces = (a.query_len < page ? a.query_len : page) * (a.head_dim / 8);
   if (pieces <= 32) return launch_group<BF16, MODE, UNIT, 32, 1>(a, s);
   if (pieces <= 128) return launch_group<BF16, MODE, UNIT, 32, 4>(a, s);
-  if (pieces <= 256) return launch_group<BF16, MODE, UNIT, 64, 4>(a, s);
-  if (pieces <= 512) return launch_group<BF16, MODE, UNIT, 128, 4>(a, s);
-  if (pieces <= 1024) return launch_group<BF16, MODE, UNIT, 256, 4>(a, s);
-  return launch_group<BF16, MODE, UNIT, 512, 4>(a, s);
+  if (pieces <= 256) return launch_group<BF16, MODE, UNIT, 32, 8>(a, s);
+  if (pieces <= 512) return launch_group<BF16, MODE, UNIT, 64, 8>(a, s);
+  if (pieces <= 1024) return launch_group<BF16, MODE, UNIT, 128, 8>(a, s);
+  return launch_group<BF16, MODE, UNIT, 256, 8>(a, s);
 }
 
 template <bool BF16, bool UNIT>
