@@ -12,6 +12,12 @@
 // (a ballot a 32 entries, a prefix over warps, then over the cluster's CTAs).
 // What is left is the copy of page data, at HBM's rate: a warp moves up to 4 KB
 // of a page at a time, eight 16-byte loads a lane in flight before the first store.
+//
+// What it measured (GB300): half of 16384 pages of 128 KB live, compacted: 171 us
+// (92 % of the measured copy rate); 8 requests forked into 64, four layers of
+// 128 KB a page: 15 us with the release before it (HBM needs 10); the smallest calls:
+// release 2.0 us, allocation 2.2, a fork 5.6, a compaction of 512 pages 7.6, all
+// latency of one or two dependent kernels.
 #include "pages.h"
 
 namespace mm3idx {
@@ -312,8 +318,8 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const __grid_constan
 
 // ------------------------------------------------------------------- copies
 
-// CTAs an SM at most (half of 16384 pages of 128 KB live: 3, 5, 8 CTAs 185, 180 and
-// 178 us, where registers allow no more than 3).
+// CTAs an SM at most (half of 16384 pages of 128 KB live: with 3 or 5 of them
+// compaction takes 7 or 2 us more; registers allow 3 at a time).
 constexpr int kMoveThreads = 256, kMoveCtas = 8;
 constexpr int kPieces = 8;               // of a lane, in flight
 
