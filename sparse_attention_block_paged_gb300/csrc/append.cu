@@ -121,13 +121,13 @@ __global__ void __launch_bounds__(kThreads, N > 4 ? 4 : MODE == kScaled ? 5 : 6)
   int from = 0, pieces = 0, column = 0, bits = 0;
   int64_t row = 0;
   if (unit < a.units) {
-    const int raw = __ldg(a.seq_lens + req);
+    const int raw = a.seq_lens[req];
     const int len = min(max(raw, 0), a.max_seq_len);
     int rows = a.query_len;
     bits = raw > a.max_seq_len ? MM3IDX_DEV_SEQ_TOO_LONG : 0;
     int64_t row0 = static_cast<int64_t>(req) * a.query_len;
     if (a.cu) {
-      const int c0 = __ldg(a.cu + req), c1 = __ldg(a.cu + req + 1);
+      const int c0 = a.cu[req], c1 = a.cu[req + 1];
       const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total_q && c1 - c0 <= a.query_len;
       if (!ok || (req == 0 && c0 != 0) || (req == a.num_reqs - 1 && c1 != a.total_q))
         bits |= MM3IDX_DEV_BAD_ROWS;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, N > 4 ? 4 : MODE == kScaled ? 5 : 6)
   for (int m = 0; m < N; ++m) v[m] = load(m);
   int page = -1;
   if (pieces > 0) {
-    page = __ldg(a.table + req * a.table_stride + column);
+    page = a.table[req * a.table_stride + column];
     if (page < 0 || page >= a.num_pages) {
       bits |= MM3IDX_DEV_BAD_PAGE;
       pieces = 0;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, N > 4 ? 4 : MODE == kScaled ? 5 : 6)
   By to_codes{1.0f, 1.0f, true};
   if constexpr (MODE == kScaled) {
     float* at = side.scales + page * side.s_page + head * side.s_head;
-    const float old = pieces > 0 && from > 0 ? fminf(fmaxf(*at, kLowScale), kHighScale) : 0.0f;
+    const float old = pieces > 0 && from > 0 ? fminf(fmaxf(__ldcg(at), kLowScale), kHighScale) : 0.0f;
     // The largest magnitude (a maximum passes over NaN); where that is infinite,
     // once more without the infinities, from memory (registers are not indexed).
     auto larger = [&](float top, uint4 q, bool finite) {

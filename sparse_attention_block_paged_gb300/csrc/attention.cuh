@@ -523,7 +523,7 @@ __device__ __forceinline__ void load_scales(const AttentionArgs& a, Walker walk,
     auto ids_from = [&](int p) { return p + lane < pages ? __ldg(table + p + lane) : -1; };
     auto both_of = [&](int id) {
       if (id < 0 || id >= a.num_pages) return make_float2(1.0f, 1.0f);
-      return make_float2(__ldg(ks + id * a.ks_page), __ldg(vs + id * a.vs_page));
+      return make_float2(__ldcg(ks + id * a.ks_page), __ldcg(vs + id * a.vs_page));
     };
     int ids = ids_from(sg.b0 * per + 32), k = 0;
     float2 now = both_of(ids_from(sg.b0 * per)), next = make_float2(1.0f, 1.0f);

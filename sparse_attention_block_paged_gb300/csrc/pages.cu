@@ -23,6 +23,9 @@
 namespace mm3idx {
 namespace {
 
+// Counts, tables and lengths are what the kernels before wrote, some of them on
+// other SMs in the lines of what is read here: L2 is where they are read.
+
 // ------------------------------------------------------------ ordered scans
 
 constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
@@ -176,7 +179,7 @@ __device__ __forceinline__ void prefixes(Counts* c, const int64_t (&mine)[N], Pa
 }
 
 __device__ __forceinline__ int clamped_len(const ScanArgs& a, int i, bool* over) {
-  const int raw = max(__ldg(a.seq_lens + i), 0);
+  const int raw = max(__ldcg(a.seq_lens + i), 0);
   const int64_t most = static_cast<int64_t>(a.width) * a.page_size;
   *over = raw > most;
   return static_cast<int>(min(static_cast<int64_t>(raw), most));
@@ -196,12 +199,12 @@ __device__ __forceinline__ int32_t* allocation_entry(const ScanArgs& a, int64_t 
 
 // The partly filled last page of fork k's parent, or -1.
 __device__ __forceinline__ int last_page(const ScanArgs& a, int64_t k) {
-  const int i = __ldg(a.parents + k);
+  const int i = __ldcg(a.parents + k);
   if (i < 0 || i >= a.num_reqs) return -1;
   bool over;
   const int len = clamped_len(a, i, &over), full = len / a.page_size;
   if (full * a.page_size == len) return -1;
-  const int page = __ldg(a.table + i * a.table_stride + full);
+  const int page = __ldcg(a.table + i * a.table_stride + full);
   return page >= 0 && page < a.num_pages ? page : -1;
 }
 
@@ -347,11 +350,11 @@ __device__ __forceinline__ void fork_rows(const MoveArgs& a) {
   for (int64_t e = static_cast<int64_t>(last) * kMoveThreads + threadIdx.x; e < all;
        e += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
     const int k = static_cast<int>(e / max(a.width, 1)), c = static_cast<int>(e - static_cast<int64_t>(k) * max(a.width, 1));
-    const int i = __ldg(a.parents + k);
+    const int i = __ldcg(a.parents + k);
     int len = 0;
     if (i >= a.num_reqs) bits |= MM3IDX_DEV_BAD_ROWS;
     if (i >= 0 && i < a.num_reqs) {
-      const int64_t raw = max(__ldg(a.seq_lens + i), 0);
+      const int64_t raw = max(__ldcg(a.seq_lens + i), 0);
       const int64_t most = static_cast<int64_t>(a.width) * a.page_size;
       if (raw > most) bits |= MM3IDX_DEV_SEQ_TOO_LONG;
       len = static_cast<int>(min(raw, most));
@@ -361,7 +364,7 @@ __device__ __forceinline__ void fork_rows(const MoveArgs& a) {
     const int full = len / a.page_size;
     int32_t page = -1;
     if (c < full || (c == full && full * a.page_size < len)) {
-      page = __ldg(a.table + i * a.table_stride + c);
+      page = __ldcg(a.table + i * a.table_stride + c);
       if (page < 0 || page >= a.num_pages) {
         bits |= MM3IDX_DEV_BAD_PAGE;
         page = -1;
@@ -435,10 +438,10 @@ __global__ void __launch_bounds__(kMoveThreads) release_kernel(const __grid_cons
        e += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
     const int64_t i = e / a.width, c = e - i * a.width;
     if (a.seq_lens) {
-      const int64_t len = max(__ldg(a.seq_lens + i), 0);
+      const int64_t len = max(__ldcg(a.seq_lens + i), 0);
       if (c >= (len + a.page_size - 1) / a.page_size) continue;
     }
-    const int32_t page = __ldg(a.table + i * a.table_stride + c);
+    const int32_t page = __ldcg(a.table + i * a.table_stride + c);
     if (page < 0) continue;
     if (page >= a.num_pages) {
       bits |= MM3IDX_DEV_BAD_PAGE;
