@@ -847,7 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     bool more = walk.next(a, sg);
-    if (more) load_queries(sg);
+    // Scaled pages: a segment's queries are read at its start.  (The next one's read
+    // before the join made the compiler copy the queries' registers in every tile:
+    // 185 us for 64 x 4 rows over 4K to 32K tokens instead of 172.)
+    if (!SC && more) load_queries(sg);
     while (more) {
       const int head = sg.head, row0 = sg.row0;
       const int rows = min(64, R - row0);                  // of this task
@@ -862,6 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_lo = shift + j_lo, lim_hi = shift + j_hi;
       const bool idle = row0 + rt * 16 >= R;               // no row of this 16-row tile
 
+      if constexpr (SC) load_queries(sg);
       float sc_a = a.scale * kLog2e, sc_b = sc_a;
       if constexpr (kByte) {
         // fp16 queries, each row scaled by the power of two that brings its
@@ -937,7 +941,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.0f;
-        if (live) {
+        // (Scaled pages: scores that are not live are replaced below, and no branch
+        // here spares the zeros and the spills that one costs: 169 us instead of 172.)
+        if (SC || live) {
           // All slices at once: 2 NS chains of products.  What lies behind the
           // last token may be anything; its scores are replaced below.
           const uint32_t kbase = ring + slot * C::kSlot + koff;
@@ -1206,10 +1212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&empty[bar]);
         next_slot();
       }
-      // The next segment's queries are under way during the join.
+      // The next segment's queries are under way during the join (pages without scales).
       Segment after;
       more = walk.next(a, after);
-      if (more) load_queries(after);
+      if (!SC && more) load_queries(after);
 
       // ------------------------------------------------ join of the warps
       // Quad sums of l, then the warps' triples through shared memory, 32
