@@ -398,6 +398,16 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "memory");
 }
 
+// Bytes of 16 rows by 32 columns, transposed: the lane's are rows 4 c .. 4 c + 3 of
+// columns g, g + 8, g + 16, g + 24.  Lane l gives the address of 16 bytes: row
+// l mod 16, columns 16 (l / 16) on.
+__device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -793,6 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // instructions, unused, cost the e4m3 batch above 236 us instead of 223.)
     constexpr bool rest = !kByte || Q == MM3IDX_TYPE_FP16;
 
+    // The tokens of a lane's scores in a slice: kCol c, kStep further, and the one
+    // behind each.  Scaled pages: four tokens in a row, so that one transposed load of
+    // bytes has the pairs of the second product (112 instructions of 1110 a warp and
+    // tile less than words of two tokens, interleaved).
+    constexpr int kCol = SC ? 4 : 2, kStep = SC ? 2 : 8;
     // Offsets of this lane in a slot for slice 0 of its tokens.  A 16-byte
     // piece p of a row lies at p xor (row mod 8) (swizzled copies); slices and
     // k-steps only add rows or flip bits of p, so the rest are constants.
@@ -803,9 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       koff = twisted((first + ((lane >> 4) << 3) + (lane & 7)) * C::kRow + ((lane >> 3) & 1) * 16);
       voff0 = twisted((first + (lane & 15)) * C::kRow + (lane >> 4) * 16);
     } else {
-      koff = twisted((first + g) * C::kRow + c * (D / 4));
-      voff0 = twisted((first + 2 * c) * C::kRow + g * 4);
-      voff1 = twisted((first + 2 * c + 1) * C::kRow + g * 4);
+      koff = twisted((first + (SC ? (g >> 1) * 4 + (g & 1) : g)) * C::kRow + c * (D / 4));
+      voff0 = twisted(SC ? (first + (lane & 15)) * C::kRow + (lane >> 4) * 16
+                         : (first + 2 * c) * C::kRow + g * 4);
+      voff1 = SC ? 0 : twisted((first + 2 * c + 1) * C::kRow + g * 4);
     }
 
     const int R = a.group * a.query_len;
@@ -969,7 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  w[n][x] = lds128((kbase ^ (16 * u)) + (n * 16 + 8 * x) * C::kRow);
+                  w[n][x] = SC ? lds128((kbase ^ (16 * u) ^ (x * C::kRow / 4)) +
+                                        (n * 16 + 2 * x) * C::kRow)
+                               : lds128((kbase ^ (16 * u)) + (n * 16 + 8 * x) * C::kRow);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -1003,12 +1021,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool on = live && t0 + n * 16 < lim_hi &&
                             ((pages >> ((first + n * 16) >> a.page_shift)) & 1u);
             if (!on) act &= ~(1u << n);
-            const int t = t0 + n * 16 + 2 * c;
+            const int t = t0 + n * 16 + kCol * c;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (!on || t + 8 * x + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][x][e] = -INFINITY;
+                if (!on || t + kStep * x + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][x][e] = -INFINITY;
           }
         }
         float top_a = -INFINITY, top_b = -INFINITY;
@@ -1115,6 +1133,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (!kByte) {
             ldmatrix4_trans(((vbase + voff0) ^ ((2 * u & 7) << 4)) + (u >> 2) * C::kHalf +
                                 at * C::kRow, r);
+          } else if constexpr (SC) {
+            uint32_t w[4];
+            ldmatrix_bytes_trans(((vbase + voff0) ^ (u * 32)) + at * C::kRow, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              r[2 * k] = widen_lo(w[k]);
+              r[2 * k + 1] = widen_hi(w[k]);
+            }
           } else {
             const uint32_t even = (vbase + voff0) ^ (u * 32), odd = (vbase + voff1) ^ (u * 32);
             uint32_t w[4];
@@ -1181,11 +1207,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (rest) prn[e] = pr[x][e];
                 }
               }
-            const int t = t0 + n * 16 + 2 * c;
+            const int t = t0 + n * 16 + kCol * c;
 #pragma unroll 1
             for (int j = j_lo; j <= j_hi; ++j) {
               const int end = shift + j;
-              const uint32_t k0 = below(t, end), k1 = below(t + 8, end);
+              const uint32_t k0 = below(t, end), k1 = below(t + kStep, end);
 #pragma unroll
               for (int u = 0; u < NU; ++u) {
                 uint32_t r[2 * TU];
@@ -1283,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float(&o)[4] = st.o[u * 4 + k];
-            if constexpr (!kByte) {
+            if constexpr (!kByte || SC) {
               *reinterpret_cast<float2*>(mine + g * kRedStride + 8 * k + 2 * c) =
                   make_float2(o[0] * fa, o[1] * fa);
               *reinterpret_cast<float2*>(mine + (g + 8) * kRedStride + 8 * k + 2 * c) =
