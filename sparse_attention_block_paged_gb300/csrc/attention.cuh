@@ -1029,6 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!on || t + kStep * x + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][x][e] = -INFINITY;
           }
         }
+        // Scaled pages wait for the values here: the exponentials then lie next to the
+        // second product (161 -> 153 us).
+        if (SC && !dead) dead = !all_wait(&full[bar], phase, abort_flag);
         float top_a = -INFINITY, top_b = -INFINITY;
         if constexpr (SC) {
 #pragma unroll
@@ -1109,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         st.l1 += sum_b;
 
         // ------------------------------------------------------- values
-        if (!dead) dead = !all_wait(&full[bar], phase, abort_flag);
+        if (!SC && !dead) dead = !all_wait(&full[bar], phase, abort_flag);
         const uint32_t vbase = ring + slot * C::kSlot;
         if (weigh) {
           // (the values' arrival says that the slot's last weights were read)
