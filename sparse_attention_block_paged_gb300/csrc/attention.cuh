@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 16-bit D = 128 and 64 where a tile is half the bytes (or RT = 4).
   constexpr int ALT = (C::kSlot == 32768 ? 2 : 4) / RT > 1 ? (C::kSlot == 32768 ? 2 : 4) / RT : 1;
   static_assert(NB / 2 % ALT == 0, "a barrier belongs to one group of warps");
+  static_assert(2 * ALT <= S, "a step is at most one round of the ring");
   constexpr int TG = TJ / ALT;                      // token groups of a tile
   constexpr int NS = 8 / TG;                        // 16-token slices of a warp
   constexpr int NT = D / 8;                         // output tiles of 8 columns
@@ -926,7 +927,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       st.m0 = st.m1 = -INFINITY;
       st.l0 = st.l1 = 0.0f;
 
-      for (int b = sg.b0; b < sg.b1; ++b) {
+      // Slots and barriers on or back, at most one round.
+      auto ahead = [&](uint32_t n) {
+        slot += n;
+        if (slot >= S) slot -= S;
+        bar += n;
+        if (bar >= NB) {
+          bar -= NB;
+          phase ^= 1;
+        }
+      };
+      auto back = [&](uint32_t n) {
+        if (slot < n) slot += S;
+        slot -= n;
+        if (bar < n) {
+          bar += NB;
+          phase ^= 1;
+        }
+        bar -= n;
+      };
+      // A warp takes every ALT-th tile.  Scaled pages: it steps from one of its tiles to
+      // the next; elsewhere it passes over the others one by one (64 x 4 rows, 4K to 32K
+      // tokens, with scales: 149 us against 153; 64 x 4 rows of 16 selected blocks,
+      // 16 bits: 151 against 144).
+      constexpr int kEvery = SC ? ALT : 1;
+      int b = sg.b0;
+      if constexpr (SC) {
+        const uint32_t skip = (alt + ALT - turn) % ALT;
+        turn = (turn + sg.b1 - sg.b0) % ALT;
+        b += skip;
+        ahead(2 * skip);
+      }
+      for (; b < sg.b1; b += kEvery) {
         auto next_slot = [&] {      // to the next tile's keys
           if (++slot >= S) slot = 0;
           if (++bar >= NB) {
@@ -934,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         };
-        if constexpr (ALT > 1) {
+        if constexpr (!SC && ALT > 1) {
           const bool mine = turn == alt;
           turn = (turn + 1) % ALT;
           if (!mine) {
@@ -1239,8 +1271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[bar]);
-        next_slot();
+        if constexpr (SC) ahead(2 * ALT - 1);
+        else next_slot();
       }
+      if constexpr (SC) back(2 * static_cast<uint32_t>(b - sg.b1));   // to the next segment's first
       // The next segment's queries are under way during the join (pages without scales).
       Segment after;
       more = walk.next(a, after);
