@@ -65,8 +65,8 @@
 // tokens, 8 heads a kv head, bf16: 189 us (94 %); 16 x 32K-128K e4m3: 214 us
 // (93 %); 64 x 4 rows of 16 selected blocks: 145 us; one request of 128K
 // tokens, head_dim 64, pages of 16: 48 us (82 %; 9 us of it start and join);
-// 8 x 128K: 310 us (100 %).  With a scale for each page and head: 16 x 32K-128K 220 us
-// (98 %); 64 x 4 rows 153 us (60 %: 32 rows are bound by the consumers); head_dim 64,
+// 8 x 128K: 310 us (100 %).  With a scale for each page and head: 16 x 32K-128K 222 us
+// (97 %); 64 x 4 rows 149 us (62 %: 32 rows are bound by the consumers); head_dim 64,
 // pages of 16 43 us (copies of 1 KB).  From L2 (no HBM) a 64 KB tile takes 0.80 us with
 // up to 16 rows, 1.41 with 32 and 2.26 with 64, against 1.47 us at the HBM
 // rate: 64 rows are bound by the products.
