@@ -619,7 +619,8 @@ int mm3idx_verify_drafts(const mm3idx_drafts_t *d, void *stream);
 #define MM3IDX_MAX_CACHES 64   /* caches of one page pool that a call takes     */
 
 /* One fp32 scale a page and kv head of an e4m3 cache.  Host struct of device
- * pointers (4-byte aligned); strides count elements and are >= 0.  Scales
+ * pointers (4-byte aligned); strides count elements and are >= 0 (0 in a call
+ * that only reads them: pages or heads with a scale in common).  Scales
  * are used as if clamped to [2^-60, 2^60] (NaN: 2^-60). */
 typedef struct mm3idx_kv_scales {
     float  *k;                     /* [num_pages, kv_heads]                                 */
@@ -693,7 +694,11 @@ typedef struct mm3idx_append {
  *                    saturated.
  * Nothing else of a page is written.  A page that gets tokens must belong to
  * one request alone (mm3idx_fork_pages gives a request its own last page).
- * Inputs must not overlap the caches.
+ * Inputs must not overlap the caches, nor the caches each other.  Scales are
+ * written: no two of the 2 * num_pages * kv_heads may be the same float
+ * (MM3IDX_ERR_ATTENTION_LAYOUT; so is one cache given for both sides, with
+ * scales).  Where the strides of the two sides differ, they must lie in ranges of
+ * memory that do not overlap.
  */
 int mm3idx_append_kv(const mm3idx_append_t *a, void *stream);
 

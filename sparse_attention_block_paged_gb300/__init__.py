@@ -889,7 +889,8 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_lens, *, query_len, max
     (0: an empty slot, its rows become 0).  Returns ``out``, like q.
 
     ``k_scales`` and ``v_scales``, fp32 [pages, kv_heads]: scales of each page
-    and head of float8_e4m3fn caches, as :func:`append_kv` writes them.
+    and head of float8_e4m3fn caches, as :func:`append_kv` writes them (or
+    broadcast: they are only read here).
 
     ``lse`` fp32 [rows, q_heads] and ``block_weights`` fp32 [rows,
     cdiv(max_seq_len, 128)] are written when given: the log-sum-exp of each
@@ -989,7 +990,8 @@ def append_kv(k, v, k_cache, v_cache, page_table, seq_lens, *, query_len, max_se
     tokens' scale; in others it only grows, and the older codes follow it.
 
     Pages that get tokens must not be shared (:func:`fork_pages` copies the
-    one that its new rows go on with)."""
+    one that its new rows go on with), nor caches overlap.  Scales are written: a
+    broadcast tensor, or one for both sides, is refused."""
     with _HERE if stream is None else _run_on(stream, k):
         _binding.append_kv(k, v, k_cache, v_cache, page_table, seq_lens, query_len, max_seq_len,
                            k_scale, v_scale, k_scales, v_scales, cu_seqlens_q)

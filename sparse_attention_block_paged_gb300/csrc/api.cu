@@ -688,7 +688,8 @@ const char* mm3idx_status_string(int status) {
       return "attention serves q_heads a multiple of kv_heads, head_dim 64 or 128, pages of 16, 32, 64 or 128 tokens, "
              "bf16 or fp16 queries over keys and values of the same type or e4m3";
     case MM3IDX_ERR_ATTENTION_LAYOUT:
-      return "attention tensors must be 16-byte aligned with strides that are multiples of 16 bytes, and outputs must not overlap";
+      return "attention tensors must be 16-byte aligned with strides that are multiples of 16 bytes, and outputs "
+             "(appended tokens' scales among them) must not overlap";
     case MM3IDX_ERR_BUDGET:
       return "eviction needs init >= 0, local >= 1, init + local <= budget and a decay in 0..1";
     case MM3IDX_ERR_VOCAB:

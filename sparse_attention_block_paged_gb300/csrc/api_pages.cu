@@ -5,6 +5,8 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <numeric>
 
 #include "pages.h"
 
@@ -23,6 +25,32 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 bool stride16(int64_t stride, int bytes) { return stride > 0 && stride * bytes % 16 == 0; }
 
 constexpr int32_t kMaxPages = 1 << 30, kMaxReqs = 1 << 20;
+
+// One side's scales [pages, heads]: are they all different floats?  The first two
+// pairs that meet are hs / g pages and ps / g heads apart, g the strides' common divisor.
+bool own_floats(int64_t pages, int64_t heads, int64_t ps, int64_t hs) {
+  if (pages == 1) ps = 0;
+  if (heads == 1) hs = 0;
+  const int64_t g = std::gcd(ps, hs);
+  return g == 0 ? pages * heads == 1 : hs / g >= pages || ps / g >= heads;
+}
+
+// Keys' and values' scales, each of own floats: is no float one of both?  Sides of
+// unlike strides have to lie in ranges of their own.
+bool no_common_float(const mm3idx_kv_scales_t& s, int64_t pages, int64_t heads) {
+  const int64_t ps = pages > 1 ? s.k_page_stride : 0, hs = heads > 1 ? s.k_head_stride : 0;
+  const int64_t pv = pages > 1 ? s.v_page_stride : 0, hv = heads > 1 ? s.v_head_stride : 0;
+  const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(s.v) -
+                                           reinterpret_cast<uintptr_t>(s.k)) / 4;
+  if (off > (pages - 1) * ps + (heads - 1) * hs || -off > (pages - 1) * pv + (heads - 1) * hv)
+    return true;
+  if (ps != pv || hs != hv) return false;
+  for (int64_t h = 1 - heads; h < heads; ++h) {      // a head apart, and how many pages?
+    const int64_t rest = off - h * hs;
+    if (rest == 0 || (ps != 0 && rest % ps == 0 && std::abs(rest / ps) < pages)) return false;
+  }
+  return true;
+}
 
 int check_append(const mm3idx_append_t* a) {
   if (!a || a->num_reqs < 0) return MM3IDX_ERR_INVALID_ARGUMENT;
@@ -63,7 +91,9 @@ int check_append(const mm3idx_append_t* a) {
     return MM3IDX_ERR_ATTENTION_LAYOUT;
   if (scaled && (!aligned4(a->scales.k, a->scales.v) || a->scales.k_page_stride < 0 ||
                  a->scales.k_head_stride < 0 || a->scales.v_page_stride < 0 ||
-                 a->scales.v_head_stride < 0))
+                 a->scales.v_head_stride < 0 ||
+                 !own_floats(a->num_pages, a->kv_heads, a->scales.k_page_stride, a->scales.k_head_stride) ||
+                 !own_floats(a->num_pages, a->kv_heads, a->scales.v_page_stride, a->scales.v_head_stride)))
     return MM3IDX_ERR_ATTENTION_LAYOUT;
   if (a->table_width < cdiv(a->max_seq_len, a->page_size) || a->table_stride < a->table_width)
     return MM3IDX_ERR_TABLE_LAYOUT;
@@ -157,6 +187,9 @@ int mm3idx_append_kv(const mm3idx_append_t* p, void* stream) {
   int rc = check_append(p);
   if (rc) return rc;
   if (p->num_reqs == 0 || p->total_q == 0) return MM3IDX_OK;
+  // the codes of a page follow its scale: what another group writes too ends up wrong
+  if (p->scales.k && (p->k_cache == p->v_cache || !no_common_float(p->scales, p->num_pages, p->kv_heads)))
+    return MM3IDX_ERR_ATTENTION_LAYOUT;
   int sms = 0;
   int32_t* status = nullptr;
   if ((rc = library_device(&sms, &status))) return rc;
