@@ -765,7 +765,12 @@ int mm3idx_release_pages(const mm3idx_pool_t *p, void *stream);
  * (MM3IDX_DEV_SEQ_TOO_LONG).  What rows of `out` and out_lens held before is
  * not released.  They must not overlap rows that are parents in this call, nor
  * anything else that is read; other rows of p->page_table and p->seq_lens they
- * may be.  num_caches 0..MM3IDX_MAX_CACHES; num_forks 0..2^20.
+ * may be.  The parents' pages must be in use (fork first, then release rows that
+ * end): a free page may be taken for a copy while it is read.
+ * num_caches 0..MM3IDX_MAX_CACHES; num_forks 0..2^20.  In a pool of more caches
+ * mm3idx_copy_pages copies the others' last pages: of each k whose out_lens[k] is no
+ * multiple of page_size, with c = out_lens[k] / page_size, from page_table[parents[k], c]
+ * to out[k, c].
  */
 int mm3idx_fork_pages(const mm3idx_pool_t *p, const int32_t *parents, int32_t num_forks,
                       int32_t *out, int64_t out_stride, int32_t *out_lens,
@@ -778,7 +783,9 @@ int mm3idx_fork_pages(const mm3idx_pool_t *p, const int32_t *parents, int32_t nu
  * to the k-th free one before L; pages before L stay.  refs_out and table_out
  * (which may be p->refs and p->page_table with its stride) get the counts and
  * the table (all columns; entries that name a free page, or none, stay) as they
- * then are, *live (an int32 on the device) L.
+ * then are, *live (an int32 on the device) L.  What moves depends on p->refs
+ * alone: in a pool of more than MM3IDX_MAX_CACHES caches call it for each part of them,
+ * with p->refs as it was (only the last call may overwrite it).
  */
 int mm3idx_compact_pages(const mm3idx_pool_t *p, int32_t *refs_out, int32_t *table_out,
                          int64_t table_out_stride, int32_t *live, const mm3idx_cache_t *caches,

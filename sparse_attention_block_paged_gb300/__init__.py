@@ -1050,7 +1050,12 @@ def fork_pages(refs, page_table, seq_lens, parents, caches, *, page_size, out=No
 
     ``out`` / ``out_lens`` may be other rows of ``page_table`` and ``seq_lens``
     than the parents', e.g. a batch's free slots; what they held is not
-    released."""
+    released.  The parents' pages must be in use: release rows that end after the
+    fork.
+
+    The last pages of more caches than a call takes go by :func:`copy_pages`: of
+    each row k whose length is no multiple of ``page_size``, column ``length //
+    page_size`` of row ``parents[k]`` to that column of row k (-1 elsewhere)."""
     with _HERE if stream is None else _run_on(stream, refs):
         return _binding.fork_pages(refs, page_table, seq_lens, parents, caches, page_size, out,
                                    out_lens, workspace)
@@ -1069,7 +1074,9 @@ def compact_pages(refs, page_table, caches, *, in_place=False, workspace=None, s
     ``caches`` (up to 64 tensors [num_pages, ...], pages without gaps): the k-th of
     those from L on goes to the k-th free one before L.  Returns a
     :class:`Compaction`; ``refs`` and ``page_table`` (all tables of the pool, as
-    rows of one tensor) are left as they are, or with ``in_place`` overwritten."""
+    rows of one tensor) are left as they are, or with ``in_place`` overwritten.
+    With more caches call it for each part of them, all but the last time without
+    ``in_place``: the same pages move."""
     with _HERE if stream is None else _run_on(stream, refs):
         return tuple.__new__(Compaction, _binding.compact_pages(refs, page_table, caches, in_place,
                                                                 workspace))
