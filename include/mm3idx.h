@@ -87,9 +87,9 @@ extern "C" {
 #define MM3IDX_DEV_SEQ_TOO_SHORT 4  /* seq_lens[i] < query_len              */
 #define MM3IDX_DEV_TIMEOUT       8  /* an on-chip pipeline wait gave up; outputs of that launch are invalid */
 #define MM3IDX_DEV_BAD_ROWS     16  /* ragged calls: cu_seqlens_q does not run from 0 to total_q without decreasing */
+#define MM3IDX_DEV_BAD_TOKEN    32  /* mm3idx_verify_drafts: a drafted token outside [0, vocab) (rejected) */
 #define MM3IDX_DEV_NO_PAGES     64  /* page pool: fewer free pages than were asked for */
 #define MM3IDX_DEV_NOT_HELD    128  /* mm3idx_release_pages: a page without a reference (left at 0) */
-#define MM3IDX_DEV_BAD_TOKEN    32  /* mm3idx_verify_drafts: a drafted token outside [0, vocab) (rejected) */
 
 #define MM3IDX_MAX_TOPK            32  /* largest topk served                  */
 #define MM3IDX_MAX_DECODE_ROWS     32  /* heads * query_len limit of the fused decode kernel */
@@ -698,7 +698,8 @@ typedef struct mm3idx_append {
  * written: no two of the 2 * num_pages * kv_heads may be the same float
  * (MM3IDX_ERR_ATTENTION_LAYOUT; so is one cache given for both sides, with
  * scales).  Where the strides of the two sides differ, they must lie in ranges of
- * memory that do not overlap.
+ * memory that do not overlap.  num_reqs * kv_heads * (the pages that query_len
+ * tokens can touch) must stay below 2^30 (MM3IDX_ERR_INVALID_ARGUMENT).
  */
 int mm3idx_append_kv(const mm3idx_append_t *a, void *stream);
 

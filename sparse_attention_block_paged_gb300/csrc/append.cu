@@ -17,11 +17,20 @@
 // the length is known, before the page table; what is rare (an infinity, an old
 // scale that is no power of two) reads them again instead of holding registers.
 //
-// What it measured (GB300): four prompts of 8192 tokens, 8 heads of 128, into e4m3
-// pages of 64: 32 us (92 % of the measured copy rate; with the page first, 107
-// registers and two CTAs an SM 104 us); pieces of 32 prompts, 134 MB, in 16 bits: 22 us
-// (90 %); a decode step's tokens (64 x 1, 2 heads): 2.0 us; 256 x 4 drafts, 8 heads
-// of 64: 3.5 us, both a chain of four dependent loads.
+// What it measured (GB300, calls captured in a CUDA graph): four prompts of 8192 tokens,
+// 8 heads of 128, into e4m3 pages of 64: 32 us (92 % of the measured copy rate; with the
+// page first, 107 registers and two CTAs an SM 104 us), 31 us without page scales; pieces
+// of 32 prompts, 134 MB, in 16 bits: 22 us (90 %); a decode step's tokens (64 x 1, 2
+// heads): 2.0 us (3.1 to 3.5 issued from Python, the host's time); 256 x 4 drafts, 8
+// heads of 64: 3.5 us, both a chain of four dependent loads.
+//
+// Where it is slow.  Groups are dealt out by the most rows that a request may have: one
+// prompt chunk beside many single tokens launches a chunk's groups for every request
+// (64 x 1 and 8192 tokens, pages of 128: 234 us where the bytes need 8).  Tensors' scales
+// other than 1 with page scales: 64 us (a power of two) or 111 for the prompts above.
+//
+// Plain loads of what kernels before this one wrote (lengths, table, older codes) lie
+// behind griddepcontrol.wait, which makes those writes seen.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -13,18 +13,23 @@
 // What is left is the copy of page data, at HBM's rate: a warp moves up to 4 KB
 // of a page at a time, eight 16-byte loads a lane in flight before the first store.
 //
-// What it measured (GB300): half of 16384 pages of 128 KB live, compacted: 171 us
-// (92 % of the measured copy rate); 8 requests forked into 64, four layers of
-// 128 KB a page: 15 us with the release before it (HBM needs 10); the smallest calls:
-// release 2.0 us, allocation 2.2, a fork 5.6, a compaction of 512 pages 7.6, all
-// latency of one or two dependent kernels.
+// What it measured (GB300, calls captured in a CUDA graph): half of 16384 pages of
+// 128 KB live, compacted: 171 us (92 % of the measured copy rate); 8 requests forked
+// into 64, four layers of 128 KB a page: 15 us with the release before it (HBM needs
+// 10); 1024 pages of 128 KB copied: 41.7 us (95 %); the smallest calls: release 1.8 us,
+// allocation 3.3 where nothing is wanted and about 4 where it gives pages (512 or 4096
+// pages; 5 of 16384), a fork 5.6, a compaction of 512 pages 7.6, all latency of one or
+// two dependent kernels.  Issued from Python one after another: release 2.5, allocation
+// as above, a compaction of 512 pages 8.9 to 10.
 #include "pages.h"
 
 namespace mm3idx {
 namespace {
 
-// Counts, tables and lengths are what the kernels before wrote, some of them on
-// other SMs in the lines of what is read here: L2 is where they are read.
+// Loads that name L2 (__ldcg): what another CTA of the same kernel wrote (lists, pairs)
+// has to be read there.  Counts, tables and lengths, which only kernels before
+// this one wrote, need not: griddepcontrol.wait makes those writes seen by any load
+// behind it.  They are read once, so L1 has nothing to give, and alike here.
 
 // ------------------------------------------------------------ ordered scans
 
